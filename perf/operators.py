@@ -240,7 +240,7 @@ def prepare(case, seed):
         B, mpp = s["table"].shape
         s["prob"] = sa.Problem(B=B, Hq=Hq, Hk=Hk, max_pages_per_seq=mpp, num_pages=s["k_pool"].shape[0], sink=4, window=64,
                                block_sizes=[P] * Hk, k_per_head=[1] * Hq, kcap=1)
-        s["ws"] = sa.Workspace(s["prob"], rows=s["q"].shape[0] if "q" in s else 0)
+        s["ws"] = sa.Workspace(s["prob"], rows=True)
         if s["op"] == "rotate":
             s["rope"] = sa.Rope(_ints(case["axis_pairs"]), sa.ROPE_HALVES if case["layout"] == "halves" else sa.ROPE_PAIRS)
     return s
