@@ -98,6 +98,8 @@ extern "C" {
 #define SA_MAX_GROUP 8   /* G <= 8 */
 #define SA_MAX_HK 64
 #define SA_MAX_HQ 256
+#define SA_MAX_AXES 4    /* position axes of a rotation */
+#define SA_MAX_TREE 64   /* drafted tokens of one sequence */
 
 /* Shapes and selection settings of one attention layer.  Host memory. */
 typedef struct sa_problem {
@@ -415,6 +417,153 @@ int sa_decode_step_bypass(const sa_problem* prob, const void* q,
                           int32_t* sel_idx, int32_t* sel_cnt, float* out,
                           float* lse, float* rho_or_null, int32_t* bypass,
                           void* ws, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Packed rows: prompts, drafts and single tokens around the decode step.  The
+ * pages of the sources name the paged cache (SPIN, abstract and Fig. 6) and
+ * stop at its door; these calls fill it, read it with many query rows, and
+ * keep its pages.  Conventions of theirs:
+ *   - The rows of all sequences lie behind each other: sequence b has the
+ *     n = row_offsets[b + 1] - row_offsets[b] rows from row_offsets[b] on
+ *     (device int32 [B + 1], non-decreasing, row_offsets[B] <= n_rows; n = 0
+ *     is allowed).  They are its newest n tokens: with L = seq_lens[b], which
+ *     counts them, row i sits at position L - n + i of the cache.  Rows
+ *     before row_offsets[0] and from row_offsets[B] on belong to nobody and
+ *     their outputs are left as they were.
+ *   - Device errors: offsets that decrease or pass n_rows are cut to the rows
+ *     there are and record SA_ERR_INVALID_ARG; L above max_pages_per_seq * P
+ *     records SA_ERR_CAPACITY and the positions behind the table are left
+ *     out; a page outside the pool records SA_ERR_BAD_PAGE and its tokens are
+ *     left out.
+ *   - Their workspace has sa_rows_workspace_size bytes (one of
+ *     max(sa_workspace_size, sa_rows_workspace_size) serves every call).  They
+ *     use the problem's shapes and scale; selection settings play no part. */
+
+/* Workspace bytes of the packed-row and page calls (0 if prob is invalid). */
+size_t sa_rows_workspace_size(const sa_problem* prob);
+
+/* which dims a rotation turns together */
+#define SA_ROPE_HALVES 0 /* dim j with dim j + R / 2, j < R / 2 */
+#define SA_ROPE_PAIRS 1  /* dim 2 j with dim 2 j + 1 */
+
+/* Rotary positions.  R / 2 = sum of axis_pairs dim pairs turn (R <= 128, a
+ * multiple of 16; the dims from R on stay); the first axis_pairs[0] of them
+ * by the position on axis 0, the next axis_pairs[1] by axis 1, and so on (one
+ * axis for text; time, height and width for pictures). */
+typedef struct sa_rope {
+  int32_t layout;                  /* SA_ROPE_HALVES or SA_ROPE_PAIRS */
+  int32_t axes;                    /* 1 .. SA_MAX_AXES */
+  int32_t axis_pairs[SA_MAX_AXES]; /* each >= 0; entries from `axes` on are ignored */
+} sa_rope;
+
+/* Norm, rotation and append of packed rows, in one pass.  For row i with
+ * query heads q[i][h][:], key heads k[i][kvh][:] and values v[i][kvh][:]:
+ *   x <- x / sqrt(mean(x^2) + eps) * w      (q_weight / k_weight bf16 [D];
+ *                                            NULL: that one has no norm)
+ *   pair j of axis a: angle = positions[a][i] * inv_freq[j],
+ *   (x1, x2) <- (x1 cos - x2 sin, x2 cos + x1 sin)
+ * in fp32, rounded to bf16 once; the angle is reduced to one turn from the
+ * exact product of position and inv_freq (fp32 [R / 2]), so far positions
+ * lose nothing.  q goes to q_out [n_rows][Hq][D], k and v to the row's
+ * position in the pools.  rope_or_null = NULL: no rotation.
+ * positions_or_null: int32 [axes][n_rows], any values; NULL: the row's
+ * position in the cache on every axis.
+ * q, k and v may be slices of one projection: row i starts q_stride (k_stride,
+ * v_stride) elements after row i - 1, a multiple of 8, at least the row's own
+ * size.  q_out may be q itself if q is dense; otherwise they must not
+ * overlap.  A row whose position is not in the table or pool gets its q_out
+ * and is not appended. */
+int sa_qk_norm_rope(const sa_problem* prob, int32_t n_rows, const void* q, int64_t q_stride, const void* k,
+                    int64_t k_stride, const void* v, int64_t v_stride, const void* q_weight_or_null,
+                    const void* k_weight_or_null, float eps, const sa_rope* rope_or_null, const float* inv_freq,
+                    const int32_t* positions_or_null, const int32_t* row_offsets, const int32_t* seq_lens,
+                    const int32_t* page_table, void* q_out, void* k_pool, void* v_pool, void* ws, void* stream);
+
+/* Causal attention of packed rows over the paged cache: row i of sequence b
+ * (query heads q [n_rows][Hq][D]) sees the positions 0 .. L - n + i, i.e. a
+ * whole prompt (n = L), the rest of one behind a prefix that is in the cache
+ * already, or one token (n = 1).
+ *   out[row][h][:] = sum_t softmax(z)_t v_t (bf16), z_t = scale q.k_t,
+ *   lse_or_null[row][h] = log sum_t e^{z_t} (fp32)
+ * Products of bf16 in fp32 sums; the softmax weights are rounded to bf16 for
+ * their product with V, the sum beneath them is of the unrounded ones.  A row
+ * that sees nothing gets out = 0, lse = -inf.  What a row does not see cannot
+ * change it, whatever is stored there (NaN and infinities included). */
+int sa_prompt_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
+                        const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
+                        const int32_t* row_offsets, void* out, float* lse_or_null, void* ws, void* stream);
+
+/* Attention of drafted tokens: the n <= SA_MAX_TREE rows of a sequence are the
+ * nodes of a tree behind its other L - n tokens (appended at positions L - n
+ * on, by sa_qk_norm_rope with each node's depth as its rotary position).
+ * Row i sees the positions 0 .. L - n - 1 and draft j where bit j of
+ * tree_mask[row] is set (uint64 [n_rows]: its ancestors' bits and its own;
+ * any bits are allowed, those from n on are ignored).  out and lse as above.
+ * n above SA_MAX_TREE records SA_ERR_CAPACITY and leaves the sequence's
+ * outputs as they were. */
+int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
+                      const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
+                      const int32_t* row_offsets, const uint64_t* tree_mask, void* out, float* lse_or_null,
+                      void* ws, void* stream);
+
+/* Takes over the accepted nodes of a tree: for every sequence b the K and V
+ * rows at positions base_lens[b] + path[b][i] move to base_lens[b] + i,
+ * i < path_cnt[b].  base_lens: tokens before the draft; path [B][max_path]
+ * (max_path <= SA_MAX_TREE, the nodes from the root on); path_cnt [B], 0
+ * leaves the sequence alone.  All rows are read before any is written.  The
+ * sequence then has base_lens[b] + path_cnt[b] tokens; the pages of its draft
+ * must not be shared with another (sa_plan_pages sees to that).  A node
+ * below 0 or position behind the table, or a count outside [0, max_path],
+ * records SA_ERR_INVALID_ARG, a bad page SA_ERR_BAD_PAGE; that sequence is
+ * then left as it was. */
+int sa_accept_rows(const sa_problem* prob, void* k_pool, void* v_pool, const int32_t* page_table,
+                   const int32_t* base_lens, const int32_t* path, int32_t max_path, const int32_t* path_cnt, void* ws,
+                   void* stream);
+
+/* The next page table: fork, free, truncate and grow in one call.  Pages have
+ * no other owner than the rows of the table: a page is free when no row holds
+ * it, and a prefix kept for later is a row of its own.  New row b goes on from
+ * old row parent[b] (several may name the same one: they are forked; an old
+ * row that nobody names is freed; -1 starts empty): its first keep[b] tokens
+ * are the parent's, and it gets pages for lens[b] tokens (less than keep[b]:
+ * for keep[b]).
+ *   - Whole pages are shared.  A row that will write behind keep[b] inside a
+ *     page (keep[b] % P != 0 and lens[b] > keep[b]) while another row holds
+ *     that page too gets a copy of its own; where every holder is such a row
+ *     the lowest keeps the page.
+ *   - Pages are taken in ascending order of their index by the rows in
+ *     ascending order, a row's copy before its other new pages.
+ * table_out [B][max_pages_per_seq] (must not overlap table_in) is the new
+ * table, -1 where a row has no page.  The copies to make, in row order, go to
+ * copy_src / copy_dst [B], -1 behind them; counts[0] is their number and
+ * counts[1] the free pages left.  sa_copy_pages makes them, once for every
+ * layer's pools.  Too few free pages record SA_ERR_CAPACITY: counts[1] is
+ * then what is missing, negative, and the entries without a page are -1.
+ * Device errors: parent outside [-1, B), keep or lens behind the table
+ * (SA_ERR_INVALID_ARG: the row is empty); a page outside the pool among
+ * the tokens kept (SA_ERR_BAD_PAGE: that entry is -1).  B above 1024 gives
+ * SA_ERR_UNSUPPORTED. */
+int sa_plan_pages(const sa_problem* prob, const int32_t* table_in, const int32_t* parent, const int32_t* keep,
+                  const int32_t* lens, int32_t* table_out, int32_t* copy_src, int32_t* copy_dst, int32_t* counts,
+                  void* ws, void* stream);
+
+/* Packs the live pages to the front of the pool: with n live pages (held by
+ * the first ceil(seq_lens[b] / P) entries of some row), the i-th live page at
+ * or behind index n, ascending, moves to the i-th free page below n.
+ * table_out [B][max_pages_per_seq] (must not overlap table_in) is the new
+ * table, -1 behind a row's pages; the moves go to move_src / move_dst
+ * [num_pages], -1 behind them; counts[0] is their number, counts[1] is n.
+ * sa_copy_pages makes the moves (no page is both source and target), once for
+ * every layer's pools.  Errors as sa_plan_pages. */
+int sa_compact_pages(const sa_problem* prob, const int32_t* table_in, const int32_t* seq_lens, int32_t* table_out,
+                     int32_t* move_src, int32_t* move_dst, int32_t* counts, void* ws, void* stream);
+
+/* Copies page src[i] to page dst[i] in both pools, i < min(count[0], max_pages)
+ * (count on the device; src and dst hold max_pages entries).  No page may be
+ * dst twice, or both src and dst.  A page outside the pool records
+ * SA_ERR_BAD_PAGE and its copy is left out. */
+int sa_copy_pages(const sa_problem* prob, void* k_pool, void* v_pool, const int32_t* src, const int32_t* dst,
+                  const int32_t* count, int32_t max_pages, void* ws, void* stream);
 
 /* Step a6 standalone -- merge two partial attentions over disjoint sets:
  * m = max(lse_a, lse_b), w_x = e^{lse_x - m},

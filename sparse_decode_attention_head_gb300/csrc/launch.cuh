@@ -1,9 +1,11 @@
 // Host entry points of the kernels (one definition each, in the .cu file
 // named beside it), shared by the C ABI (sa_api.cu) and the allocation-free
-// decode (noalloc.cu), and the host helpers of the C ABI that noalloc.cu uses.
+// decode (noalloc.cu), and the host helpers of the C ABI that noalloc.cu and
+// rows_api.cu use.
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "sa_common.cuh"
 #include "sparsity.cuh"
@@ -52,4 +54,5 @@ namespace sa_host {
 int make_params(const sa_problem* pr, sa::Params* p);
 int make_kv_map(CUtensorMap* m, const void* pool, const sa::Params& p);
 int num_sms_current();
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 }  // namespace sa_host

@@ -1,0 +1,351 @@
+// The pages of the cache: the next table of a batch (fork, free, truncate,
+// grow), packing the pool, copying pages, taking over a tree's accepted rows.
+//
+// Who holds a page is counted afresh from the table each time (integer
+// counts, so the order of the atomics leaves no trace); there is no state of
+// its own that could disagree with it.  Ranks of free, live and moved pages
+// come from a count of each chunk of 1024 pages and a sum over the chunks
+// before; four small launches, each waiting for the one before through
+// dependent launch, so a call is bound by their latency.  The copies are
+// bound by HBM: a page is read and written once, a warp moving a 4 KB slab
+// (one head of one page) with eight 16-byte loads a lane in flight.
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kP - 1) / kP; }
+
+// A row of the next table: the old row it goes on from, the tokens it keeps
+// and has room for.  Impossible ones are empty (and recorded by the count).
+struct PlanRow {
+  int parent, keep, room;
+  bool writes;     // will write inside the last page that it keeps
+};
+
+template <bool PLAN>
+__device__ __forceinline__ PlanRow plan_row(const PageArgs& A, int b, int* status) {
+  PlanRow r;
+  const int cap = A.mpp * kP;
+  r.keep = A.keep[b];
+  if (PLAN) {
+    r.parent = A.parent[b];
+    r.room = A.lens[b];
+    const bool ok = r.parent >= -1 && r.parent < A.B && r.keep >= 0 && r.keep <= cap && r.room <= cap;
+    if (!ok) {
+      if (status != nullptr) set_status(status, SA_ERR_INVALID_ARG);
+      r.parent = -1;
+      r.room = 0;
+    }
+    if (r.parent < 0) r.keep = 0;
+    r.room = max(r.room, r.keep);
+    r.writes = r.keep % kP != 0 && r.room > r.keep;
+  } else {
+    if (r.keep < 0 || r.keep > cap) {
+      if (status != nullptr) set_status(status, SA_ERR_INVALID_ARG);
+      r.keep = 0;
+    }
+    r.parent = b;
+    r.room = r.keep;
+    r.writes = false;
+  }
+  return r;
+}
+
+// Holders of every page; for a plan also the rows that will write inside it
+// and the lowest of them.
+template <bool PLAN>
+__global__ void __launch_bounds__(kThreads) count_kernel(PageArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y;
+  const PlanRow r = plan_row<PLAN>(A, b, blockIdx.x == 0 && threadIdx.x == 0 ? A.status : nullptr);
+  const int held = pages_of(r.keep);
+  const int j = blockIdx.x * kThreads + threadIdx.x;
+  if (j >= held) return;
+  const int page = A.table_in[(size_t)r.parent * A.mpp + j];
+  if (page < 0 || page >= A.num_pages) {
+    set_status(A.status, SA_ERR_BAD_PAGE);
+    return;
+  }
+  atomicAdd(A.refs + page, 1);
+  if (PLAN && r.writes && j == held - 1) {
+    atomicAdd(A.writers + page, 1);
+    atomicMax(A.lowest + page, kMaxPlanRows - b);
+  }
+}
+
+// Inclusive sum over a block of 1024 threads.
+__device__ __forceinline__ int block_scan(int x, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = warp_incl_scan(x);
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) s_warp[lane] = warp_incl_scan(s_warp[lane]);
+  __syncthreads();
+  return x + (warp > 0 ? s_warp[warp - 1] : 0);
+}
+
+// Free (plan) or live (compact) pages of each chunk; the last block of a plan
+// lines up what the rows need.
+template <bool PLAN>
+__global__ void __launch_bounds__(kPageChunk) chunk_kernel(PageArgs A, int chunks) {
+  __shared__ int s_warp[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x < chunks) {
+    const int page = blockIdx.x * kPageChunk + tid;
+    const int n = __syncthreads_count(page < A.num_pages && (A.refs[page] == 0) == PLAN);
+    if (tid == 0) A.chunk[blockIdx.x] = n;
+    return;
+  }
+  int need = 0, copy = 0;
+  if (tid < A.B) {
+    const PlanRow r = plan_row<true>(A, tid, nullptr);
+    const int held = pages_of(r.keep);
+    if (r.writes) {
+      const int page = A.table_in[(size_t)r.parent * A.mpp + held - 1];
+      if (page >= 0 && page < A.num_pages)
+        copy = !(A.writers[page] == A.refs[page] && A.lowest[page] == kMaxPlanRows - tid);
+    }
+    need = copy + pages_of(r.room) - held;
+  }
+  const int upto = block_scan(need, s_warp);
+  const int copies = block_scan(copy, s_warp);
+  if (tid < A.B) {
+    A.need[2 * tid] = upto - need;
+    A.need[2 * tid + 1] = 2 * (copies - copy) + copy;
+  }
+  if (tid == kPageChunk - 1) {
+    A.need[2 * A.B] = upto;
+    A.need[2 * A.B + 1] = 2 * copies;
+  }
+}
+
+// Ranks: the first free pages that the plan takes; or source and target of
+// every move.
+template <bool PLAN>
+__global__ void __launch_bounds__(kPageChunk) rank_kernel(PageArgs A, int chunks) {
+  __shared__ int s_warp[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, c = blockIdx.x;
+  int before = 0, all = 0;
+  for (int i = tid; i < chunks; i += kPageChunk) {
+    const int n = A.chunk[i];
+    all += n;
+    if (i < c) before += n;
+  }
+  // both sums at once: the counts of 1024 pages a chunk stay below 2^31
+  __shared__ int s_sum[2];
+  before = block_scan(before, s_warp);
+  if (tid == kPageChunk - 1) s_sum[0] = before;
+  all = block_scan(all, s_warp);
+  if (tid == kPageChunk - 1) s_sum[1] = all;
+  const int page = c * kPageChunk + tid;
+  const bool in = page < A.num_pages;
+  const bool hit = in && (A.refs[page] == 0) == PLAN;
+  const int upto = block_scan(hit, s_warp);
+  before = s_sum[0] + upto - hit;      // hits below this page
+  all = s_sum[1];
+  if (PLAN) {
+    const int take = A.need[2 * A.B];
+    if (hit && before < take) A.list[before] = page;
+    if (c == 0 && tid == 0) {
+      A.counts[0] = A.need[2 * A.B + 1] >> 1;
+      A.counts[1] = all - take;
+      if (all < take) set_status(A.status, SA_ERR_CAPACITY);
+      A.chunk[chunks] = all;
+    }
+    return;
+  }
+  // live pages below index `all`, the number of live pages
+  int low = 0;
+  for (int i = tid; i < min(chunks, all / kPageChunk); i += kPageChunk) low += A.chunk[i];
+  const int edge = all / kPageChunk * kPageChunk + tid;
+  low += edge < all && edge < A.num_pages && A.refs[edge] != 0;
+  low = block_scan(low, s_warp);
+  if (tid == kPageChunk - 1) s_sum[0] = low;
+  __syncthreads();
+  low = s_sum[0];
+  const int moves = all - low;
+  if (in) {
+    if (hit && page >= all) {
+      A.src[before - low] = page;
+      A.list[page] = before - low;
+    }
+    if (!hit && page < all) A.dst[page - before] = page;
+    if (page >= moves) A.src[page] = A.dst[page] = -1;
+  }
+  if (c == 0 && tid == 0) {
+    A.counts[0] = moves;
+    A.counts[1] = all;
+  }
+}
+
+// The next table, and a plan's list of copies.
+template <bool PLAN>
+__global__ void __launch_bounds__(kThreads) table_kernel(PageArgs A, int chunks) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y;
+  const int j = blockIdx.x * kThreads + threadIdx.x;
+  if (j >= A.mpp) return;
+  const PlanRow r = plan_row<PLAN>(A, b, nullptr);
+  const int held = pages_of(r.keep);
+  int page = -1;
+  if (j < held) {
+    page = A.table_in[(size_t)r.parent * A.mpp + j];
+    if (page < 0 || page >= A.num_pages) page = -1;
+  }
+  if (PLAN) {
+    const int start = A.need[2 * b], copy = A.need[2 * b + 1] & 1, free_pages = A.chunk[chunks];
+    const bool copied = copy && j == held - 1;
+    if (copied || (j >= held && j < pages_of(r.room))) {
+      const int at = start + (copied ? 0 : copy + j - held);
+      const int fresh = at < free_pages ? A.list[at] : -1;
+      if (copied) {
+        const int rank = A.need[2 * b + 1] >> 1;
+        A.src[rank] = page;
+        A.dst[rank] = fresh;
+      }
+      page = fresh;
+    }
+    if (j == 0) {     // rows behind the number of copies clear its entries
+      const int copies = A.need[2 * A.B + 1] >> 1;
+      if (b >= copies) A.src[b] = A.dst[b] = -1;
+    }
+  } else if (page >= A.counts[1]) {
+    page = A.dst[A.list[page]];
+  }
+  A.table_out[(size_t)b * A.mpp + j] = page;
+}
+
+template <bool PLAN>
+int launch_table(const PageArgs& A, cudaStream_t stream) {
+  const int chunks = (A.num_pages + kPageChunk - 1) / kPageChunk;
+  const size_t zero = (size_t)A.num_pages * (PLAN ? 3 : 1) * sizeof(int);   // refs, writers, lowest lie together
+  if (cudaMemsetAsync(A.refs, 0, zero, stream) != cudaSuccess) return SA_ERR_CUDA;
+  const dim3 entries((A.mpp + kThreads - 1) / kThreads, A.B);
+  cudaError_t e = launch_pdl(count_kernel<PLAN>, entries, dim3(kThreads), 0, stream, A);
+  if (e == cudaSuccess)
+    e = launch_pdl(chunk_kernel<PLAN>, dim3(chunks + (PLAN ? 1 : 0)), dim3(kPageChunk), 0, stream, A, chunks);
+  if (e == cudaSuccess) e = launch_pdl(rank_kernel<PLAN>, dim3(chunks), dim3(kPageChunk), 0, stream, A, chunks);
+  if (e == cudaSuccess) e = launch_pdl(table_kernel<PLAN>, entries, dim3(kThreads), 0, stream, A, chunks);
+  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- copies
+
+__global__ void __launch_bounds__(kThreads)
+copy_pages_kernel(uint4* __restrict__ k_pool, uint4* __restrict__ v_pool, const int* __restrict__ src,
+                  const int* __restrict__ dst, const int* __restrict__ count, int max_pages, int num_pages, int Hk,
+                  int* status) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kSlab = kP * kD * 2 / 16;    // 16-byte chunks of one head of one page
+  const int lane = threadIdx.x & 31;
+  const int n = min(max(__ldg(count), 0), max_pages);
+  const long long units = (long long)n * 2 * Hk;
+  for (long long u = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
+       u += (long long)gridDim.x * (kThreads / 32)) {
+    const int i = (int)(u / (2 * Hk)), rest = (int)(u - (long long)i * 2 * Hk);
+    const int s = __ldg(src + i), d = __ldg(dst + i);
+    if (s < 0 || s >= num_pages || d < 0 || d >= num_pages) {
+      if (lane == 0) set_status(status, SA_ERR_BAD_PAGE);
+      continue;
+    }
+    uint4* pool = rest < Hk ? k_pool : v_pool;
+    const int h = rest < Hk ? rest : rest - Hk;
+    const uint4* from = pool + ((size_t)s * Hk + h) * kSlab + lane;
+    uint4* to = pool + ((size_t)d * Hk + h) * kSlab + lane;
+    uint4 x[kSlab / 32];
+#pragma unroll
+    for (int k = 0; k < kSlab / 32; ++k) x[k] = from[32 * k];
+#pragma unroll
+    for (int k = 0; k < kSlab / 32; ++k) to[32 * k] = x[k];
+  }
+}
+
+// One block a (KV head, sequence): all rows of the path are in registers
+// before the first is written.
+__global__ void __launch_bounds__(kThreads)
+accept_rows_kernel(uint4* k_pool, uint4* v_pool, const int* __restrict__ page_table, const int* __restrict__ base_lens,
+                   const int* __restrict__ path, int max_path, const int* __restrict__ path_cnt, int Hk, int mpp,
+                   int num_pages, int* status) {
+  constexpr int kChunks = kD * 2 / 16;                              // of a row
+  constexpr int kEach = kMaxTree * kChunks * 2 / kThreads;          // of a thread, K and V
+  pdl_wait();
+  pdl_trigger();
+  const int kvh = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int base = base_lens[b], cnt = path_cnt[b];
+  const int* pt = page_table + (size_t)b * mpp;
+  int error = SA_OK;
+  if (cnt < 0 || cnt > max_path || base < 0 || base > mpp * kP - cnt) error = SA_ERR_INVALID_ARG;
+  if (cnt == 0 || error != SA_OK) {
+    if (error != SA_OK && tid == 0) set_status(status, error);
+    return;
+  }
+  // row offsets in the pools, in 16-byte chunks
+  __shared__ long long s_from[kMaxTree], s_to[kMaxTree];
+  if (tid < cnt) {
+    const int node = path[(size_t)b * max_path + tid];
+    const int to = base + tid;
+    if (node < 0 || node >= mpp * kP - base) {
+      error = SA_ERR_INVALID_ARG;
+    } else {
+      const int from = base + node;
+      const int pf = __ldg(pt + from / kP), pd = __ldg(pt + to / kP);
+      if (pf < 0 || pf >= num_pages || pd < 0 || pd >= num_pages) error = SA_ERR_BAD_PAGE;
+      s_from[tid] = (((long long)pf * Hk + kvh) * kP + from % kP) * kChunks;
+      s_to[tid] = (((long long)pd * Hk + kvh) * kP + to % kP) * kChunks;
+    }
+    if (error != SA_OK) set_status(status, error);
+  }
+  if (__syncthreads_or(error != SA_OK)) return;
+  uint4 x[kEach];
+  const int rows = 2 * cnt;       // K rows, then V rows
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * (kThreads / kChunks) + tid / kChunks;
+    if (i < rows) x[e] = (i < cnt ? k_pool : v_pool)[s_from[i < cnt ? i : i - cnt] + tid % kChunks];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * (kThreads / kChunks) + tid / kChunks;
+    if (i < rows) (i < cnt ? k_pool : v_pool)[s_to[i < cnt ? i : i - cnt] + tid % kChunks] = x[e];
+  }
+}
+
+}  // namespace
+
+int launch_plan_pages(const PageArgs& A, cudaStream_t stream) { return launch_table<true>(A, stream); }
+int launch_compact_pages(const PageArgs& A, cudaStream_t stream) { return launch_table<false>(A, stream); }
+
+int launch_copy_pages(void* k_pool, void* v_pool, const int* src, const int* dst, const int* count, int max_pages,
+                      int num_pages, int Hk, int* status, int num_sms, cudaStream_t stream) {
+  const long long units = (long long)max_pages * 2 * Hk;
+  const int grid = (int)std::min<long long>((units + kThreads / 32 - 1) / (kThreads / 32), (long long)num_sms * 6);
+  const cudaError_t e =
+      launch_pdl(copy_pages_kernel, dim3(grid), dim3(kThreads), 0, stream, static_cast<uint4*>(k_pool),
+                 static_cast<uint4*>(v_pool), src, dst, count, max_pages, num_pages, Hk, status);
+  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+int launch_accept_rows(void* k_pool, void* v_pool, const int* page_table, const int* base_lens, const int* path,
+                       int max_path, const int* path_cnt, int B, int Hk, int mpp, int num_pages, int* status,
+                       cudaStream_t stream) {
+  const cudaError_t e = launch_pdl(accept_rows_kernel, dim3(Hk, B), dim3(kThreads), 0, stream,
+                                   static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), page_table, base_lens, path,
+                                   max_path, path_cnt, Hk, mpp, num_pages, status);
+  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // namespace sa

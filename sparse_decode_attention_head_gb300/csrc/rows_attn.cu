@@ -1,0 +1,744 @@
+// Attention of packed rows over the paged cache: prompts (causal) and trees of
+// drafted tokens (ancestor words).
+//
+// For query row i of a sequence and a head, with z_t = scale q.k_t over the
+// positions t that the row sees,
+//   out = sum_t e^{z_t - m} v_t / sum_t e^{z_t - m},   lse = m + log sum_t e^{z_t - m}
+// in one pass over t with a running maximum m, tile after tile of 128 tokens.
+//
+// Work: an item is one KV head of one sequence with up to 256 rows, a row
+// being one of the G query heads of a token (so the G heads share every K and
+// V byte): two query tiles of 128 rows, or one.  The items of all sequences
+// are laid end to end, weighted by the KV tokens they see, and cut into one
+// equal run for each block (one block an SM, persistent): many rows give
+// whole items, few rows over a long cache split an item's KV range over
+// blocks.  A cut item leaves (maximum, sum, unnormalised output) for each
+// row, and the merge kernel joins the pieces in order with the log-sum-exp
+// identity; blocks never wait on one another and nothing is added atomically,
+// so results do not depend on timing.
+//
+// Block: 12 warps.
+//   warps 0-3, 4-7  softmax of query tile 0 and 1, a thread a row
+//   warp 8          issues the matrix instructions (one thread)
+//   warp 9          loads: Q tiles once an item, K and V tiles into a ring of
+//                   five 32 KB slots, one TMA box of 4 KB a page
+//   warps 10, 11    clean the V tiles at the edge of what rows see
+// S = Q K^T and O += P V run on tcgen05, accumulators in TMEM (S0 S1 O0 O1,
+// 128 columns each); P overwrites the first half of its S as packed bf16 and
+// is the product's left operand there.  While one tile's softmax runs, the
+// tensor core works on the other's.  An item with one query tile instead
+// gives every other KV tile to the second softmax group, with a maximum, sum
+// and output of its own, joined at the item's end.
+//
+// The running maximum is let lag: O and the sum are rescaled only when a row
+// maximum has grown by more than 2^8, which the fp32 sums and the bf16 of P
+// (whose relative precision does not depend on its size) hold with ease.
+//
+// Masked places: a weight of zero times a non-finite V would be NaN, so in the
+// tiles that hold positions some row of the item does not see, V rows behind
+// the item's last position become zero and non-finite values become zero in
+// shared memory; rows that do see such a value add it at the end.
+#include <algorithm>
+
+#include "rows.cuh"
+#include "tcgen.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kRows = 128;               // rows of a query tile, tokens of a KV tile
+constexpr int kTileBytes = kRows * kD * 2;
+constexpr int kSlots = 5;                // K and V tiles in flight: what 227 KB leave beside two query tiles
+constexpr int kThreads = 384;
+constexpr int kItemCost = 256;           // an item's fixed cost in KV tokens (query load, epilogue)
+constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
+
+enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
+
+struct Ctl {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t edge_go[kSlots], clean[kSlots];   // a V tile at the edge: its load is under way, it is clean
+  uint64_t ml_full, ml_free;
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int4 range[2];             // (sequence, KV head, item, KV tile) at which this block begins and ends
+  uint32_t bad[16];          // pages outside the pool, a bit each, of the last tiles loaded
+  int poison[4];             // 1 + the piece that met a non-finite V at its edge
+  float2 ml[kRows];          // (maximum, sum) of the second softmax group
+};
+constexpr size_t kSmemBytes = 1024 + 2 * kTileBytes + kSlots * kTileBytes + sizeof(Ctl);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && *(volatile int*)&c->abort) return false;
+  }
+  set_status(status, SA_ERR_TIMEOUT);
+  *(volatile int*)&c->abort = 1;
+  return false;
+}
+
+// The same by a whole warp: all lanes see the same answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, c, status));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ---------------------------------------------------------------- the items
+
+struct Seq : RowSeq {
+  int items;      // of one KV head
+  int T;          // tokens of an item
+};
+
+__device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int b, int* status) {
+  Seq s;
+  static_cast<RowSeq&>(s) = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, status);
+  s.T = 2 * A.tpt;
+  s.items = (s.n + s.T - 1) / s.T;
+  if (A.tree != nullptr && s.n > kMaxTree) {
+    if (status != nullptr) set_status(status, SA_ERR_CAPACITY);
+    s.items = 0;
+  }
+  return s;
+}
+
+// The first position that no row of item i sees.
+__device__ __forceinline__ int item_end(const RowsAttnArgs& A, const Seq& s, int i) {
+  if (A.tree != nullptr) return s.L;
+  return max(0, min(s.L, s.a + min(s.n, (i + 1) * s.T)));
+}
+// The first position that some row of item i does not see (positions of a tree's drafts included).
+__device__ __forceinline__ int item_edge(const RowsAttnArgs& A, const Seq& s, int i) {
+  return max(0, A.tree != nullptr ? s.a : s.a + i * s.T + 1);
+}
+__device__ __forceinline__ int tiles_of(int end) { return (end + kRows - 1) / kRows; }
+
+// Weight of a KV head's first k items: KV tokens seen (in closed form) and a fixed cost each.
+__device__ __forceinline__ long long weight_before(const RowsAttnArgs& A, const Seq& s, int k) {
+  if (A.tree != nullptr) return (long long)k * (s.L + kItemCost);
+  const long long cut = k == s.items ? (long long)s.items * s.T - s.n : 0;
+  return (long long)k * (max(s.a, 0) + kItemCost) + (long long)s.T * k * (k + 1) / 2 - cut;
+}
+
+// One warp: the total weight, and per lane the sequences' (chunk by chunk of 32).
+__device__ long long total_weight(const RowsAttnArgs& A, int* status) {
+  const int lane = threadIdx.x & 31;
+  long long w = 0;
+  for (int b = lane; b < A.B; b += 32) {
+    const Seq s = load_seq(A, b, status);
+    w += weight_before(A, s, s.items) * A.Hk;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return w;
+}
+
+// One warp: the item and KV tile at weight w (the end: sequence B).
+__device__ int4 locate(const RowsAttnArgs& A, long long w) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int b0 = 0; b0 < A.B; b0 += 32) {
+    const int b = b0 + lane;
+    Seq s{};
+    long long mine = 0;
+    if (b < A.B) {
+      s = load_seq(A, b, nullptr);
+      mine = weight_before(A, s, s.items) * A.Hk;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, w < before + upto);
+    if (hit == 0) {
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      continue;
+    }
+    const int src = __ffs(hit) - 1;
+    int4 r = make_int4(b, 0, 0, 0);
+    if (lane == src) {
+      long long rem = w - (before + upto - mine);
+      const long long each = mine / A.Hk;
+      r.y = (int)(rem / each);
+      rem -= each * r.y;
+      int lo = 0, hi = s.items;     // the item: weight_before(lo) <= rem < weight_before(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (weight_before(A, s, mid) <= rem) lo = mid; else hi = mid;
+      }
+      const long long w0 = weight_before(A, s, lo), w1 = weight_before(A, s, lo + 1);
+      r.z = lo;
+      r.w = (int)((rem - w0) * tiles_of(item_end(A, s, lo)) / (w1 - w0));
+    }
+    r.x = __shfl_sync(0xffffffffu, r.x, src);
+    r.y = __shfl_sync(0xffffffffu, r.y, src);
+    r.z = __shfl_sync(0xffffffffu, r.z, src);
+    r.w = __shfl_sync(0xffffffffu, r.w, src);
+    return r;
+  }
+  return make_int4(A.B, 0, 0, 0);
+}
+
+// The pieces of a block's run, in order; every role of the block walks them.
+struct Piece {
+  int b, kvh, i;
+  int k0, k1, nt;     // KV tiles [k0, k1) of the item's nt
+  int row0;           // first packed row of the item
+  int tokens;         // of the item
+  int end, edge;      // item_end, item_edge
+  int a;              // tokens of the sequence ahead of its rows
+  int first;          // the item's first row in the sequence
+  bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
+};
+
+struct Walk {
+  const RowsAttnArgs& A;
+  int b, kvh, i, kt;
+  int4 end;
+  bool done;
+  Seq s;
+  __device__ Walk(const RowsAttnArgs& a, const Ctl* c) : A(a) {
+    const int4 r = c->range[0];
+    b = r.x; kvh = r.y; i = r.z; kt = r.w;
+    end = c->range[1];
+    done = b >= A.B;
+    if (!done) s = load_seq(A, b, nullptr);
+  }
+  __device__ bool next(Piece& p) {
+    while (!done) {
+      const bool at_end = b == end.x && kvh == end.y && i == end.z;
+      p.b = b; p.kvh = kvh; p.i = i;
+      p.end = item_end(A, s, i);
+      p.edge = item_edge(A, s, i);
+      p.nt = tiles_of(p.end);
+      p.k0 = kt;
+      p.k1 = at_end ? end.w : p.nt;
+      p.a = s.a;
+      p.first = i * s.T;
+      p.row0 = s.row0 + i * s.T;
+      p.tokens = min(s.T, s.n - i * s.T);
+      p.dual = p.tokens <= A.tpt;
+      const bool some = p.k0 < p.k1 || (p.nt == 0 && !at_end);
+      kt = 0;
+      if (at_end) {
+        done = true;
+      } else if (++i == s.items) {
+        i = 0;
+        if (++kvh == A.Hk) {
+          kvh = 0;
+          do {
+            if (++b >= A.B) { done = true; break; }
+            s = load_seq(A, b, nullptr);
+          } while (s.items == 0);
+        }
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Adds the non-finite values of V at the item's edge positions that this row
+// sees to its dims [32 c, 32 c + 32): the product with them was taken as zero.
+__device__ __noinline__ void add_poison(const RowsAttnArgs& A, const Piece& p, int lim, unsigned long long word, int c,
+                                        float* o) {
+  for (int t = max(p.edge, p.k0 * kRows); t < min(p.end, p.k1 * kRows); ++t) {
+    const int bit = t - p.a;
+    if (!(t < lim || (bit >= 0 && bit < 64 && ((word >> bit) & 1ull)))) continue;
+    const int phys = __ldg(A.page_table + (size_t)p.b * A.mpp + t / kP);
+    if (phys < 0 || phys >= A.num_pages) continue;
+    const uint32_t* v =
+        reinterpret_cast<const uint32_t*>(A.v_pool + (((size_t)phys * A.Hk + p.kvh) * kP + t % kP) * kD + 32 * c);
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t w = __ldg(v + j);
+      if ((w & 0x7f80u) == 0x7f80u) o[2 * j] += bf16_lo(w);
+      if ((w & 0x7f800000u) == 0x7f800000u) o[2 * j + 1] += bf16_hi(w);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+__global__ void __launch_bounds__(kThreads, 1)
+rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem;                                  // two tiles: [half of the dims][128 rows][64]
+  uint8_t* s_kv = smem + 2 * kTileBytes;                // kSlots tiles: [16 groups of 8 tokens][half][8][64]
+  Ctl* c = reinterpret_cast<Ctl*>(s_kv + kSlots * kTileBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&c->full[i], 1);
+      mbar_init(&c->empty[i], 1);
+      mbar_init(&c->edge_go[i], 1);
+      mbar_init(&c->clean[i], 2);
+    }
+    mbar_init(&c->q_full, 1);
+    mbar_init(&c->q_empty, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&c->s_full[h], 1);
+      mbar_init(&c->p_full[h], kRows);
+      mbar_init(&c->o_done[h], 1);
+    }
+    mbar_init(&c->ml_full, kRows);
+    mbar_init(&c->ml_free, kRows);
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    for (int i = 0; i < 4; ++i) c->poison[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&c->tmem, 512);
+  pdl_wait();
+  pdl_trigger();
+  if (warp < 2) {   // where this block's run begins (warp 0) and ends (warp 1)
+    const long long W = total_weight(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr);
+    const int4 r = locate(A, W * (blockIdx.x + warp) / gridDim.x);
+    if (lane == 0) c->range[warp] = r;
+  }
+  if (tid < 2) A.desc[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  Walk walk(A, c);
+  Piece p;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax: a thread a row
+    const int h = warp >> 2;
+    const int r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, in the address' upper half
+    const uint32_t tS = tmem + lanes + h * 128, tO = tmem + lanes + 256 + h * 128;
+    const int t_row = r / A.G, g = r - t_row * A.G;
+    uint32_t steps_done = 0, items_done = 0, duals = 0, tiles = 0;
+    int piece = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int ntp = p.k1 - p.k0;
+      const int N = p.dual ? ntp : 2 * ntp;
+      const int tok = t_row + (p.dual || h == 0 ? 0 : A.tpt);
+      const bool valid = t_row < A.tpt && tok < p.tokens;
+      // what the row sees: positions below lim, and bit j of its word for position p.a + j
+      int lim = 0;
+      unsigned long long word = 0;
+      if (valid) {
+        if (A.tree != nullptr) {
+          lim = p.a;
+          word = __ldg(A.tree + p.row0 + tok);
+        } else {
+          lim = p.a + p.first + tok + 1;
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int s = h; s < N; s += 2) {
+        const int t = p.dual ? s : s >> 1;
+        const int kt = p.k0 + t;
+        if (!(ok = wait_warp(&c->s_full[h], steps_done & 1, c, A.status))) break;
+        ++steps_done;
+        tc_fence_after();
+        float v[128];
+        tmem_ld128(tS, v);
+        const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
+        if ((kt + 1) * kRows > p.edge || bad != 0) {
+          // bit j of see[w]: column 32 w + j
+          const int base = kt * kRows;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int c0 = base + 32 * w;
+            const int nlim = lim - c0;
+            uint32_t see = nlim >= 32 ? 0xffffffffu : nlim <= 0 ? 0u : (1u << nlim) - 1u;
+            const int sh = c0 - p.a;     // column c0 is bit sh of the word
+            if (sh > -32 && sh < 64) see |= sh >= 0 ? (uint32_t)(word >> sh) : (uint32_t)(word << -sh);
+            const int nend = p.end - c0;
+            see &= nend >= 32 ? 0xffffffffu : nend <= 0 ? 0u : (1u << nend) - 1u;
+            if ((bad >> (2 * w)) & 1u) see &= 0xffff0000u;
+            if ((bad >> (2 * w + 1)) & 1u) see &= 0x0000ffffu;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[32 * w + j] = (see >> j) & 1u ? v[32 * w + j] : -INFINITY;
+          }
+        }
+        float mx = v[0];
+#pragma unroll
+        for (int j = 1; j < 128; ++j) mx = fmaxf(mx, v[j]);
+        mx *= A.scale_log2;
+        if (m == -INFINITY) m = mx;   // all zeros so far: nothing to rescale
+        const bool grow = mx > m + kLag;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = fmaxf(m, mx);
+          const float alpha = ex2(m - mn);
+          m = mn;
+          l *= alpha;
+          if (s >= 2) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              float o[32];
+              uint32_t ow[32];
+              tmem_ld32(tO + 32 * q4, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ow[j] = __float_as_uint(o[j] * alpha);
+              tmem_st32(tO + 32 * q4, ow);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        float sum0 = 0.f, sum1 = 0.f;
+        uint32_t pw[2][32];
+#pragma unroll
+        for (int j = 0; j < 128; j += 2) {
+          const float p0 = ex2(fmaf(v[j], A.scale_log2, -mu));
+          const float p1 = ex2(fmaf(v[j + 1], A.scale_log2, -mu));
+          sum0 += p0;
+          sum1 += p1;
+          pw[j >> 6][(j & 63) >> 1] = pack_bf16(p0, p1);
+        }
+        tmem_st32(tS, pw[0]);
+        tmem_st32(tS + 32, pw[1]);
+        l += sum0 + sum1;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&c->p_full[h]);
+      }
+      if (!ok) break;
+      const bool mine = N > h;     // this group had a tile
+      if (mine) {
+        if (!(ok = wait_warp(&c->o_done[h], items_done & 1, c, A.status))) break;
+        ++items_done;
+        tc_fence_after();
+      }
+      const bool poisoned = *(volatile int*)&c->poison[piece & 3] == piece + 1;
+      const bool whole = p.k0 == 0 && p.k1 == p.nt;
+      float m1 = -INFINITY, l1 = 0.f;
+      if (p.dual) {
+        if (h == 1) {
+          c->ml[r] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(&c->ml_full);
+        } else {
+          if (!(ok = wait_warp(&c->ml_full, duals & 1, c, A.status))) break;
+          tc_fence_after();
+          const float2 x = c->ml[r];
+          m1 = x.x;
+          l1 = x.y;
+        }
+      }
+      if (!(p.dual && h == 1)) {
+        // the two groups' states of a row joined; a group without a tile, or without a position seen, has l = 0
+        const bool two = p.dual && N > 1;
+        const float M = two ? fmaxf(m, m1) : m;
+        const float w0 = l == 0.f ? 0.f : two ? ex2(m - M) : 1.f, w1 = two && l1 != 0.f ? ex2(m1 - M) : 0.f;
+        const float lt = l * w0 + (two ? l1 * w1 : 0.f);
+        const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
+        const int which = p.k0 > 0 ? 0 : 1;
+        const size_t slot = ((size_t)blockIdx.x * 2 + which) * 2 + h;
+        const size_t row = (size_t)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
+#pragma unroll 1
+        for (int q4 = 0; q4 < 4; ++q4) {
+          float o[32];
+          if (mine) {
+            tmem_ld32(tO + 32 * q4, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = w0 == 0.f ? 0.f : o[j] * w0;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0.f;
+          }
+          if (two) {
+            float o1[32];
+            tmem_ld32(tO + 128 + 32 * q4, o1);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] += w1 == 0.f ? 0.f : o1[j] * w1;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] *= inv;
+          if (poisoned && valid) add_poison(A, p, lim, word, q4, o);
+          if (whole) {
+            if (valid) {
+              uint4* dst = reinterpret_cast<uint4*>(A.out + row * kD + 32 * q4);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                dst[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                    pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+            }
+          } else if (valid) {
+            float4* dst = reinterpret_cast<float4*>(A.part + (slot * kRows + r) * kD + 32 * q4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        if (whole) {
+          if (valid && A.lse != nullptr) A.lse[row] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.693147180559945309f;
+        } else {
+          if (valid) A.part_ml[slot * kRows + r] = make_float2(M, lt);
+          if (tid == 0)
+            A.desc[blockIdx.x * 2 + which] =
+                make_int4(p.b, p.kvh, p.i, kDescValid | (p.k0 == 0 ? kDescFirst : 0) | (p.k1 == p.nt ? kDescLast : 0) |
+                                               (p.dual ? kDescDual : 0));
+        }
+      }
+      if (p.dual) {   // the second group's O may be written again
+        if (h == 0) {
+          tc_fence_before();
+          mbar_arrive(&c->ml_free);
+        } else if (!(ok = wait_warp(&c->ml_free, duals & 1, c, A.status))) {
+          break;
+        }
+        ++duals;
+      }
+      tiles += ntp;
+      ++piece;
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ matrix instructions
+    if (lane == 0) {
+      constexpr uint32_t idS = bf16_idesc(128, 128, false), idO = bf16_idesc(128, 128, true);
+      uint32_t tile = 0, pieces = 0, cleaned = 0, p_seen[2] = {0, 0};   // cleaned: a parity bit a slot
+      const uint32_t aQ = smem_u32(s_q), aKV = smem_u32(s_kv);
+      bool ok = true;
+      while (ok && walk.next(p)) {
+        const int ntp = p.k1 - p.k0;
+        if (ntp == 0) continue;
+        const int N = p.dual ? ntp : 2 * ntp;
+        if (!(ok = wait_bar(&c->q_full, pieces & 1, c, A.status))) break;
+        ++pieces;
+        auto issue_s = [&](int s) -> bool {
+          const int h = s & 1, t = p.dual ? s : s >> 1;
+          const uint32_t idx = 2 * (tile + t), slot = idx % kSlots;
+          if ((p.dual || h == 0) && !wait_bar(&c->full[slot], (idx / kSlots) & 1, c, A.status)) return false;
+          const uint64_t dq = smem_desc(aQ + (p.dual ? 0 : h * kTileBytes), 16, 1024);
+          const uint64_t dk = smem_desc(aKV + slot * kTileBytes, 16, 2048);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ss(tmem + h * 128, dq + (k >> 2) * (kTileBytes / 2 / 16) + (k & 3) * 2,
+                      dk + (k >> 2) * (1024 / 16) + (k & 3) * 2, idS, k != 0);
+          tc_commit(&c->s_full[h]);
+          if (p.dual || h == 1) tc_commit(&c->empty[slot]);
+          if (s == N - 1) tc_commit(&c->q_empty);
+          return true;
+        };
+        if (!(ok = issue_s(0))) break;
+        if (N > 1 && !(ok = issue_s(1))) break;
+        for (int s = 0; s < N; ++s) {
+          const int h = s & 1, t = p.dual ? s : s >> 1;
+          const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
+          if (p.dual || h == 0) {
+            if (!(ok = wait_bar(&c->full[slot], (idx / kSlots) & 1, c, A.status))) break;
+            if ((p.k0 + t + 1) * kRows > p.edge) {
+              if (!(ok = wait_bar(&c->clean[slot], (cleaned >> slot) & 1, c, A.status))) break;
+              cleaned ^= 1u << slot;
+            }
+          }
+          if (!(ok = wait_bar(&c->p_full[h], p_seen[h] & 1, c, A.status))) break;
+          ++p_seen[h];
+          tc_fence_after();
+          const uint64_t dv = smem_desc(aKV + slot * kTileBytes, 1024, 2048);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, dv + k * (4096 / 16), idO, s >= 2 || k != 0);
+          if (p.dual || h == 1) tc_commit(&c->empty[slot]);
+          if (s + 2 >= N) tc_commit(&c->o_done[h]);
+          if (s + 2 < N && !(ok = issue_s(s + 2))) break;
+        }
+        tile += ntp;
+      }
+      // nothing of this block is in flight when it frees its TMEM and ends
+      tc_commit(&c->drain);
+      mbar_wait_bounded(&c->drain, 0, A.status);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ loads
+    uint32_t tile = 0, pieces = 0, loads = 0;
+    const uint32_t q_bytes = (uint32_t)(A.tpt * A.G) * kD * 2;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int ntp = p.k1 - p.k0;
+      if (ntp == 0) continue;
+      if (pieces > 0 && !(ok = wait_warp(&c->q_empty, (pieces - 1) & 1, c, A.status))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&c->q_full, p.dual ? q_bytes : 2 * q_bytes);
+        for (int x = 0; x < (p.dual ? 2 : 4); ++x)
+          tma_load_3d(s_q + x * (kTileBytes / 2), &tmQ, (x & 1) * 64, p.kvh * A.G, p.row0 + (x >> 1) * A.tpt, &c->q_full);
+      }
+      ++pieces;
+      const int* pt = A.page_table + (size_t)p.b * A.mpp;
+      for (int t = 0; t < ntp; ++t) {
+        const int page = (p.k0 + t) * (kRows / kP) + lane;
+        const bool there = lane < kRows / kP && page * kP < p.end;
+        const int phys = there ? __ldg(pt + page) : -1;
+        const bool good = phys >= 0 && phys < A.num_pages;
+        const unsigned goods = __ballot_sync(0xffffffffu, good), bads = __ballot_sync(0xffffffffu, there && !good);
+        if (bads != 0 && lane == 0) set_status(A.status, SA_ERR_BAD_PAGE);
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t idx = 2 * (tile + t) + kv, slot = idx % kSlots;
+          if (idx >= kSlots && !(ok = wait_warp(&c->empty[slot], (idx / kSlots - 1) & 1, c, A.status))) break;
+          uint8_t* dst = s_kv + slot * kTileBytes;
+          if (kv == 0) {
+            if (lane == 0) *(volatile uint32_t*)&c->bad[(tile + t) & 15] = bads;
+          } else if (bads != 0) {   // V of a page that is not there: zeros
+            for (int x = lane; x < kTileBytes / 16; x += 32)
+              if ((bads >> (x >> 8)) & 1u) reinterpret_cast<uint4*>(dst)[x] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&c->full[slot], __popc(goods) * 4096);
+            if (kv == 1 && (p.k0 + t + 1) * kRows > p.edge) mbar_arrive(&c->edge_go[slot]);
+          }
+          ++loads;
+          __syncwarp();
+          if (good)
+            tma_load_4d(dst + lane * 4096, kv == 0 ? (const void*)&tmK : (const void*)&tmV, 0, 0, 0,
+                        (phys * A.Hk + p.kvh) * 2, &c->full[slot]);
+        }
+        if (!ok) break;
+      }
+      tile += ntp;
+    }
+    // copies in flight land before the block ends
+    for (uint32_t j = loads > kSlots ? loads - kSlots : 0; j < loads; ++j)
+      mbar_wait_bounded(&c->full[j % kSlots], (j / kSlots) & 1, A.status);
+    if (pieces > 0) mbar_wait_bounded(&c->q_full, (pieces - 1) & 1, A.status);
+  } else {
+    // ------------------------------------------------------------ the edge of V
+    const int w = warp - 10;
+    // edge_go orders these warps behind the loads: they skip most uses of a
+    // slot, so the parity of its full barrier alone would not tell which one
+    uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
+    int piece = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int ntp = p.k1 - p.k0;
+      for (int t = max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
+        const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
+        if (!(ok = wait_warp(&c->edge_go[slot], (gone >> slot) & 1, c, A.status))) break;
+        gone ^= 1u << slot;
+        if (!(ok = wait_warp(&c->full[slot], (idx / kSlots) & 1, c, A.status))) break;
+        const int base = (p.k0 + t) * kRows;
+        uint4* sv = reinterpret_cast<uint4*>(s_kv + slot * kTileBytes);   // 16-byte chunk x: token group x / 128, row (x / 8) % 8
+        bool found = false;
+        for (int x = (max(0, p.edge - base) >> 3) * 128 + w * 32 + lane; x < kTileBytes / 16; x += 64) {
+          const int pos = base + (x >> 7) * 8 + ((x >> 3) & 7);
+          if (pos >= p.end) {
+            sv[x] = make_uint4(0, 0, 0, 0);
+          } else if (pos >= p.edge) {
+            uint4 q = sv[x];
+            uint32_t* e = reinterpret_cast<uint32_t*>(&q);
+            bool hit = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (!bf16_pair_nonfinite(e[j])) continue;
+              hit = true;
+              if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u;
+              if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0x0000ffffu;
+            }
+            if (hit) sv[x] = q;
+            found |= hit;
+          }
+        }
+        if (found) *(volatile int*)&c->poison[piece & 3] = piece + 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->clean[slot]);
+      }
+      tile += ntp;
+      ++piece;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+// Joins the pieces of a cut item, in the order of the cache: a warp a row.
+// Block (c, y) takes rows 8 y on of the item that begins in block c of the
+// attention kernel and does not end there; the others leave at once.
+__global__ void __launch_bounds__(256) rows_merge_kernel(RowsAttnArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  const int ctas = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31;
+  int4 d = A.desc[2 * c + 1];
+  if (!(d.w & kDescValid)) return;
+  const bool dual = d.w & kDescDual;
+  const int R = blockIdx.y * 8 + (threadIdx.x >> 5), half = R >> 7, r = R & 127;
+  const int t_row = r / A.G, g = r - t_row * A.G;
+  const Seq s = load_seq(A, d.x, nullptr);
+  const int tok = d.z * s.T + half * A.tpt + t_row;    // the row in its sequence
+  if ((dual && half) || t_row >= A.tpt || tok >= s.n) return;
+  float M = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  int cc = c, which = 1;
+  while (true) {
+    const size_t at = (((size_t)cc * 2 + which) * 2 + half) * kRows + r;
+    const float2 ml = A.part_ml[at];
+    if (ml.y != 0.f) {
+      const float4 x = reinterpret_cast<const float4*>(A.part + at * kD)[lane];
+      const float Mn = fmaxf(M, ml.x);
+      const float w0 = l == 0.f ? 0.f : ex2(M - Mn), w1 = ex2(ml.x - Mn);
+      o.x = o.x * w0 + x.x * w1;
+      o.y = o.y * w0 + x.y * w1;
+      o.z = o.z * w0 + x.z * w1;
+      o.w = o.w * w0 + x.w * w1;
+      l = l * w0 + ml.y * w1;
+      M = Mn;
+    }
+    if (d.w & kDescLast) break;
+    which = 0;
+    do {
+      if (++cc >= ctas) break;
+      d = A.desc[2 * cc];
+    } while (!(d.w & kDescValid));
+    if (cc >= ctas) break;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t row = (size_t)(s.row0 + tok) * A.Hq + (size_t)A.desc[2 * c + 1].y * A.G + g;
+  uint2 w;
+  w.x = pack_bf16(o.x * inv, o.y * inv);
+  w.y = pack_bf16(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(A.out + row * kD)[lane] = w;
+  if (lane == 0 && A.lse != nullptr) A.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
+}
+
+}  // namespace
+
+int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                          int num_sms, cudaStream_t stream) {
+  const int ctas = std::min(num_sms, kRowsMaxCtas);
+  if (smem_limit_at_least(reinterpret_cast<const void*>(rows_attention_kernel), (int)kSmemBytes) != cudaSuccess)
+    return SA_ERR_CUDA;
+  cudaError_t e = launch_pdl(rows_attention_kernel, dim3(ctas), dim3(kThreads), kSmemBytes, stream, A, tmQ, tmK, tmV);
+  if (e != cudaSuccess) return SA_ERR_CUDA;
+  e = launch_pdl(rows_merge_kernel, dim3(ctas, 2 * kRows / 8), dim3(256), 0, stream, A);
+  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // namespace sa

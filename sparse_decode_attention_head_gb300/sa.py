@@ -36,6 +36,10 @@ SELECT_GROUP = 1
 BLOCKS_TAIL = -1
 HEAD_DIM = 128
 PAGE_SIZE = 16
+ROPE_HALVES = 0
+ROPE_PAIRS = 1
+MAX_AXES = 4
+MAX_TREE = 64
 
 
 class SAError(RuntimeError):
@@ -54,6 +58,10 @@ class _Problem(ctypes.Structure):
     ]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("axes", ctypes.c_int32), ("axis_pairs", ctypes.c_int32 * MAX_AXES)]
+
+
 _lib = None
 
 
@@ -65,7 +73,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with sparse_decode_attention_head_gb300.build_lib.build()")
         L = ctypes.CDLL(LIB_PATH)
         P = ctypes.POINTER(_Problem)
-        vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sig = {
             "sa_block_slots": (i32, [P]),
             "sa_workspace_size": (sz, [P]),
@@ -92,6 +100,15 @@ def lib():
                                                    ctypes.POINTER(vp)]),
             "sa_step_plan_launch": (ctypes.c_int, [vp, vp]),
             "sa_step_plan_destroy": (ctypes.c_int, [vp]),
+            "sa_rows_workspace_size": (sz, [P]),
+            "sa_qk_norm_rope": (ctypes.c_int, [P, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float,
+                                               ctypes.POINTER(_Rope), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_prompt_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_tree_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_accept_rows": (ctypes.c_int, [P, vp, vp, vp, vp, vp, i32, vp, vp, vp]),
+            "sa_plan_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_compact_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_copy_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, i32, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -187,12 +204,16 @@ class Problem:
 
 
 class Workspace:
-    """Device scratch for one problem (sa_workspace_size bytes), zeroed once."""
+    """Device scratch for one problem (sa_workspace_size bytes), zeroed once.
+    rows: also large enough for the packed-row and page calls."""
 
-    def __init__(self, prob: Problem, device="cuda"):
+    def __init__(self, prob: Problem, device="cuda", rows: bool = False):
         n = prob.workspace_size()
         if n == 0:
             raise SAError(SA_ERR_INVALID_ARG, "sa_workspace_size")
+        if rows:
+            n = max(n, int(lib().sa_rows_workspace_size(prob.ref)))
+        self.rows = bool(rows)
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
         _check(lib().sa_workspace_init(_ptr(self.buf), n, _stream()), "sa_workspace_init")
 
@@ -473,3 +494,184 @@ class StepPlan:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ packed rows and pages
+
+class Rope:
+    """Rotary positions (sa_rope): dim pairs for each position axis and which
+    dims make a pair (ROPE_HALVES: j with j + R/2; ROPE_PAIRS: 2j with 2j + 1)."""
+
+    def __init__(self, axis_pairs: Sequence[int] = (HEAD_DIM // 2,), layout: int = ROPE_HALVES):
+        self.axis_pairs, self.layout = [int(x) for x in axis_pairs], layout
+        if not 1 <= len(self.axis_pairs) <= MAX_AXES:
+            raise ValueError(f"1 to {MAX_AXES} axes, got {len(self.axis_pairs)}")
+        self._c = _Rope(layout, len(self.axis_pairs), (ctypes.c_int32 * MAX_AXES)(*self.axis_pairs))
+
+    @property
+    def pairs(self) -> int:
+        return sum(self.axis_pairs)
+
+
+def _need_rows(t: torch.Tensor, name: str, heads: int, n: Optional[int] = None):
+    """Packed rows [n][heads][D] bf16, dense within a row; returns the row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1:] != (heads, HEAD_DIM) or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must have shape ({'n' if n is None else n}, {heads}, {HEAD_DIM}), got {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM)):
+        raise ValueError(f"{name} must be dense within a row")
+    return t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
+
+
+def _need_pools(prob: Problem, k_pool, v_pool):
+    shape = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
+    _need(k_pool, torch.bfloat16, "k_pool", shape)
+    _need(v_pool, torch.bfloat16, "v_pool", shape)
+
+
+def _need_ws(ws: Workspace):
+    if not ws.rows:
+        raise ValueError("the workspace must be made with rows=True")
+
+
+def _one_device(*tensors):
+    """All on one device, and that device the current one."""
+    d = {t.device for t in tensors if t is not None}
+    if len(d) != 1 or next(iter(d)).index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current device, got {sorted(map(str, d))}")
+
+
+def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_out, k_pool, v_pool, ws: Workspace,
+                 rope: Optional[Rope] = None, inv_freq=None, positions=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6):
+    """Per-head norm and rotation of packed query and key rows; queries to
+    q_out, keys and values appended to the pages (sa_qk_norm_rope).  q, k, v
+    [n][heads][D] may be slices of one projection (any row stride that is a
+    multiple of 8).  positions: int32 [axes][n], None: the cache positions."""
+    n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    strides = [_need_rows(q, "q", prob.Hq), _need_rows(k, "k", prob.Hk, n), _need_rows(v, "v", prob.Hk, n)]
+    _need(row_offsets, torch.int32, "row_offsets", (prob.B + 1,))
+    _need(seq_lens, torch.int32, "seq_lens", (prob.B,))
+    _need(page_table, torch.int32, "page_table", (prob.B, prob.max_pages_per_seq))
+    _need(q_out, torch.bfloat16, "q_out", (n, prob.Hq, prob.D))
+    _need_pools(prob, k_pool, v_pool)
+    _need_ws(ws)
+    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, torch.bfloat16, nm, (prob.D,))
+    if rope is not None:
+        if inv_freq is None:
+            raise ValueError("a rotation needs inv_freq")
+        _need(inv_freq, torch.float32, "inv_freq", (rope.pairs,))
+        if positions is not None:
+            _need(positions, torch.int32, "positions", (len(rope.axis_pairs), n))
+    _one_device(q, k, v, row_offsets, seq_lens, page_table, q_out, k_pool, v_pool, q_weight, k_weight, inv_freq,
+                positions, ws.buf)
+    _check(lib().sa_qk_norm_rope(prob.ref, n, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
+                                 _ptr(q_weight), _ptr(k_weight), float(eps),
+                                 None if rope is None else ctypes.byref(rope._c), _ptr(inv_freq), _ptr(positions),
+                                 _ptr(row_offsets), _ptr(seq_lens), _ptr(page_table), _ptr(q_out), _ptr(k_pool),
+                                 _ptr(v_pool), _ptr(ws.buf), _stream()), "sa_qk_norm_rope")
+
+
+def _check_attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, *more):
+    n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    _need(q, torch.bfloat16, "q", (n, prob.Hq, prob.D))
+    _need_pools(prob, k_pool, v_pool)
+    _need(page_table, torch.int32, "page_table", (prob.B, prob.max_pages_per_seq))
+    _need(seq_lens, torch.int32, "seq_lens", (prob.B,))
+    _need(row_offsets, torch.int32, "row_offsets", (prob.B + 1,))
+    _need(out, torch.bfloat16, "out", (n, prob.Hq, prob.D))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (n, prob.Hq))
+    _need_ws(ws)
+    _one_device(q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws.buf, *more)
+    return n
+
+
+def prompt_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, ws: Workspace, lse=None):
+    """Causal attention of packed prompt rows over the paged cache
+    (sa_prompt_attention): row i of a sequence's n sees positions 0 .. L - n + i."""
+    n = _check_attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws)
+    _check(lib().sa_prompt_attention(prob.ref, n, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
+                                     _ptr(seq_lens), _ptr(row_offsets), _ptr(out), _ptr(lse), _ptr(ws.buf),
+                                     _stream()), "sa_prompt_attention")
+
+
+def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, tree_mask, out, ws: Workspace,
+                   lse=None):
+    """Attention of a tree's drafted tokens, a sequence's newest n <= MAX_TREE
+    rows, over the cache before them and the drafts whose bits are set in
+    tree_mask [n_rows] int64 (sa_tree_attention)."""
+    if isinstance(q, torch.Tensor) and q.dim():
+        _need(tree_mask, torch.int64, "tree_mask", (q.shape[0],))
+    n = _check_attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, tree_mask)
+    _check(lib().sa_tree_attention(prob.ref, n, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(seq_lens),
+                                   _ptr(row_offsets), _ptr(tree_mask), _ptr(out), _ptr(lse), _ptr(ws.buf), _stream()),
+           "sa_tree_attention")
+
+
+def accept_rows(prob: Problem, k_pool, v_pool, page_table, base_lens, path, path_cnt, ws: Workspace):
+    """The accepted nodes' K and V rows to the places behind base_lens
+    (sa_accept_rows); path [B][max_path], path_cnt [B]."""
+    _need_pools(prob, k_pool, v_pool)
+    _need(page_table, torch.int32, "page_table", (prob.B, prob.max_pages_per_seq))
+    _need(base_lens, torch.int32, "base_lens", (prob.B,))
+    most = path.shape[1] if isinstance(path, torch.Tensor) and path.dim() == 2 else 0
+    _need(path, torch.int32, "path", (prob.B, most))
+    _need(path_cnt, torch.int32, "path_cnt", (prob.B,))
+    _need_ws(ws)
+    _one_device(k_pool, v_pool, page_table, base_lens, path, path_cnt, ws.buf)
+    _check(lib().sa_accept_rows(prob.ref, _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(base_lens), _ptr(path),
+                                most, _ptr(path_cnt), _ptr(ws.buf), _stream()), "sa_accept_rows")
+
+
+def plan_pages(prob: Problem, table_in, parent, keep, lens, table_out, copy_src, copy_dst, counts, ws: Workspace):
+    """The next page table: new row b goes on from old row parent[b] with its
+    first keep[b] tokens and gets room for lens[b] (sa_plan_pages).  The
+    copies to make (copy_pages) go to copy_src / copy_dst [B]; counts [2]: their
+    number, free pages left."""
+    for t, nm in ((table_in, "table_in"), (table_out, "table_out")):
+        _need(t, torch.int32, nm, (prob.B, prob.max_pages_per_seq))
+    for t, nm in ((parent, "parent"), (keep, "keep"), (lens, "lens"), (copy_src, "copy_src"), (copy_dst, "copy_dst")):
+        _need(t, torch.int32, nm, (prob.B,))
+    _need(counts, torch.int32, "counts", (2,))
+    _need_ws(ws)
+    _one_device(table_in, parent, keep, lens, table_out, copy_src, copy_dst, counts, ws.buf)
+    _check(lib().sa_plan_pages(prob.ref, _ptr(table_in), _ptr(parent), _ptr(keep), _ptr(lens), _ptr(table_out),
+                               _ptr(copy_src), _ptr(copy_dst), _ptr(counts), _ptr(ws.buf), _stream()), "sa_plan_pages")
+
+
+def compact_pages(prob: Problem, table_in, seq_lens, table_out, move_src, move_dst, counts, ws: Workspace):
+    """The live pages packed to the front of the pool (sa_compact_pages): the
+    new table and the moves to make (copy_pages), move_src / move_dst
+    [num_pages]; counts [2]: moves, live pages."""
+    for t, nm in ((table_in, "table_in"), (table_out, "table_out")):
+        _need(t, torch.int32, nm, (prob.B, prob.max_pages_per_seq))
+    _need(seq_lens, torch.int32, "seq_lens", (prob.B,))
+    for t, nm in ((move_src, "move_src"), (move_dst, "move_dst")):
+        _need(t, torch.int32, nm, (prob.num_pages,))
+    _need(counts, torch.int32, "counts", (2,))
+    _need_ws(ws)
+    _one_device(table_in, seq_lens, table_out, move_src, move_dst, counts, ws.buf)
+    _check(lib().sa_compact_pages(prob.ref, _ptr(table_in), _ptr(seq_lens), _ptr(table_out), _ptr(move_src),
+                                  _ptr(move_dst), _ptr(counts), _ptr(ws.buf), _stream()), "sa_compact_pages")
+
+
+def copy_pages(prob: Problem, k_pool, v_pool, src, dst, count, ws: Workspace):
+    """Page src[i] to page dst[i] in both pools for i < count[0] (sa_copy_pages);
+    count: int32 on the device (the counts of plan_pages or compact_pages)."""
+    _need_pools(prob, k_pool, v_pool)
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else 0
+    _need(src, torch.int32, "src", (n,))
+    _need(dst, torch.int32, "dst", (n,))
+    _need(count, torch.int32, "count")
+    if count.numel() < 1:
+        raise ValueError("count must hold a number")
+    _need_ws(ws)
+    _one_device(k_pool, v_pool, src, dst, count, ws.buf)
+    _check(lib().sa_copy_pages(prob.ref, _ptr(k_pool), _ptr(v_pool), _ptr(src), _ptr(dst), _ptr(count), n, _ptr(ws.buf),
+                               _stream()), "sa_copy_pages")
