@@ -50,15 +50,37 @@ constexpr int kRows = 128;               // rows of a query tile, tokens of a KV
 constexpr int kTileBytes = kRows * kD * 2;
 constexpr int kSlots = 5;                // K and V tiles in flight: what 227 KB leave beside two query tiles
 constexpr int kThreads = 384;
+// Registers a thread, out of the 168 the block is launched with: a row's 128
+// scores stay in the softmax threads' registers.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
 constexpr int kItemCost = 256;           // an item's fixed cost in KV tokens (query load, epilogue)
 constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
 
+// A piece of a block's run: KV tiles [k0, k1) of one item.  The loading warp
+// walks the run and hands the pieces to the other roles through a ring.
+struct Piece {
+  int b, kvh, i;
+  int k0, k1, nt;     // of the item's nt tiles; k0 < 0: the run is over
+  int row0;           // first packed row of the item
+  int tokens;         // of the item
+  int end, edge;      // item_end, item_edge
+  int a;              // tokens of the sequence ahead of its rows
+  int first;          // the item's first row in the sequence
+  bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
+};
+
+constexpr int kPieces = 4;
+constexpr int kPieceReaders = 11;        // warps: softmax, matrix instructions, edge
+
 struct Ctl {
+  Piece piece[kPieces];
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2][2], o_done[2];
   uint64_t edge_go[kSlots], clean[kSlots];   // a V tile at the edge: its load is under way, it is clean
   uint64_t ml_full, ml_free;
   uint64_t drain;
@@ -199,18 +221,7 @@ __device__ int4 locate(const RowsAttnArgs& A, long long w) {
   return make_int4(A.B, 0, 0, 0);
 }
 
-// The pieces of a block's run, in order; every role of the block walks them.
-struct Piece {
-  int b, kvh, i;
-  int k0, k1, nt;     // KV tiles [k0, k1) of the item's nt
-  int row0;           // first packed row of the item
-  int tokens;         // of the item
-  int end, edge;      // item_end, item_edge
-  int a;              // tokens of the sequence ahead of its rows
-  int first;          // the item's first row in the sequence
-  bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
-};
-
+// One thread walks a block's run, piece by piece.
 struct Walk {
   const RowsAttnArgs& A;
   int b, kvh, i, kt;
@@ -264,21 +275,26 @@ __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// Adds the non-finite values of V at the item's edge positions that this row
-// sees to its dims [32 c, 32 c + 32): the product with them was taken as zero.
-__device__ __noinline__ void add_poison(const RowsAttnArgs& A, const Piece& p, int lim, unsigned long long word, int c,
-                                        float* o) {
-  for (int t = max(p.edge, p.k0 * kRows); t < min(p.end, p.k1 * kRows); ++t) {
-    const int bit = t - p.a;
-    if (!(t < lim || (bit >= 0 && bit < 64 && ((word >> bit) & 1ull)))) continue;
-    const int phys = __ldg(A.page_table + (size_t)p.b * A.mpp + t / kP);
+// The non-finite values of V at the edge positions [t0, t1) that a row sees
+// are added to its stored result (the product with them was taken as zero).
+// Rare, and kept out of the kernel's registers.
+struct EdgeRow {
+  const int* pages;             // the sequence's row of the page table
+  unsigned long long word;
+  int t0, t1, lim, a;           // sees t < lim, and bit t - a of word
+};
+__device__ __noinline__ void add_poison(const RowsAttnArgs& A, EdgeRow e, int kvh, __nv_bfloat16* out, float* part) {
+  for (int t = e.t0; t < e.t1; ++t) {
+    const int bit = t - e.a;
+    if (!(t < e.lim || (bit >= 0 && bit < 64 && ((e.word >> bit) & 1ull)))) continue;
+    const int phys = __ldg(e.pages + t / kP);
     if (phys < 0 || phys >= A.num_pages) continue;
-    const uint32_t* v =
-        reinterpret_cast<const uint32_t*>(A.v_pool + (((size_t)phys * A.Hk + p.kvh) * kP + t % kP) * kD + 32 * c);
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t w = __ldg(v + j);
-      if ((w & 0x7f80u) == 0x7f80u) o[2 * j] += bf16_lo(w);
-      if ((w & 0x7f800000u) == 0x7f800000u) o[2 * j + 1] += bf16_hi(w);
+    const __nv_bfloat16* v = A.v_pool + (((size_t)phys * A.Hk + kvh) * kP + t % kP) * kD;
+    for (int d = 0; d < kD; ++d) {
+      const float x = __bfloat162float(v[d]);
+      if (isfinite(x)) continue;
+      if (out != nullptr) out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
+      else part[d] += x;
     }
   }
 }
@@ -306,12 +322,17 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     mbar_init(&c->q_empty, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&c->s_full[h], 1);
-      mbar_init(&c->p_full[h], kRows);
+      mbar_init(&c->p_full[h][0], kRows);
+      mbar_init(&c->p_full[h][1], kRows);
       mbar_init(&c->o_done[h], 1);
     }
     mbar_init(&c->ml_full, kRows);
     mbar_init(&c->ml_free, kRows);
     mbar_init(&c->drain, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&c->piece_full[i], 1);
+      mbar_init(&c->piece_empty[i], kPieceReaders);
+    }
     c->abort = 0;
     for (int i = 0; i < 4; ++i) c->poison[i] = 0;
     fence_mbar_init();
@@ -329,10 +350,9 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c->tmem;
-  Walk walk(A, c);
-  Piece p;
 
   if (warp < 8) {
+    regs_inc<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax: a thread a row
     const int h = warp >> 2;
     const int r = tid & 127;
@@ -340,12 +360,14 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     const uint32_t tS = tmem + lanes + h * 128, tO = tmem + lanes + 256 + h * 128;
     const int t_row = r / A.G, g = r - t_row * A.G;
     uint32_t steps_done = 0, items_done = 0, duals = 0, tiles = 0;
-    int piece = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
-      const int ntp = p.k1 - p.k0;
-      const int N = p.dual ? ntp : 2 * ntp;
-      const int tok = t_row + (p.dual || h == 0 ? 0 : A.tpt);
+    for (int piece = 0; (ok = wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status)); ++piece) {
+      const Piece& p = c->piece[piece % kPieces];
+      const int k0 = p.k0, ntp = p.k1 - k0, edge = p.edge;
+      const bool dual = p.dual;
+      if (k0 < 0) break;
+      const int N = dual ? ntp : 2 * ntp;
+      const int tok = t_row + (dual || h == 0 ? 0 : A.tpt);
       const bool valid = t_row < A.tpt && tok < p.tokens;
       // what the row sees: positions below lim, and bit j of its word for position p.a + j
       int lim = 0;
@@ -360,15 +382,15 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       }
       float m = -INFINITY, l = 0.f;
       for (int s = h; s < N; s += 2) {
-        const int t = p.dual ? s : s >> 1;
-        const int kt = p.k0 + t;
+        const int t = dual ? s : s >> 1;
+        const int kt = k0 + t;
         if (!(ok = wait_warp(&c->s_full[h], steps_done & 1, c, A.status))) break;
         ++steps_done;
         tc_fence_after();
         float v[128];
         tmem_ld128(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
-        if ((kt + 1) * kRows > p.edge || bad != 0) {
+        if ((kt + 1) * kRows > edge || bad != 0) {
           // bit j of see[w]: column 32 w + j
           const int base = kt * kRows;
 #pragma unroll
@@ -386,9 +408,15 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             for (int j = 0; j < 32; ++j) v[32 * w + j] = (see >> j) & 1u ? v[32 * w + j] : -INFINITY;
           }
         }
-        float mx = v[0];
+        float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int j = 1; j < 128; ++j) mx = fmaxf(mx, v[j]);
+        for (int j = 4; j < 124; j += 8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top[x] = fmaxf(fmaxf(top[x], v[j + x]), v[j + 4 + x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], v[124 + x]);
+        float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         mx *= A.scale_log2;
         if (m == -INFINITY) m = mx;   // all zeros so far: nothing to rescale
         const bool grow = mx > m + kLag;
@@ -410,22 +438,30 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           }
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        float sum0 = 0.f, sum1 = 0.f;
-        uint32_t pw[2][32];
+        const uint64_t scale2 = pack2(A.scale_log2, A.scale_log2), shift2 = pack2(-mu, -mu);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 128; j += 2) {
-          const float p0 = ex2(fmaf(v[j], A.scale_log2, -mu));
-          const float p1 = ex2(fmaf(v[j + 1], A.scale_log2, -mu));
-          sum0 += p0;
-          sum1 += p1;
-          pw[j >> 6][(j & 63) >> 1] = pack_bf16(p0, p1);
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float p0, p1;
+            unpack2(fma2(pack2(v[32 * q4 + 2 * j], v[32 * q4 + 2 * j + 1]), scale2, shift2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
+            pw[j] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tS + 16 * q4, pw);
+          if (q4 & 1) {   // half of the weights are there: their product may begin
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&c->p_full[h][q4 >> 1]);
+          }
         }
-        tmem_st32(tS, pw[0]);
-        tmem_st32(tS + 32, pw[1]);
+        float sum0, sum1;
+        unpack2(add2(sum[0], sum[1]), sum0, sum1);
         l += sum0 + sum1;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&c->p_full[h]);
       }
       if (!ok) break;
       const bool mine = N > h;     // this group had a tile
@@ -479,7 +515,6 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] *= inv;
-          if (poisoned && valid) add_poison(A, p, lim, word, q4, o);
           if (whole) {
             if (valid) {
               uint4* dst = reinterpret_cast<uint4*>(A.out + row * kD + 32 * q4);
@@ -494,6 +529,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
+        if (poisoned && valid)
+          add_poison(A, EdgeRow{A.page_table + (size_t)p.b * A.mpp, word, max(p.edge, p.k0 * kRows),
+                                min(p.end, p.k1 * kRows), lim, p.a},
+                     p.kvh, whole ? A.out + row * kD : nullptr, whole ? nullptr : A.part + (slot * kRows + r) * kD);
         if (whole) {
           if (valid && A.lse != nullptr) A.lse[row] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.693147180559945309f;
         } else {
@@ -514,17 +553,23 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         ++duals;
       }
       tiles += ntp;
-      ++piece;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
     }
-  } else if (warp == 8) {
+  } else {
+    regs_dec<kOtherRegs>();
+  if (warp == 8) {
     // ------------------------------------------------------------ matrix instructions
     if (lane == 0) {
       constexpr uint32_t idS = bf16_idesc(128, 128, false), idO = bf16_idesc(128, 128, true);
       uint32_t tile = 0, pieces = 0, cleaned = 0, p_seen[2] = {0, 0};   // cleaned: a parity bit a slot
       const uint32_t aQ = smem_u32(s_q), aKV = smem_u32(s_kv);
       bool ok = true;
-      while (ok && walk.next(p)) {
+      for (int piece = 0; wait_bar(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
+        const Piece p = c->piece[piece % kPieces];
+        mbar_arrive(&c->piece_empty[piece % kPieces]);
         const int ntp = p.k1 - p.k0;
+        if (p.k0 < 0) break;
         if (ntp == 0) continue;
         const int N = p.dual ? ntp : 2 * ntp;
         if (!(ok = wait_bar(&c->q_full, pieces & 1, c, A.status))) break;
@@ -556,17 +601,22 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
               cleaned ^= 1u << slot;
             }
           }
-          if (!(ok = wait_bar(&c->p_full[h], p_seen[h] & 1, c, A.status))) break;
-          ++p_seen[h];
-          tc_fence_after();
           const uint64_t dv = smem_desc(aKV + slot * kTileBytes, 1024, 2048);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, dv + k * (4096 / 16), idO, s >= 2 || k != 0);
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = wait_bar(&c->p_full[h][half], p_seen[h] & 1, c, A.status))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              tc_mma_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, dv + k * (4096 / 16), idO, s >= 2 || k != 0);
+          }
+          if (!ok) break;
+          ++p_seen[h];
           if (p.dual || h == 1) tc_commit(&c->empty[slot]);
           if (s + 2 >= N) tc_commit(&c->o_done[h]);
           if (s + 2 < N && !(ok = issue_s(s + 2))) break;
         }
+        if (!ok) break;
         tile += ntp;
       }
       // nothing of this block is in flight when it frees its TMEM and ends
@@ -579,7 +629,18 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     uint32_t tile = 0, pieces = 0, loads = 0;
     const uint32_t q_bytes = (uint32_t)(A.tpt * A.G) * kD * 2;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    Walk walk(A, c);
+    for (int piece = 0;; ++piece) {
+      Piece p;
+      if (!walk.next(p)) p.k0 = p.k1 = -1;
+      if (piece >= kPieces &&
+          !(ok = wait_warp(&c->piece_empty[piece % kPieces], (piece / kPieces - 1) & 1, c, A.status)))
+        break;
+      if (lane == 0) {
+        c->piece[piece % kPieces] = p;
+        mbar_arrive(&c->piece_full[piece % kPieces]);
+      }
+      if (p.k0 < 0) break;
       const int ntp = p.k1 - p.k0;
       if (ntp == 0) continue;
       if (pieces > 0 && !(ok = wait_warp(&c->q_empty, (pieces - 1) & 1, c, A.status))) break;
@@ -621,6 +682,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         }
         if (!ok) break;
       }
+      if (!ok) break;
       tile += ntp;
     }
     // copies in flight land before the block ends
@@ -633,9 +695,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     // edge_go orders these warps behind the loads: they skip most uses of a
     // slot, so the parity of its full barrier alone would not tell which one
     uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
-    int piece = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
+      const Piece p = c->piece[piece % kPieces];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
+      if (p.k0 < 0) break;
       const int ntp = p.k1 - p.k0;
       for (int t = max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
         const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
@@ -669,9 +734,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->clean[slot]);
       }
+      if (!ok) break;
       tile += ntp;
-      ++piece;
     }
+  }
   }
   tc_fence_before();
   __syncthreads();
