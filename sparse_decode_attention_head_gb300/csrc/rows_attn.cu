@@ -94,17 +94,44 @@ struct Ctl {
 constexpr size_t kSmemBytes = 1024 + 2 * kTileBytes + kSlots * kTileBytes + sizeof(Ctl);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && *(volatile int*)&c->abort) return false;
-  }
-  set_status(status, SA_ERR_TIMEOUT);
-  *(volatile int*)&c->abort = 1;
-  return false;
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
 }
 
-// The same by a whole warp: all lanes see the same answer.
+// Waits with a limit of kWaitNs; a wait that runs out, here or elsewhere in the
+// block, ends the block's work.
+constexpr unsigned long long kWaitNs = 2000000000ull;
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63u) != 0) continue;
+    if (*(volatile int*)&c->abort) return false;
+    const unsigned long long t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitNs) {
+      set_status(status, SA_ERR_TIMEOUT);
+      *(volatile int*)&c->abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// For what is in flight when a block ends: not cut short by an abort.
+__device__ __forceinline__ void wait_out(uint64_t* bar, uint32_t parity, int* status) {
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (now_ns() - t0 > kWaitNs) {
+      set_status(status, SA_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// wait_bar by a whole warp: all lanes see the same answer.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, c, status));
 }
@@ -122,6 +149,18 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
+
+// A place in the ring of K and V tiles and the parity of its use.
+struct Ring {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void advance(int n) {
+    slot += n;
+    if (slot >= kSlots) {
+      slot -= kSlots;
+      parity ^= 1;
+    }
+  }
+};
 
 // ---------------------------------------------------------------- the items
 
@@ -560,68 +599,102 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     regs_dec<kOtherRegs>();
   if (warp == 8) {
     // ------------------------------------------------------------ matrix instructions
-    if (lane == 0) {
-      constexpr uint32_t idS = bf16_idesc(128, 128, false), idO = bf16_idesc(128, 128, true);
-      uint32_t tile = 0, pieces = 0, cleaned = 0, p_seen[2] = {0, 0};   // cleaned: a parity bit a slot
-      const uint32_t aQ = smem_u32(s_q), aKV = smem_u32(s_kv);
-      bool ok = true;
-      for (int piece = 0; wait_bar(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
-        const Piece p = c->piece[piece % kPieces];
-        mbar_arrive(&c->piece_empty[piece % kPieces]);
-        const int ntp = p.k1 - p.k0;
-        if (p.k0 < 0) break;
-        if (ntp == 0) continue;
-        const int N = p.dual ? ntp : 2 * ntp;
-        if (!(ok = wait_bar(&c->q_full, pieces & 1, c, A.status))) break;
-        ++pieces;
-        auto issue_s = [&](int s) -> bool {
-          const int h = s & 1, t = p.dual ? s : s >> 1;
-          const uint32_t idx = 2 * (tile + t), slot = idx % kSlots;
-          if ((p.dual || h == 0) && !wait_bar(&c->full[slot], (idx / kSlots) & 1, c, A.status)) return false;
-          const uint64_t dq = smem_desc(aQ + (p.dual ? 0 : h * kTileBytes), 16, 1024);
-          const uint64_t dk = smem_desc(aKV + slot * kTileBytes, 16, 2048);
+    // The whole warp runs the loop and one elected lane issues; the others
+    // wait for it at the end of each group (spinning ahead at the next
+    // barrier they would take its issue slots).
+    constexpr uint32_t idS = bf16_idesc(128, 128, false), idO = bf16_idesc(128, 128, true);
+    const uint64_t dQ = smem_desc(smem_u32(s_q), 16, 1024);
+    const uint64_t dK = smem_desc(smem_u32(s_kv), 16, 2048), dV = smem_desc(smem_u32(s_kv), 1024, 2048);
+    Ring kr, vr;               // the next K and the next V tile
+    vr.advance(1);
+    uint32_t pieces = 0, cleaned = 0, p_par[2] = {0, 0};   // cleaned: a parity bit a slot
+    bool ok = true;
+    for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
+      const Piece* pp = &c->piece[piece % kPieces];
+      const int k0 = pp->k0, ntp = pp->k1 - k0, edge = pp->edge;
+      const bool dual = pp->dual;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
+      if (k0 < 0) break;
+      if (ntp == 0) continue;
+      const int N = dual ? ntp : 2 * ntp;
+      if (!(ok = wait_warp(&c->q_full, pieces & 1, c, A.status))) break;
+      ++pieces;
+      // S of half h from the tile at kr; `last` of the tile's, of the piece's
+      auto issue_s = [&](int h, bool first_of_tile, bool last_of_tile, bool last) -> bool {
+        if (first_of_tile && !wait_warp(&c->full[kr.slot], kr.parity, c, A.status)) return false;
+        const uint64_t q = dQ + (dual ? 0 : h * (kTileBytes / 16)), k = dK + kr.slot * (kTileBytes / 16);
+        const uint32_t d = tmem + h * 128;
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ss(tmem + h * 128, dq + (k >> 2) * (kTileBytes / 2 / 16) + (k & 3) * 2,
-                      dk + (k >> 2) * (1024 / 16) + (k & 3) * 2, idS, k != 0);
+          for (int x = 0; x < 8; ++x)
+            tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2, k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS,
+                      x != 0);
           tc_commit(&c->s_full[h]);
-          if (p.dual || h == 1) tc_commit(&c->empty[slot]);
-          if (s == N - 1) tc_commit(&c->q_empty);
-          return true;
-        };
-        if (!(ok = issue_s(0))) break;
-        if (N > 1 && !(ok = issue_s(1))) break;
-        for (int s = 0; s < N; ++s) {
-          const int h = s & 1, t = p.dual ? s : s >> 1;
-          const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
-          if (p.dual || h == 0) {
-            if (!(ok = wait_bar(&c->full[slot], (idx / kSlots) & 1, c, A.status))) break;
-            if ((p.k0 + t + 1) * kRows > p.edge) {
-              if (!(ok = wait_bar(&c->clean[slot], (cleaned >> slot) & 1, c, A.status))) break;
-              cleaned ^= 1u << slot;
+          if (last_of_tile) tc_commit(&c->empty[kr.slot]);
+          if (last) tc_commit(&c->q_empty);
+        }
+        __syncwarp();
+        if (last_of_tile) kr.advance(2);
+        return true;
+      };
+      // O of half h from the tile at vr
+      auto issue_o = [&](int h, int kt, bool first_of_tile, bool last_of_tile, bool first, bool last) -> bool {
+        if (first_of_tile) {
+          if (!wait_warp(&c->full[vr.slot], vr.parity, c, A.status)) return false;
+          if ((kt + 1) * kRows > edge) {
+            if (!wait_warp(&c->clean[vr.slot], (cleaned >> vr.slot) & 1, c, A.status)) return false;
+            cleaned ^= 1u << vr.slot;
+          }
+        }
+        const uint64_t v = dV + vr.slot * (kTileBytes / 16);
+        const uint32_t d = tmem + 256 + h * 128, w = tmem + h * 128;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (!wait_warp(&c->p_full[h][part], p_par[h], c, A.status)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 4 * part; x < 4 * part + 4; ++x)
+              tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
+            if (part == 1) {
+              if (last_of_tile) tc_commit(&c->empty[vr.slot]);
+              if (last) tc_commit(&c->o_done[h]);
             }
           }
-          const uint64_t dv = smem_desc(aKV + slot * kTileBytes, 1024, 2048);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!(ok = wait_bar(&c->p_full[h][half], p_seen[h] & 1, c, A.status))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              tc_mma_ts(tmem + 256 + h * 128, tmem + h * 128 + k * 8, dv + k * (4096 / 16), idO, s >= 2 || k != 0);
-          }
-          if (!ok) break;
-          ++p_seen[h];
-          if (p.dual || h == 1) tc_commit(&c->empty[slot]);
-          if (s + 2 >= N) tc_commit(&c->o_done[h]);
-          if (s + 2 < N && !(ok = issue_s(s + 2))) break;
+          __syncwarp();
         }
-        if (!ok) break;
-        tile += ntp;
+        p_par[h] ^= 1;
+        if (last_of_tile) vr.advance(2);
+        return true;
+      };
+      if (dual) {
+        if (!(ok = issue_s(0, true, true, N == 1))) break;
+        if (N > 1 && !(ok = issue_s(1, true, true, N == 2))) break;
+#pragma unroll 1
+        for (int s = 0; s < N; ++s) {
+          if (!(ok = issue_o(s & 1, k0 + s, true, true, s < 2, s + 2 >= N))) break;
+          if (s + 2 < N && !(ok = issue_s(s & 1, true, true, s + 3 == N))) break;
+        }
+      } else {
+        if (!(ok = issue_s(0, true, false, false))) break;
+        if (!(ok = issue_s(1, false, true, ntp == 1))) break;
+#pragma unroll 1
+        for (int t = 0; t < ntp; ++t) {
+          const bool first = t == 0, last = t == ntp - 1;
+          if (!(ok = issue_o(0, k0 + t, true, false, first, last))) break;
+          if (!last && !(ok = issue_s(0, true, false, false))) break;
+          if (!(ok = issue_o(1, k0 + t, false, true, first, last))) break;
+          if (!last && !(ok = issue_s(1, false, true, t + 2 == ntp))) break;
+        }
       }
-      // nothing of this block is in flight when it frees its TMEM and ends
+      if (!ok) break;
+    }
+    // nothing of this block is in flight when it frees its TMEM and ends
+    __syncwarp();
+    if (elect_one()) {
       tc_commit(&c->drain);
-      mbar_wait_bounded(&c->drain, 0, A.status);
+      wait_out(&c->drain, 0, A.status);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -687,8 +760,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     }
     // copies in flight land before the block ends
     for (uint32_t j = loads > kSlots ? loads - kSlots : 0; j < loads; ++j)
-      mbar_wait_bounded(&c->full[j % kSlots], (j / kSlots) & 1, A.status);
-    if (pieces > 0) mbar_wait_bounded(&c->q_full, (pieces - 1) & 1, A.status);
+      wait_out(&c->full[j % kSlots], (j / kSlots) & 1, A.status);
+    if (pieces > 0) wait_out(&c->q_full, (pieces - 1) & 1, A.status);
   } else {
     // ------------------------------------------------------------ the edge of V
     const int w = warp - 10;

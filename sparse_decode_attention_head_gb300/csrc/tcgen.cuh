@@ -129,6 +129,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]
       : "memory");
 }
 
+// One lane of a converged warp.  Matrix instructions and copies take uniform
+// operands: a warp that computes them together and elects a lane to issue
+// keeps them in uniform registers, a lane alone has to move each one there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Two fp32 in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
