@@ -45,7 +45,7 @@ struct RowsAttnArgs {
   const unsigned long long* tree;   // [n_rows] words of a tree, NULL: causal
   __nv_bfloat16* out;               // [n_rows][Hq][kD]
   float* lse;                       // [n_rows][Hq] or NULL
-  float* part;                      // split items: [cta][2][2][128][kD] sums
+  float* part;                      // split items: [cta][2][2][kD / 4][128][4] sums
   float2* part_ml;                  // [cta][2][2][128] (maximum, sum), base 2
   int4* desc;                       // [cta][2] what the partials are of
   int* status;

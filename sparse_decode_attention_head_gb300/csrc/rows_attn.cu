@@ -55,6 +55,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
 constexpr int kItemCost = 256;           // an item's fixed cost in KV tokens (query load, epilogue)
+constexpr int kMinRun = 512;             // the least a block is given, in the same measure
 constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
@@ -199,13 +200,21 @@ __device__ __forceinline__ long long weight_before(const RowsAttnArgs& A, const 
   return (long long)k * (max(s.a, 0) + kItemCost) + (long long)s.T * k * (k + 1) / 2 - cut;
 }
 
-// One warp: the total weight, and per lane the sequences' (chunk by chunk of 32).
-__device__ long long total_weight(const RowsAttnArgs& A, int* status) {
+// One warp: the total weight of all items.  `s` and `mine` are the lane's own
+// sequence, of the first 32, and its weight.
+__device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* status, Seq& s, long long& mine) {
   const int lane = threadIdx.x & 31;
   long long w = 0;
+  mine = 0;
+  s = Seq{};
   for (int b = lane; b < A.B; b += 32) {
-    const Seq s = load_seq(A, b, status);
-    w += weight_before(A, s, s.items) * A.Hk;
+    const Seq x = load_seq(A, b, status);
+    const long long m = weight_before(A, x, x.items) * A.Hk;
+    w += m;
+    if (b < 32) {
+      s = x;
+      mine = m;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
@@ -213,16 +222,17 @@ __device__ long long total_weight(const RowsAttnArgs& A, int* status) {
 }
 
 // One warp: the item and KV tile at weight w (the end: sequence B).
-__device__ int4 locate(const RowsAttnArgs& A, long long w) {
+__device__ __forceinline__ int4 locate(const RowsAttnArgs& A, long long w, Seq s, long long mine) {
   const int lane = threadIdx.x & 31;
   long long before = 0;
   for (int b0 = 0; b0 < A.B; b0 += 32) {
     const int b = b0 + lane;
-    Seq s{};
-    long long mine = 0;
-    if (b < A.B) {
-      s = load_seq(A, b, nullptr);
-      mine = weight_before(A, s, s.items) * A.Hk;
+    if (b0 > 0) {
+      mine = 0;
+      if (b < A.B) {
+        s = load_seq(A, b, nullptr);
+        mine = weight_before(A, s, s.items) * A.Hk;
+      }
     }
     long long upto = mine;
 #pragma unroll
@@ -333,9 +343,13 @@ __device__ __noinline__ void add_poison(const RowsAttnArgs& A, EdgeRow e, int kv
       const float x = __bfloat162float(v[d]);
       if (isfinite(x)) continue;
       if (out != nullptr) out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
-      else part[d] += x;
+      else part[(d >> 2) * (4 * kRows) + (d & 3)] += x;
     }
   }
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -377,11 +391,20 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     fence_mbar_init();
   }
   if (warp == 8) tmem_alloc(&c->tmem, 512);
+  if (tid == 288) {
+    prefetch_map(&tmQ);
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
   pdl_wait();
   pdl_trigger();
   if (warp < 2) {   // where this block's run begins (warp 0) and ends (warp 1)
-    const long long W = total_weight(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr);
-    const int4 r = locate(A, W * (blockIdx.x + warp) / gridDim.x);
+    Seq s;
+    long long mine;
+    const long long W = total_weight(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr, s, mine);
+    // as many runs as there are blocks, or fewer of at least kMinRun
+    const long long runs = min((long long)gridDim.x, max(1ll, W / kMinRun));
+    const int4 r = locate(A, min(W, W * (blockIdx.x + warp) / runs), s, mine);
     if (lane == 0) c->range[warp] = r;
   }
   if (tid < 2) A.desc[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
@@ -534,14 +557,21 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
         const int which = p.k0 > 0 ? 0 : 1;
         const size_t slot = ((size_t)blockIdx.x * 2 + which) * 2 + h;
-        const size_t row = (size_t)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
+        float* part = A.part + slot * kRows * kD + 4 * r;     // [dims / 4][row][4]
+        const long long row = (long long)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
+        // a row's result lies in one lane: four lanes exchange theirs, so that
+        // a store covers 64 bytes of each of 8 rows and not 16 of 32
+        long long rows4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) rows4[j] = __shfl_sync(0xffffffffu, valid ? row : -1ll, (lane & 28) + j);
+        const float f0 = w0 * inv, f1 = w1 * inv;
 #pragma unroll 1
         for (int q4 = 0; q4 < 4; ++q4) {
           float o[32];
           if (mine) {
             tmem_ld32(tO + 32 * q4, o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = w0 == 0.f ? 0.f : o[j] * w0;
+            for (int j = 0; j < 32; ++j) o[j] = w0 == 0.f ? 0.f : o[j] * f0;
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0.f;
@@ -550,28 +580,43 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             float o1[32];
             tmem_ld32(tO + 128 + 32 * q4, o1);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] += w1 == 0.f ? 0.f : o1[j] * w1;
+            for (int j = 0; j < 32; ++j) o[j] += w1 == 0.f ? 0.f : o1[j] * f1;
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] *= inv;
           if (whole) {
-            if (valid) {
-              uint4* dst = reinterpret_cast<uint4*>(A.out + row * kD + 32 * q4);
+            uint32_t x[4][4];     // pieces of 16 bytes; then row j's piece lane % 4
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                dst[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
-                                    pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+            for (int j = 0; j < 16; ++j) x[j >> 2][j & 3] = pack_bf16(o[2 * j], o[2 * j + 1]);
+#pragma unroll
+            for (int step = 1; step <= 2; step <<= 1) {
+              const bool upper = lane & step;
+#pragma unroll
+              for (int a0 = 0; a0 < 4; ++a0) {
+                if (a0 & step) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[a0][j] : x[a0 + step][j], step);
+                  if (upper) x[a0][j] = got; else x[a0 + step][j] = got;
+                }
+              }
             }
-          } else if (valid) {
-            float4* dst = reinterpret_cast<float4*>(A.part + (slot * kRows + r) * kD + 32 * q4);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j)
+              if (rows4[j] >= 0)
+                reinterpret_cast<uint4*>(A.out + rows4[j] * kD + 32 * q4)[lane & 3] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(part + (8 * q4 + j) * (4 * kRows)) =
+                  make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
-        if (poisoned && valid)
-          add_poison(A, EdgeRow{A.page_table + (size_t)p.b * A.mpp, word, max(p.edge, p.k0 * kRows),
-                                min(p.end, p.k1 * kRows), lim, p.a},
-                     p.kvh, whole ? A.out + row * kD : nullptr, whole ? nullptr : A.part + (slot * kRows + r) * kD);
+        if (poisoned) {
+          __syncwarp();     // the row was stored by its neighbours too
+          if (valid)
+            add_poison(A, EdgeRow{A.page_table + (size_t)p.b * A.mpp, word, max(p.edge, p.k0 * kRows),
+                                  min(p.end, p.k1 * kRows), lim, p.a},
+                       p.kvh, whole ? A.out + row * kD : nullptr, whole ? nullptr : part);
+        }
         if (whole) {
           if (valid && A.lse != nullptr) A.lse[row] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.693147180559945309f;
         } else {
@@ -818,53 +863,84 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   if (warp == 8) tmem_free(tmem, 512);
 }
 
-// Joins the pieces of a cut item, in the order of the cache: a warp a row.
-// Block (c, y) takes rows 8 y on of the item that begins in block c of the
-// attention kernel and does not end there; the others leave at once.
-__global__ void __launch_bounds__(256) rows_merge_kernel(RowsAttnArgs A) {
+// Joins the pieces of a cut item, in the order of the cache.  Block (c, y)
+// takes rows 32 y on of the item that begins in block c of the attention
+// kernel and does not end there (the others leave at once); a warp takes 8
+// rows, four lanes a row.  The weights of all pieces come first, so that the
+// loads of the sums do not wait on one another.
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnArgs A) {
+  __shared__ int s_last;
+  __shared__ float s_w[kMergeWarps][kRowsMaxCtas][8];   // weight of piece i for row j of the warp
   pdl_wait();
   pdl_trigger();
-  const int ctas = gridDim.x, c = blockIdx.x, lane = threadIdx.x & 31;
-  int4 d = A.desc[2 * c + 1];
+  const int ctas = gridDim.x, c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int4 d = A.desc[2 * c + 1];
   if (!(d.w & kDescValid)) return;
   const bool dual = d.w & kDescDual;
-  const int R = blockIdx.y * 8 + (threadIdx.x >> 5), half = R >> 7, r = R & 127;
+  if (dual && (int)blockIdx.y >= kRows / (kMergeWarps * 8)) return;
+  if (tid == 0) s_last = ctas;
+  __syncthreads();
+  for (int i = c + 1 + tid; i < ctas; i += kMergeWarps * 32) {
+    const int4 e = A.desc[2 * i];
+    if ((e.w & kDescValid) && (e.w & kDescLast)) {
+      atomicMin(&s_last, i);
+      break;
+    }
+  }
+  __syncthreads();
+  const int n = min(s_last, ctas - 1) - c + 1;     // pieces: block c's second, then the first of the blocks behind
+  const int R = blockIdx.y * (kMergeWarps * 8) + warp * 8 + (lane & 7), half = R >> 7, r = R & 127, part = lane >> 3;
+  auto slot_of = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * 2 + half; };
+  float M = -INFINITY;
+  for (int i = part; i < n; i += 4) {
+    const bool there = i == 0 || (A.desc[2 * (c + i)].w & kDescValid);
+    const float2 ml = there ? A.part_ml[slot_of(i) * kRows + r] : make_float2(0.f, 0.f);
+    s_w[warp][i][lane & 7] = ml.y == 0.f ? -INFINITY : ml.x;
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+  float l = 0.f;
+  for (int i = part; i < n; i += 4) {
+    const float m = s_w[warp][i][lane & 7];
+    const float w = m == -INFINITY ? 0.f : ex2(m - M);
+    s_w[warp][i][lane & 7] = w;
+    if (w != 0.f) l += w * A.part_ml[slot_of(i) * kRows + r].y;
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+  __syncwarp();
+  float4 o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const float w = s_w[warp][i][lane & 7];
+    if (w == 0.f) continue;
+    const float4* x = reinterpret_cast<const float4*>(A.part) + (slot_of(i) * (kD / 4) + part) * kRows + r;
+    float4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[4 * j * kRows];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      o[j].x = fmaf(v[j].x, w, o[j].x);
+      o[j].y = fmaf(v[j].y, w, o[j].y);
+      o[j].z = fmaf(v[j].z, w, o[j].z);
+      o[j].w = fmaf(v[j].w, w, o[j].w);
+    }
+  }
   const int t_row = r / A.G, g = r - t_row * A.G;
   const Seq s = load_seq(A, d.x, nullptr);
   const int tok = d.z * s.T + half * A.tpt + t_row;    // the row in its sequence
-  if ((dual && half) || t_row >= A.tpt || tok >= s.n) return;
-  float M = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  int cc = c, which = 1;
-  while (true) {
-    const size_t at = (((size_t)cc * 2 + which) * 2 + half) * kRows + r;
-    const float2 ml = A.part_ml[at];
-    if (ml.y != 0.f) {
-      const float4 x = reinterpret_cast<const float4*>(A.part + at * kD)[lane];
-      const float Mn = fmaxf(M, ml.x);
-      const float w0 = l == 0.f ? 0.f : ex2(M - Mn), w1 = ex2(ml.x - Mn);
-      o.x = o.x * w0 + x.x * w1;
-      o.y = o.y * w0 + x.y * w1;
-      o.z = o.z * w0 + x.z * w1;
-      o.w = o.w * w0 + x.w * w1;
-      l = l * w0 + ml.y * w1;
-      M = Mn;
-    }
-    if (d.w & kDescLast) break;
-    which = 0;
-    do {
-      if (++cc >= ctas) break;
-      d = A.desc[2 * cc];
-    } while (!(d.w & kDescValid));
-    if (cc >= ctas) break;
-  }
+  if (t_row >= A.tpt || tok >= s.n) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const size_t row = (size_t)(s.row0 + tok) * A.Hq + (size_t)A.desc[2 * c + 1].y * A.G + g;
-  uint2 w;
-  w.x = pack_bf16(o.x * inv, o.y * inv);
-  w.y = pack_bf16(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(A.out + row * kD)[lane] = w;
-  if (lane == 0 && A.lse != nullptr) A.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
+  const size_t row = (size_t)(s.row0 + tok) * A.Hq + (size_t)d.y * A.G + g;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    reinterpret_cast<uint2*>(A.out + row * kD)[4 * j + part] =
+        make_uint2(pack_bf16(o[j].x * inv, o[j].y * inv), pack_bf16(o[j].z * inv, o[j].w * inv));
+  if (part == 0 && A.lse != nullptr) A.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
 }
 
 }  // namespace
@@ -876,7 +952,7 @@ int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const C
     return SA_ERR_CUDA;
   cudaError_t e = launch_pdl(rows_attention_kernel, dim3(ctas), dim3(kThreads), kSmemBytes, stream, A, tmQ, tmK, tmV);
   if (e != cudaSuccess) return SA_ERR_CUDA;
-  e = launch_pdl(rows_merge_kernel, dim3(ctas, 2 * kRows / 8), dim3(256), 0, stream, A);
+  e = launch_pdl(rows_merge_kernel, dim3(ctas, 2 * kRows / (kMergeWarps * 8)), dim3(kMergeWarps * 32), 0, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

@@ -215,6 +215,7 @@ class Workspace:
             n = max(n, int(lib().sa_rows_workspace_size(prob.ref)))
         self.rows = bool(rows)
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
+        self.device_index = self.buf.get_device()
         _check(lib().sa_workspace_init(_ptr(self.buf), n, _stream()), "sa_workspace_init")
 
     def status(self) -> int:
@@ -506,11 +507,12 @@ class Rope:
         self.axis_pairs, self.layout = [int(x) for x in axis_pairs], layout
         if not 1 <= len(self.axis_pairs) <= MAX_AXES:
             raise ValueError(f"1 to {MAX_AXES} axes, got {len(self.axis_pairs)}")
+        self.pairs = sum(self.axis_pairs)
         self._c = _Rope(layout, len(self.axis_pairs), (ctypes.c_int32 * MAX_AXES)(*self.axis_pairs))
 
     @property
-    def pairs(self) -> int:
-        return sum(self.axis_pairs)
+    def ref(self):
+        return ctypes.byref(self._c)
 
 
 def _need_rows(t: torch.Tensor, name: str, heads: int, n: Optional[int] = None):
@@ -526,22 +528,35 @@ def _need_rows(t: torch.Tensor, name: str, heads: int, n: Optional[int] = None):
     return t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
 
 
-def _need_pools(prob: Problem, k_pool, v_pool):
-    shape = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
-    _need(k_pool, torch.bfloat16, "k_pool", shape)
-    _need(v_pool, torch.bfloat16, "v_pool", shape)
+def _check_rows_args(ws: Workspace, args) -> int:
+    """Tensors (tensor, dtype, shape, name) of a packed-row or page call: type, shape, dense, all on the workspace's
+    device, and that device the current one.  These calls are a few microseconds long, so the checks that pass take
+    the short way; one that does not is repeated by _need for its message.  Returns the current stream."""
+    dev = ws.device_index
+    for t, dtype, shape, name in args:
+        if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
+            _need(t, dtype, name, shape)
+            raise ValueError(f"{name} must be on the workspace's device, got {t.device}")
+    return _rows_stream(ws)
 
 
-def _need_ws(ws: Workspace):
+def _rows_stream(ws: Workspace) -> int:
     if not ws.rows:
         raise ValueError("the workspace must be made with rows=True")
+    if torch.cuda.current_device() != ws.device_index:
+        raise ValueError("the workspace's device must be the current one")
+    return torch.cuda.current_stream().cuda_stream
 
 
-def _one_device(*tensors):
-    """All on one device, and that device the current one."""
-    d = {t.device for t in tensors if t is not None}
-    if len(d) != 1 or next(iter(d)).index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current device, got {sorted(map(str, d))}")
+def _need_tensors(*named):
+    """Tensors on a GPU, before anything is read off them."""
+    for t, name in named:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_out, k_pool, v_pool, ws: Workspace,
@@ -551,54 +566,60 @@ def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_ou
     q_out, keys and values appended to the pages (sa_qk_norm_rope).  q, k, v
     [n][heads][D] may be slices of one projection (any row stride that is a
     multiple of 8).  positions: int32 [axes][n], None: the cache positions."""
-    n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    strides = [_need_rows(q, "q", prob.Hq), _need_rows(k, "k", prob.Hk, n), _need_rows(v, "v", prob.Hk, n)]
-    _need(row_offsets, torch.int32, "row_offsets", (prob.B + 1,))
-    _need(seq_lens, torch.int32, "seq_lens", (prob.B,))
-    _need(page_table, torch.int32, "page_table", (prob.B, prob.max_pages_per_seq))
-    _need(q_out, torch.bfloat16, "q_out", (n, prob.Hq, prob.D))
-    _need_pools(prob, k_pool, v_pool)
-    _need_ws(ws)
-    for t, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, torch.bfloat16, nm, (prob.D,))
+    q_stride = _need_rows(q, "q", prob.Hq)
+    n = q.shape[0]
+    k_stride, v_stride = _need_rows(k, "k", prob.Hk, n), _need_rows(v, "v", prob.Hk, n)
+    pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
+    args = [(row_offsets, torch.int32, (prob.B + 1,), "row_offsets"), (seq_lens, torch.int32, (prob.B,), "seq_lens"),
+            (page_table, torch.int32, (prob.B, prob.max_pages_per_seq), "page_table"),
+            (q_out, torch.bfloat16, (n, prob.Hq, prob.D), "q_out"), (k_pool, torch.bfloat16, pool, "k_pool"),
+            (v_pool, torch.bfloat16, pool, "v_pool")]
+    if q_weight is not None:
+        args.append((q_weight, torch.bfloat16, (prob.D,), "q_weight"))
+    if k_weight is not None:
+        args.append((k_weight, torch.bfloat16, (prob.D,), "k_weight"))
     if rope is not None:
         if inv_freq is None:
             raise ValueError("a rotation needs inv_freq")
-        _need(inv_freq, torch.float32, "inv_freq", (rope.pairs,))
+        args.append((inv_freq, torch.float32, (rope.pairs,), "inv_freq"))
         if positions is not None:
-            _need(positions, torch.int32, "positions", (len(rope.axis_pairs), n))
-    _one_device(q, k, v, row_offsets, seq_lens, page_table, q_out, k_pool, v_pool, q_weight, k_weight, inv_freq,
-                positions, ws.buf)
-    _check(lib().sa_qk_norm_rope(prob.ref, n, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
-                                 _ptr(q_weight), _ptr(k_weight), float(eps),
-                                 None if rope is None else ctypes.byref(rope._c), _ptr(inv_freq), _ptr(positions),
-                                 _ptr(row_offsets), _ptr(seq_lens), _ptr(page_table), _ptr(q_out), _ptr(k_pool),
-                                 _ptr(v_pool), _ptr(ws.buf), _stream()), "sa_qk_norm_rope")
+            args.append((positions, torch.int32, (len(rope.axis_pairs), n), "positions"))
+    else:
+        inv_freq = positions = None
+    _need_tensors(*((t, name) for t, _, _, name in args))
+    stream = _check_rows_args(ws, args)
+    if not q.get_device() == k.get_device() == v.get_device() == ws.device_index:
+        raise ValueError("q, k and v must be on the workspace's device")
+    _check(lib().sa_qk_norm_rope(prob.ref, n, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                                 _p(q_weight), _p(k_weight), eps, None if rope is None else rope.ref, _p(inv_freq),
+                                 _p(positions), row_offsets.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
+                                 q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), ws.buf.data_ptr(), stream),
+           "sa_qk_norm_rope")
 
 
-def _check_attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, *more):
-    n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    _need(q, torch.bfloat16, "q", (n, prob.Hq, prob.D))
-    _need_pools(prob, k_pool, v_pool)
-    _need(page_table, torch.int32, "page_table", (prob.B, prob.max_pages_per_seq))
-    _need(seq_lens, torch.int32, "seq_lens", (prob.B,))
-    _need(row_offsets, torch.int32, "row_offsets", (prob.B + 1,))
-    _need(out, torch.bfloat16, "out", (n, prob.Hq, prob.D))
+def _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse):
+    _need_tensors((q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"), (page_table, "page_table"), (seq_lens, "seq_lens"),
+                  (row_offsets, "row_offsets"), (out, "out"))
+    rows = (q.shape[0] if q.dim() else 0, prob.Hq, prob.D)
+    pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
+    args = [(q, torch.bfloat16, rows, "q"), (k_pool, torch.bfloat16, pool, "k_pool"),
+            (v_pool, torch.bfloat16, pool, "v_pool"),
+            (page_table, torch.int32, (prob.B, prob.max_pages_per_seq), "page_table"),
+            (seq_lens, torch.int32, (prob.B,), "seq_lens"), (row_offsets, torch.int32, (prob.B + 1,), "row_offsets"),
+            (out, torch.bfloat16, rows, "out")]
     if lse is not None:
-        _need(lse, torch.float32, "lse", (n, prob.Hq))
-    _need_ws(ws)
-    _one_device(q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws.buf, *more)
-    return n
+        _need_tensors((lse, "lse"))
+        args.append((lse, torch.float32, rows[:2], "lse"))
+    return args
 
 
 def prompt_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, ws: Workspace, lse=None):
     """Causal attention of packed prompt rows over the paged cache
     (sa_prompt_attention): row i of a sequence's n sees positions 0 .. L - n + i."""
-    n = _check_attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws)
-    _check(lib().sa_prompt_attention(prob.ref, n, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
-                                     _ptr(seq_lens), _ptr(row_offsets), _ptr(out), _ptr(lse), _ptr(ws.buf),
-                                     _stream()), "sa_prompt_attention")
+    stream = _check_rows_args(ws, _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse))
+    _check(lib().sa_prompt_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                     page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
+                                     out.data_ptr(), _p(lse), ws.buf.data_ptr(), stream), "sa_prompt_attention")
 
 
 def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, tree_mask, out, ws: Workspace,
@@ -606,27 +627,31 @@ def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_o
     """Attention of a tree's drafted tokens, a sequence's newest n <= MAX_TREE
     rows, over the cache before them and the drafts whose bits are set in
     tree_mask [n_rows] int64 (sa_tree_attention)."""
-    if isinstance(q, torch.Tensor) and q.dim():
-        _need(tree_mask, torch.int64, "tree_mask", (q.shape[0],))
-    n = _check_attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, tree_mask)
-    _check(lib().sa_tree_attention(prob.ref, n, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(seq_lens),
-                                   _ptr(row_offsets), _ptr(tree_mask), _ptr(out), _ptr(lse), _ptr(ws.buf), _stream()),
+    args = _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse)
+    _need_tensors((tree_mask, "tree_mask"))
+    args.append((tree_mask, torch.int64, (q.shape[0],), "tree_mask"))
+    stream = _check_rows_args(ws, args)
+    _check(lib().sa_tree_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                   page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
+                                   tree_mask.data_ptr(), out.data_ptr(), _p(lse), ws.buf.data_ptr(), stream),
            "sa_tree_attention")
 
 
 def accept_rows(prob: Problem, k_pool, v_pool, page_table, base_lens, path, path_cnt, ws: Workspace):
     """The accepted nodes' K and V rows to the places behind base_lens
     (sa_accept_rows); path [B][max_path], path_cnt [B]."""
-    _need_pools(prob, k_pool, v_pool)
-    _need(page_table, torch.int32, "page_table", (prob.B, prob.max_pages_per_seq))
-    _need(base_lens, torch.int32, "base_lens", (prob.B,))
-    most = path.shape[1] if isinstance(path, torch.Tensor) and path.dim() == 2 else 0
-    _need(path, torch.int32, "path", (prob.B, most))
-    _need(path_cnt, torch.int32, "path_cnt", (prob.B,))
-    _need_ws(ws)
-    _one_device(k_pool, v_pool, page_table, base_lens, path, path_cnt, ws.buf)
-    _check(lib().sa_accept_rows(prob.ref, _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(base_lens), _ptr(path),
-                                most, _ptr(path_cnt), _ptr(ws.buf), _stream()), "sa_accept_rows")
+    _need_tensors((k_pool, "k_pool"), (v_pool, "v_pool"), (page_table, "page_table"), (base_lens, "base_lens"),
+                  (path, "path"), (path_cnt, "path_cnt"))
+    most = path.shape[1] if path.dim() == 2 else 0
+    pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
+    stream = _check_rows_args(ws, (
+        (k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
+        (page_table, torch.int32, (prob.B, prob.max_pages_per_seq), "page_table"),
+        (base_lens, torch.int32, (prob.B,), "base_lens"), (path, torch.int32, (prob.B, most), "path"),
+        (path_cnt, torch.int32, (prob.B,), "path_cnt")))
+    _check(lib().sa_accept_rows(prob.ref, k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(),
+                                base_lens.data_ptr(), path.data_ptr(), most, path_cnt.data_ptr(), ws.buf.data_ptr(),
+                                stream), "sa_accept_rows")
 
 
 def plan_pages(prob: Problem, table_in, parent, keep, lens, table_out, copy_src, copy_dst, counts, ws: Workspace):
@@ -634,44 +659,41 @@ def plan_pages(prob: Problem, table_in, parent, keep, lens, table_out, copy_src,
     first keep[b] tokens and gets room for lens[b] (sa_plan_pages).  The
     copies to make (copy_pages) go to copy_src / copy_dst [B]; counts [2]: their
     number, free pages left."""
-    for t, nm in ((table_in, "table_in"), (table_out, "table_out")):
-        _need(t, torch.int32, nm, (prob.B, prob.max_pages_per_seq))
-    for t, nm in ((parent, "parent"), (keep, "keep"), (lens, "lens"), (copy_src, "copy_src"), (copy_dst, "copy_dst")):
-        _need(t, torch.int32, nm, (prob.B,))
-    _need(counts, torch.int32, "counts", (2,))
-    _need_ws(ws)
-    _one_device(table_in, parent, keep, lens, table_out, copy_src, copy_dst, counts, ws.buf)
-    _check(lib().sa_plan_pages(prob.ref, _ptr(table_in), _ptr(parent), _ptr(keep), _ptr(lens), _ptr(table_out),
-                               _ptr(copy_src), _ptr(copy_dst), _ptr(counts), _ptr(ws.buf), _stream()), "sa_plan_pages")
+    table, rows = (prob.B, prob.max_pages_per_seq), (prob.B,)
+    args = [(table_in, torch.int32, table, "table_in"), (parent, torch.int32, rows, "parent"),
+            (keep, torch.int32, rows, "keep"), (lens, torch.int32, rows, "lens"),
+            (table_out, torch.int32, table, "table_out"), (copy_src, torch.int32, rows, "copy_src"),
+            (copy_dst, torch.int32, rows, "copy_dst"), (counts, torch.int32, (2,), "counts")]
+    _need_tensors(*((t, name) for t, _, _, name in args))
+    stream = _check_rows_args(ws, args)
+    _check(lib().sa_plan_pages(prob.ref, *(t.data_ptr() for t, _, _, _ in args), ws.buf.data_ptr(), stream),
+           "sa_plan_pages")
 
 
 def compact_pages(prob: Problem, table_in, seq_lens, table_out, move_src, move_dst, counts, ws: Workspace):
     """The live pages packed to the front of the pool (sa_compact_pages): the
     new table and the moves to make (copy_pages), move_src / move_dst
     [num_pages]; counts [2]: moves, live pages."""
-    for t, nm in ((table_in, "table_in"), (table_out, "table_out")):
-        _need(t, torch.int32, nm, (prob.B, prob.max_pages_per_seq))
-    _need(seq_lens, torch.int32, "seq_lens", (prob.B,))
-    for t, nm in ((move_src, "move_src"), (move_dst, "move_dst")):
-        _need(t, torch.int32, nm, (prob.num_pages,))
-    _need(counts, torch.int32, "counts", (2,))
-    _need_ws(ws)
-    _one_device(table_in, seq_lens, table_out, move_src, move_dst, counts, ws.buf)
-    _check(lib().sa_compact_pages(prob.ref, _ptr(table_in), _ptr(seq_lens), _ptr(table_out), _ptr(move_src),
-                                  _ptr(move_dst), _ptr(counts), _ptr(ws.buf), _stream()), "sa_compact_pages")
+    table, pages = (prob.B, prob.max_pages_per_seq), (prob.num_pages,)
+    args = [(table_in, torch.int32, table, "table_in"), (seq_lens, torch.int32, (prob.B,), "seq_lens"),
+            (table_out, torch.int32, table, "table_out"), (move_src, torch.int32, pages, "move_src"),
+            (move_dst, torch.int32, pages, "move_dst"), (counts, torch.int32, (2,), "counts")]
+    _need_tensors(*((t, name) for t, _, _, name in args))
+    stream = _check_rows_args(ws, args)
+    _check(lib().sa_compact_pages(prob.ref, *(t.data_ptr() for t, _, _, _ in args), ws.buf.data_ptr(), stream),
+           "sa_compact_pages")
 
 
 def copy_pages(prob: Problem, k_pool, v_pool, src, dst, count, ws: Workspace):
     """Page src[i] to page dst[i] in both pools for i < count[0] (sa_copy_pages);
     count: int32 on the device (the counts of plan_pages or compact_pages)."""
-    _need_pools(prob, k_pool, v_pool)
-    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else 0
-    _need(src, torch.int32, "src", (n,))
-    _need(dst, torch.int32, "dst", (n,))
-    _need(count, torch.int32, "count")
+    _need_tensors((k_pool, "k_pool"), (v_pool, "v_pool"), (src, "src"), (dst, "dst"), (count, "count"))
+    n = src.numel()
     if count.numel() < 1:
         raise ValueError("count must hold a number")
-    _need_ws(ws)
-    _one_device(k_pool, v_pool, src, dst, count, ws.buf)
-    _check(lib().sa_copy_pages(prob.ref, _ptr(k_pool), _ptr(v_pool), _ptr(src), _ptr(dst), _ptr(count), n, _ptr(ws.buf),
-                               _stream()), "sa_copy_pages")
+    pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
+    stream = _check_rows_args(ws, ((k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
+                                   (src, torch.int32, (n,), "src"), (dst, torch.int32, (n,), "dst"),
+                                   (count, torch.int32, tuple(count.shape), "count")))
+    _check(lib().sa_copy_pages(prob.ref, k_pool.data_ptr(), v_pool.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                               count.data_ptr(), n, ws.buf.data_ptr(), stream), "sa_copy_pages")
