@@ -54,8 +54,10 @@ constexpr int kThreads = 384;
 // scores stay in the softmax threads' registers.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
-constexpr int kItemCost = 256;           // an item's fixed cost in KV tokens (query load, epilogue)
-constexpr int kMinRun = 512;             // the least a block is given, in the same measure
+// What work weighs: a KV token of an item with one query tile (two tiles of
+// the cache at once) and with two, an item's query load and epilogue, and the
+// least a block is given.  A tile takes about 1.0 and 1.75 us.
+constexpr int kOneCost = 4, kTwoCost = 7, kItemCost = 1024, kMinRun = 2048;
 constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
@@ -193,11 +195,20 @@ __device__ __forceinline__ int item_edge(const RowsAttnArgs& A, const Seq& s, in
 }
 __device__ __forceinline__ int tiles_of(int end) { return (end + kRows - 1) / kRows; }
 
-// Weight of a KV head's first k items: KV tokens seen (in closed form) and a fixed cost each.
+// Weight of a KV head's first k items, in closed form: KV tokens seen, times
+// what a tile of them takes with one query tile or with two, and a fixed cost
+// each.  All items but a sequence's last have two query tiles.
 __device__ __forceinline__ long long weight_before(const RowsAttnArgs& A, const Seq& s, int k) {
-  if (A.tree != nullptr) return (long long)k * (s.L + kItemCost);
-  const long long cut = k == s.items ? (long long)s.items * s.T - s.n : 0;
-  return (long long)k * (max(s.a, 0) + kItemCost) + (long long)s.T * k * (k + 1) / 2 - cut;
+  if (k == 0) return 0;
+  const int full = min(k, s.items - 1);
+  const long long before = max(A.tree != nullptr ? s.L : s.a, 0);
+  long long w = (before * full + (A.tree != nullptr ? 0 : (long long)s.T * full * (full + 1) / 2)) * kTwoCost +
+                (long long)k * kItemCost;
+  if (k == s.items) {
+    const int tokens = s.n - full * s.T;
+    w += (before + (A.tree != nullptr ? 0 : s.n)) * (tokens <= A.tpt ? kOneCost : kTwoCost);
+  }
+  return w;
 }
 
 // One warp: the total weight of all items.  `s` and `mine` are the lane's own
@@ -222,22 +233,23 @@ __device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* st
 }
 
 // One warp: the item and KV tile at weight w (the end: sequence B).
-__device__ __forceinline__ int4 locate(const RowsAttnArgs& A, long long w, Seq s, long long mine) {
+template <typename T>
+__device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine) {
   const int lane = threadIdx.x & 31;
-  long long before = 0;
+  T before = 0;
   for (int b0 = 0; b0 < A.B; b0 += 32) {
     const int b = b0 + lane;
     if (b0 > 0) {
       mine = 0;
       if (b < A.B) {
         s = load_seq(A, b, nullptr);
-        mine = weight_before(A, s, s.items) * A.Hk;
+        mine = (T)weight_before(A, s, s.items) * A.Hk;
       }
     }
-    long long upto = mine;
+    T upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      const T y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, w < before + upto);
@@ -248,18 +260,18 @@ __device__ __forceinline__ int4 locate(const RowsAttnArgs& A, long long w, Seq s
     const int src = __ffs(hit) - 1;
     int4 r = make_int4(b, 0, 0, 0);
     if (lane == src) {
-      long long rem = w - (before + upto - mine);
-      const long long each = mine / A.Hk;
+      T rem = w - (before + upto - mine);
+      const T each = mine / (T)A.Hk;
       r.y = (int)(rem / each);
       rem -= each * r.y;
       int lo = 0, hi = s.items;     // the item: weight_before(lo) <= rem < weight_before(hi)
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (weight_before(A, s, mid) <= rem) lo = mid; else hi = mid;
+        if ((T)weight_before(A, s, mid) <= rem) lo = mid; else hi = mid;
       }
-      const long long w0 = weight_before(A, s, lo), w1 = weight_before(A, s, lo + 1);
+      const T w0 = (T)weight_before(A, s, lo), w1 = (T)weight_before(A, s, lo + 1);
       r.z = lo;
-      r.w = (int)((rem - w0) * tiles_of(item_end(A, s, lo)) / (w1 - w0));
+      r.w = (int)((unsigned long long)(rem - w0) * tiles_of(item_end(A, s, lo)) / (w1 - w0));
     }
     r.x = __shfl_sync(0xffffffffu, r.x, src);
     r.y = __shfl_sync(0xffffffffu, r.y, src);
@@ -403,8 +415,13 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     long long mine;
     const long long W = total_weight(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr, s, mine);
     // as many runs as there are blocks, or fewer of at least kMinRun
-    const long long runs = min((long long)gridDim.x, max(1ll, W / kMinRun));
-    const int4 r = locate(A, min(W, W * (blockIdx.x + warp) / runs), s, mine);
+    int4 r;
+    if (W < (1ll << 32) / kRowsMaxCtas) {     // in 32 bits, whose divisions are short
+      const uint32_t w = (uint32_t)W, runs = min(gridDim.x, max(1u, w / kMinRun));
+      r = locate<uint32_t>(A, min(w, w * (blockIdx.x + warp) / runs), s, (uint32_t)mine);
+    } else {
+      r = locate<long long>(A, W * (blockIdx.x + warp) / gridDim.x, s, mine);
+    }
     if (lane == 0) c->range[warp] = r;
   }
   if (tid < 2) A.desc[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
@@ -450,9 +467,23 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         ++steps_done;
         tc_fence_after();
         float v[128];
-        tmem_ld128(tS, v);
+        tmem_ld64_start<0>(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
-        if ((kt + 1) * kRows > edge || bad != 0) {
+        const bool masked = (kt + 1) * kRows > edge || bad != 0;
+        tmem_ld64_finish<0>(v);
+        tmem_ld64_start<64>(tS + 64, v);
+        float top[4] = {v[0], v[1], v[2], v[3]};
+        if (!masked) {   // the maximum of the first half while the second is on its way
+#pragma unroll
+          for (int j = 4; j < 60; j += 8) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top[x] = fmaxf(fmaxf(top[x], v[j + x]), v[j + 4 + x]);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], v[60 + x]);
+        }
+        tmem_ld64_finish<64>(v);
+        if (masked) {
           // bit j of see[w]: column 32 w + j
           const int base = kt * kRows;
 #pragma unroll
@@ -469,15 +500,16 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[32 * w + j] = (see >> j) & 1u ? v[32 * w + j] : -INFINITY;
           }
-        }
-        float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int j = 4; j < 124; j += 8) {
+          for (int x = 0; x < 4; ++x) top[x] = v[x];
+#pragma unroll
+          for (int j = 4; j < 64; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+        }
+#pragma unroll
+        for (int j = 64; j < 128; j += 8) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) top[x] = fmaxf(fmaxf(top[x], v[j + x]), v[j + 4 + x]);
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], v[124 + x]);
         float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         mx *= A.scale_log2;
         if (m == -INFINITY) m = mx;   // all zeros so far: nothing to rescale
@@ -565,16 +597,17 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
         for (int j = 0; j < 4; ++j) rows4[j] = __shfl_sync(0xffffffffu, valid ? row : -1ll, (lane & 28) + j);
         const float f0 = w0 * inv, f1 = w1 * inv;
+        // kept short (a loop over 32 columns): it runs once an item, and the
+        // fetch of its instructions costs more than the work
 #pragma unroll 1
         for (int q4 = 0; q4 < 4; ++q4) {
           float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.f;
           if (mine) {
             tmem_ld32(tO + 32 * q4, o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = w0 == 0.f ? 0.f : o[j] * f0;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0.f;
           }
           if (two) {
             float o1[32];
@@ -602,7 +635,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (rows4[j] >= 0)
-                reinterpret_cast<uint4*>(A.out + rows4[j] * kD + 32 * q4)[lane & 3] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+                reinterpret_cast<uint4*>(A.out + rows4[j] * kD + 32 * q4)[lane & 3] =
+                    make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -864,82 +898,104 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 }
 
 // Joins the pieces of a cut item, in the order of the cache.  Block (c, y)
-// takes rows 32 y on of the item that begins in block c of the attention
-// kernel and does not end there (the others leave at once); a warp takes 8
-// rows, four lanes a row.  The weights of all pieces come first, so that the
-// loads of the sums do not wait on one another.
-constexpr int kMergeWarps = 4;
+// takes rows 16 y on of the item that begins in block c of the attention
+// kernel and does not end there (the others leave at once); a warp takes 4
+// rows, eight lanes a row.  Bound by latency: what the pieces are is one look
+// at all of them, and no load waits for another's value after that.
+constexpr int kMergeWarps = 4, kMergeRows = 4 * kMergeWarps, kMergeBatch = 4;
 __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnArgs A) {
   __shared__ int s_last;
-  __shared__ float s_w[kMergeWarps][kRowsMaxCtas][8];   // weight of piece i for row j of the warp
+  __shared__ unsigned s_there[kRowsMaxCtas / 32 + 1];
+  __shared__ float2 s_ml[kMergeWarps][kRowsMaxCtas][4];   // (maximum, sum) of piece i, then (weight, -)
   pdl_wait();
   pdl_trigger();
   const int ctas = gridDim.x, c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int4 d = A.desc[2 * c + 1];
+  int4 e[kRowsMaxCtas / (kMergeWarps * 32) + 1];
+#pragma unroll
+  for (int k = 0; k < kRowsMaxCtas / (kMergeWarps * 32) + 1; ++k) {
+    const int i = c + k * (kMergeWarps * 32) + tid;        // piece i - c
+    e[k] = i < ctas ? A.desc[2 * i + (i == c ? 1 : 0)] : make_int4(0, 0, 0, 0);
+  }
   if (!(d.w & kDescValid)) return;
   const bool dual = d.w & kDescDual;
-  if (dual && (int)blockIdx.y >= kRows / (kMergeWarps * 8)) return;
+  if (dual && (int)blockIdx.y >= kRows / kMergeRows) return;
   if (tid == 0) s_last = ctas;
   __syncthreads();
-  for (int i = c + 1 + tid; i < ctas; i += kMergeWarps * 32) {
-    const int4 e = A.desc[2 * i];
-    if ((e.w & kDescValid) && (e.w & kDescLast)) {
-      atomicMin(&s_last, i);
-      break;
-    }
+#pragma unroll
+  for (int k = 0; k < kRowsMaxCtas / (kMergeWarps * 32) + 1; ++k) {
+    const int i = k * (kMergeWarps * 32) + tid;
+    const bool there = e[k].w & kDescValid;
+    const unsigned m = __ballot_sync(0xffffffffu, there);
+    if (lane == 0 && i / 32 <= kRowsMaxCtas / 32) s_there[i / 32] = m;
+    if (there && (e[k].w & kDescLast) && i > 0) atomicMin(&s_last, c + i);
   }
   __syncthreads();
   const int n = min(s_last, ctas - 1) - c + 1;     // pieces: block c's second, then the first of the blocks behind
-  const int R = blockIdx.y * (kMergeWarps * 8) + warp * 8 + (lane & 7), half = R >> 7, r = R & 127, part = lane >> 3;
-  auto slot_of = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * 2 + half; };
+  const int j4 = lane & 3, part = lane >> 2;
+  const int R = blockIdx.y * kMergeRows + warp * 4 + j4, half = R >> 7, r = R & 127;
+  const float4* sums = reinterpret_cast<const float4*>(A.part) +
+                       ((((size_t)c * 2 + 1) * 2 + half) * (kD / 4) + part) * kRows + r;   // piece 0's
+  auto sums_of = [&](int i) { return sums + (i == 0 ? 0ll : (long long)(4 * i - 2) * (kD / 4) * kRows); };
+  auto there = [&](int i) { return (s_there[i >> 5] >> (i & 31)) & 1u; };
+  float4 v[kMergeBatch][4];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k) {
+      const bool on = i0 + k < n && there(i0 + k);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        v[k][x] = on ? __ldcs(sums_of(i0 + k) + 8 * x * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load(0);
+  const Seq s = load_seq(A, d.x, nullptr);
   float M = -INFINITY;
-  for (int i = part; i < n; i += 4) {
-    const bool there = i == 0 || (A.desc[2 * (c + i)].w & kDescValid);
-    const float2 ml = there ? A.part_ml[slot_of(i) * kRows + r] : make_float2(0.f, 0.f);
-    s_w[warp][i][lane & 7] = ml.y == 0.f ? -INFINITY : ml.x;
+  for (int i = part; i < n; i += 8) {
+    const size_t slot = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * 2 + half;
+    const float2 ml = there(i) ? A.part_ml[slot * kRows + r] : make_float2(0.f, 0.f);
+    s_ml[warp][i][j4] = ml;
     if (ml.y != 0.f) M = fmaxf(M, ml.x);
   }
-  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float l = 0.f;
-  for (int i = part; i < n; i += 4) {
-    const float m = s_w[warp][i][lane & 7];
-    const float w = m == -INFINITY ? 0.f : ex2(m - M);
-    s_w[warp][i][lane & 7] = w;
-    if (w != 0.f) l += w * A.part_ml[slot_of(i) * kRows + r].y;
+  for (int i = part; i < n; i += 8) {
+    const float2 ml = s_ml[warp][i][j4];
+    const float w = ml.y == 0.f ? 0.f : ex2(ml.x - M);
+    s_ml[warp][i][j4].x = w;
+    l += ml.y == 0.f ? 0.f : w * ml.y;
   }
-  l += __shfl_xor_sync(0xffffffffu, l, 8);
-  l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
   __syncwarp();
-  float4 o[8];
+  float4 o[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = 0; i < n; ++i) {
-    const float w = s_w[warp][i][lane & 7];
-    if (w == 0.f) continue;
-    const float4* x = reinterpret_cast<const float4*>(A.part) + (slot_of(i) * (kD / 4) + part) * kRows + r;
-    float4 v[8];
+  for (int x = 0; x < 4; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+    if (i0 > 0) load(i0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = x[4 * j * kRows];
+    for (int k = 0; k < kMergeBatch; ++k) {
+      const float w = i0 + k < n ? s_ml[warp][i0 + k][j4].x : 0.f;
+      if (w == 0.f) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      o[j].x = fmaf(v[j].x, w, o[j].x);
-      o[j].y = fmaf(v[j].y, w, o[j].y);
-      o[j].z = fmaf(v[j].z, w, o[j].z);
-      o[j].w = fmaf(v[j].w, w, o[j].w);
+      for (int x = 0; x < 4; ++x) {
+        o[x].x = fmaf(v[k][x].x, w, o[x].x);
+        o[x].y = fmaf(v[k][x].y, w, o[x].y);
+        o[x].z = fmaf(v[k][x].z, w, o[x].z);
+        o[x].w = fmaf(v[k][x].w, w, o[x].w);
+      }
     }
   }
   const int t_row = r / A.G, g = r - t_row * A.G;
-  const Seq s = load_seq(A, d.x, nullptr);
   const int tok = d.z * s.T + half * A.tpt + t_row;    // the row in its sequence
   if (t_row >= A.tpt || tok >= s.n) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t row = (size_t)(s.row0 + tok) * A.Hq + (size_t)d.y * A.G + g;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    reinterpret_cast<uint2*>(A.out + row * kD)[4 * j + part] =
-        make_uint2(pack_bf16(o[j].x * inv, o[j].y * inv), pack_bf16(o[j].z * inv, o[j].w * inv));
+  for (int x = 0; x < 4; ++x)
+    reinterpret_cast<uint2*>(A.out + row * kD)[8 * x + part] =
+        make_uint2(pack_bf16(o[x].x * inv, o[x].y * inv), pack_bf16(o[x].z * inv, o[x].w * inv));
   if (part == 0 && A.lse != nullptr) A.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
 }
 
@@ -952,7 +1008,7 @@ int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const C
     return SA_ERR_CUDA;
   cudaError_t e = launch_pdl(rows_attention_kernel, dim3(ctas), dim3(kThreads), kSmemBytes, stream, A, tmQ, tmK, tmV);
   if (e != cudaSuccess) return SA_ERR_CUDA;
-  e = launch_pdl(rows_merge_kernel, dim3(ctas, 2 * kRows / (kMergeWarps * 8)), dim3(kMergeWarps * 32), 0, stream, A);
+  e = launch_pdl(rows_merge_kernel, dim3(ctas, 2 * kRows / kMergeRows), dim3(kMergeWarps * 32), 0, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
