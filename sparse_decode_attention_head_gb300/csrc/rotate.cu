@@ -5,10 +5,14 @@
 // the row's place in the paged cache.  Every byte is read and written once:
 // 2 (Hq + 2 Hk) 256 bytes a row, which bounds it.
 //
-// Half a warp takes a row and a run of its heads, 8 dims a lane (one 16-byte
-// load and store a head), four heads in flight; a lane's sines and cosines
-// are the same for all heads of the row and stay in registers.  Where rows
-// are few the heads are spread over more warps.
+// A warp takes a row and a run of its heads, half a warp a head at a time, 8
+// dims a lane.  The heads come through shared memory by bulk copies, 24 heads
+// ahead of the ones at work: what is in flight then costs no registers (held
+// there, four heads a lane, it was 1.4 times as slow).  With s = 1 / sqrt(...), a
+// lane's result is s (x (w cos) + x' (+-w' sin)) with x' its partner's values:
+// the two factors are the same for all query (key) heads of the row and stay
+// in registers, two values an instruction, and the partner's values come as
+// the packed words that were read.
 //
 // The angle: a frequency in turns is a 64-bit fraction F = frac(f / 2 pi) 2^64,
 // computed once a block in fp64, and position x F modulo 2^64 is the exact
@@ -18,154 +22,254 @@
 #include <algorithm>
 
 #include "rows.cuh"
+#include "tcgen.cuh"
 
 namespace sa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kInFlight = 4;    // heads a lane has loaded ahead
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kStage = 24;      // heads of a copy stage, of which a warp has two
 
-// Sequence whose rows hold `row`: the last one that begins at or before it.
-__device__ __forceinline__ int seq_of_row(const int* row_offsets, int B, int row) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(row_offsets + mid) <= row) lo = mid; else hi = mid;
+// Sequence whose rows hold `row`, by a warp together: the last one that begins
+// at or before it (a 32-way search, one look for B <= 32).
+__device__ __forceinline__ int seq_of_row(const int* row_offsets, int B, int row, int lane) {
+  int lo = 0, n = B;             // the answer is in [lo, lo + n)
+  while (true) {
+    const int step = (n + 31) / 32;
+    const bool before = lane * step < n && (lane == 0 || __ldg(row_offsets + lo + lane * step) <= row);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
+    lo += last * step;
+    if (step == 1) return lo;
+    n = min(step, n - last * step);
   }
-  return lo;
 }
 
-__device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
-  x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x);
-  x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-  x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z);
-  x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+__device__ __forceinline__ void unpack(const uint4& w, uint64_t (&x)[4]) {
+  x[0] = pack2(bf16_lo(w.x), bf16_hi(w.x));
+  x[1] = pack2(bf16_lo(w.y), bf16_hi(w.y));
+  x[2] = pack2(bf16_lo(w.z), bf16_hi(w.z));
+  x[3] = pack2(bf16_lo(w.w), bf16_hi(w.w));
 }
 
-__global__ void __launch_bounds__(kThreads)
-rotate_kernel(RotateArgs A, int chunk, int chunks) {
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// HALVES: the pairing (sa_rope.layout), known to the inner loops.
+template <bool HALVES>
+__global__ void __launch_bounds__(kThreads, 2) rotate_kernel(RotateArgs A, int run, int runs) {
+  extern __shared__ __align__(16) uint8_t s_heads[];            // [warp][2][kStage][kD] bf16
   __shared__ unsigned long long s_freq[kD / 2];
-  const int tid = threadIdx.x, lane = tid & 31, hl = lane & 15;
+  __shared__ uint64_t s_full[kWarps][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hl = lane & 15, half = lane >> 4;
+  const int heads = A.Hq + 2 * A.Hk, turned_heads = A.Hq + A.Hk;
+  const long long items = (long long)A.n_rows * runs, stride = (long long)gridDim.x * kWarps;
+  uint8_t* stage[2] = {s_heads + (size_t)(warp * 2) * kStage * kD * 2, s_heads + (size_t)(warp * 2 + 1) * kStage * kD * 2};
+  if (lane < 2) mbar_init(&s_full[warp][lane], 1);
+  fence_mbar_init();
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
+
+  // what is loaded next: heads [lh, lh + kStage) of item li's run
+  long long li = (long long)blockIdx.x * kWarps + warp;
+  int lh = li < items ? (int)(li % runs) * run : 0;
+  uint32_t loads = 0;
+  auto load = [&]() {
+    if (li >= items) return;
+    const int row = (int)(li / runs), end = min(heads, (int)(li % runs) * run + run);
+    const int h1 = min(end, lh + kStage);
+    if (lane == 0) {
+      uint64_t* bar = &s_full[warp][loads & 1];
+      uint8_t* dst = stage[loads & 1];
+      mbar_arrive_expect_tx(bar, (h1 - lh) * kD * 2);
+      for (int h = lh; h < h1;) {      // a copy for each of q, k and v that the stage meets
+        const int e = min(h1, h < A.Hq ? A.Hq : h < turned_heads ? turned_heads : heads);
+        const __nv_bfloat16* src = h < A.Hq           ? A.q + row * A.q_stride + h * kD
+                                   : h < turned_heads ? A.k + row * A.k_stride + (h - A.Hq) * kD
+                                                      : A.v + row * A.v_stride + (h - turned_heads) * kD;
+        bulk_load_1d(dst + (h - lh) * kD * 2, src, (e - h) * kD * 2, bar);
+        h = e;
+      }
+    }
+    ++loads;
+    lh = h1;
+    if (lh == end) {
+      li += stride;
+      lh = li < items ? (int)(li % runs) * run : 0;
+    }
+  };
+  load();
   if (tid < A.pairs) {
     const double turns = (double)A.inv_freq[tid] * 0.15915494309189533577;
     s_freq[tid] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
   }
   __syncthreads();
-  const int heads = A.Hq + 2 * A.Hk;
-  const long long items = (long long)((A.n_rows + 1) / 2) * chunks;
+
   // the partner lane of a rotation of halves, and this lane's part in it
   const int half_lanes = A.pairs / 8;
-  const bool halves = A.layout == SA_ROPE_HALVES;
-  const bool turned = 8 * hl < 2 * A.pairs;
-  const bool second = halves && hl >= half_lanes;
-  const int partner = turned && halves ? (lane & 16) + (second ? hl - half_lanes : hl + half_lanes) : lane;
-  const int npair = halves ? 8 : 4, pair0 = halves ? 8 * (second ? hl - half_lanes : hl) : 4 * hl;
+  const bool turned = 8 * hl < 2 * A.pairs, all_turned = 2 * A.pairs == kD;
+  const bool second = HALVES && hl >= half_lanes;
+  const int partner = turned && HALVES ? (lane & 16) + (second ? hl - half_lanes : hl + half_lanes) : lane;
+  const int pair0 = HALVES ? 8 * (second ? hl - half_lanes : hl) : 4 * hl;
 
-  for (long long item = (long long)blockIdx.x * (kThreads / 32) + (tid >> 5); item < items;
-       item += (long long)gridDim.x * (kThreads / 32)) {
-    const int row = (int)(item / chunks) * 2 + (lane >> 4);
-    const int h0 = (int)(item % chunks) * chunk, h1 = min(heads, h0 + chunk);
-    bool mine = row < A.n_rows, place = false;
-    int pos = 0;
-    size_t slab = 0;              // the row's offset in a pool, without its head
-    if (mine) {
-      const int b = seq_of_row(A.row_offsets, A.B, row);
-      const RowSeq s = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, A.status);
-      mine = row >= s.row0 && row < s.row0 + s.n;
-      pos = s.a + row - s.row0;
-      if (mine && pos >= 0 && pos < A.mpp * kP && h1 > A.Hq) {
-        const int phys = __ldg(A.page_table + (size_t)b * A.mpp + pos / kP);
-        place = phys >= 0 && phys < A.num_pages;
-        if (!place) set_status(A.status, SA_ERR_BAD_PAGE);
-        slab = ((size_t)phys * A.Hk * kP + pos % kP) * kD;
-      }
+  uint32_t used = 0;
+  for (long long item = (long long)blockIdx.x * kWarps + warp; item < items; item += stride) {
+    const int row = (int)(item / runs), h0 = (int)(item % runs) * run, h1 = min(heads, h0 + run);
+    int axis_pos[SA_MAX_AXES] = {0, 0, 0, 0};
+    if (A.positions != nullptr) {
+#pragma unroll
+      for (int a = 0; a < SA_MAX_AXES; ++a)
+        if (a == 0 || A.axis_end[a - 1] < A.pairs) axis_pos[a] = __ldg(A.positions + (size_t)a * A.n_rows + row);
     }
+    const int b = seq_of_row(A.row_offsets, A.B, row, lane);
+    const RowSeq s = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, A.status);
+    const bool mine = row >= s.row0 && row < s.row0 + s.n;
+    const int pos = s.a + row - s.row0;
+    bool place = false;
+    size_t slab = 0;              // the row's offset in a pool, without its head
+    if (mine && pos >= 0 && pos < A.mpp * kP && h1 > A.Hq) {
+      const int phys = __ldg(A.page_table + (size_t)b * A.mpp + pos / kP);
+      place = phys >= 0 && phys < A.num_pages;
+      if (!place) set_status(A.status, SA_ERR_BAD_PAGE);
+      slab = ((size_t)phys * A.Hk * kP + pos % kP) * kD;
+    }
+    // cos and sin of the lane's dims: 8 pairs of halves, or 4 neighbouring pairs
     float cs[8], sn[8];
-    if (h0 < A.Hq + A.Hk) {
+    if (h0 < turned_heads) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         cs[i] = 1.f;
         sn[i] = 0.f;
       }
-      if (mine && turned) {
-        int axis_pos[SA_MAX_AXES];
-#pragma unroll
-        for (int a = 0; a < SA_MAX_AXES; ++a) {
-          const bool used = a == 0 || A.axis_end[a - 1] < A.pairs;
-          axis_pos[a] = A.positions == nullptr ? pos : used ? __ldg(A.positions + (size_t)a * A.n_rows + row) : 0;
-        }
+      if (turned) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (i >= npair) break;
-          const int j = pair0 + i;
-          const int x = j < A.axis_end[0] ? axis_pos[0] : j < A.axis_end[1] ? axis_pos[1] : j < A.axis_end[2] ? axis_pos[2] : axis_pos[3];
-          const unsigned long long turn = (unsigned long long)(long long)x * s_freq[j];
+          if (!HALVES && (i & 1)) {          // the odd dim of a pair
+            cs[i] = cs[i - 1];
+            sn[i] = sn[i - 1];
+            continue;
+          }
+          const int j = pair0 + (HALVES ? i : i >> 1);
+          const int at = A.positions == nullptr ? pos
+                         : j < A.axis_end[0]    ? axis_pos[0]
+                         : j < A.axis_end[1]    ? axis_pos[1]
+                         : j < A.axis_end[2]    ? axis_pos[2]
+                                                : axis_pos[3];
+          const unsigned long long turn = (unsigned long long)(long long)at * s_freq[j];
           sincospif((float)(int)(turn >> 32) * 4.656612873077392578125e-10f, &sn[i], &cs[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (HALVES ? !second : (i & 1) == 0) sn[i] = -sn[i];
       }
     }
-    for (int hb = h0; hb < h1; hb += kInFlight) {
-      uint4 x[kInFlight];
+    uint64_t own_f[4], other_f[4];     // factors of the lane's values and of its partner's
+    int kind = -1;                     // that they are for: 0 queries, 1 keys
+    auto factors = [&](int key, const __nv_bfloat16* wt) {
+      kind = key;
+      float w[8];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int h = hb + u;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (h < h1 && mine) {
-          const __nv_bfloat16* src = h < A.Hq           ? A.q + row * A.q_stride + h * kD
-                                     : h < A.Hq + A.Hk ? A.k + row * A.k_stride + (h - A.Hq) * kD
-                                                       : A.v + row * A.v_stride + (h - A.Hq - A.Hk) * kD;
-          x[u] = reinterpret_cast<const uint4*>(src)[hl];
+      for (int i = 0; i < 8; ++i) w[i] = 1.f;
+      if (wt != nullptr) {
+        const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(wt) + hl);
+        const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = bf16_lo(ww[i]);
+          w[2 * i + 1] = bf16_hi(ww[i]);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int h = hb + u;
-        if (h >= h1) break;
-        uint4 y = x[u];
-        if (h < A.Hq + A.Hk) {
-          const __nv_bfloat16* wt = h < A.Hq ? A.q_weight : A.k_weight;
-          float own[8], scale = 1.f;
-          unpack(x[u], own);
-          uint4 w4 = make_uint4(0, 0, 0, 0);
-          if (wt != nullptr) {
-            float ss = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        // the partner's weights
+        const float w0 = HALVES ? __shfl_sync(0xffffffffu, w[2 * i], partner) : w[2 * i + 1];
+        const float w1 = HALVES ? __shfl_sync(0xffffffffu, w[2 * i + 1], partner) : w[2 * i];
+        own_f[i] = pack2(w[2 * i] * cs[2 * i], w[2 * i + 1] * cs[2 * i + 1]);
+        other_f[i] = pack2(w0 * sn[2 * i], w1 * sn[2 * i + 1]);
+      }
+    };
+    // one head: 8 values of the lane
+    auto turn = [&](uint4 y, bool norm) -> uint4 {
+      uint32_t z[4] = {y.x, y.y, y.z, y.w};      // the partner's values; none where nothing turns
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(own[i], own[i], ss);
+      for (int i = 0; i < 4; ++i) z[i] = HALVES ? __shfl_sync(0xffffffffu, z[i], partner) : __funnelshift_l(z[i], z[i], 16);
+      if (!all_turned) {
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            scale = rsqrtf(ss * (1.f / kD) + A.eps);
-            w4 = __ldg(reinterpret_cast<const uint4*>(wt) + hl);
-            float w[8];
-            unpack(w4, w);
+        for (int i = 0; i < 4; ++i) z[i] = turned ? z[i] : 0u;
+      }
+      uint64_t own[4], other[4];
+      unpack(y, own);
+      unpack(make_uint4(z[0], z[1], z[2], z[3]), other);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) own[i] = own[i] * scale * w[i];
+      for (int i = 0; i < 4; ++i) other[i] = mul2(other[i], other_f[i]);
+      if (norm) {
+        uint64_t s2 = mul2(own[0], own[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) s2 = fma2(own[i], own[i], s2);
+        float sa, sb;
+        unpack2(s2, sa, sb);
+        sa += sb;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        sa = rsqrtf(sa * (1.f / kD) + A.eps);
+        const uint64_t scale = pack2(sa, sa);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[i] = mul2(fma2(own[i], own_f[i], other[i]), scale);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[i] = fma2(own[i], own_f[i], other[i]);
+      }
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2(own[i], lo, hi);
+        r[i] = pack_bf16(lo, hi);
+      }
+      return make_uint4(r[0], r[1], r[2], r[3]);
+    };
+    for (int hs = h0; hs < h1; hs += kStage) {
+      __syncwarp();                    // the stage that is loaded next has been read
+      load();
+      const uint32_t st = used & 1;
+      mbar_wait_bounded(&s_full[warp][st], (used >> 1) & 1, A.status);
+      ++used;
+      const uint4* src = reinterpret_cast<const uint4*>(stage[st]) + hl;      // head hs + i is src[16 i]
+      const int he = min(h1, hs + kStage);
+      // queries, then keys: a head a half-warp, two of them at a time
+#pragma unroll 1
+      for (int key = 0; key < 2; ++key) {
+        const int a = max(hs, key ? A.Hq : 0), e = min(he, key ? turned_heads : A.Hq);
+        if (a >= e) continue;
+        const __nv_bfloat16* wt = key ? A.k_weight : A.q_weight;
+        if (key != kind) factors(key, wt);
+        uint4* dst = key ? reinterpret_cast<uint4*>(A.k_pool + slab) + hl + (ptrdiff_t)(a - A.Hq) * (kP * kD / 8)
+                         : reinterpret_cast<uint4*>(A.q_out + ((size_t)row * A.Hq + a) * kD) + hl;
+        const int step = key ? kP * kD / 8 : kD / 8;      // between heads, in 16-byte pieces
+        const bool write = key ? place : mine;
+        const uint4* from = src + (a - hs) * 16;
+        int h = half;
+        const int n = e - a;
+#pragma unroll 1
+        for (; h - half + 4 <= n; h += 4) {
+          const uint4 y0 = turn(from[16 * h], wt != nullptr), y1 = turn(from[16 * h + 32], wt != nullptr);
+          if (write) {
+            dst[(ptrdiff_t)h * step] = y0;
+            dst[(ptrdiff_t)(h + 2) * step] = y1;
           }
-          if (halves) {
-            float other[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, own[i], partner);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) own[i] = own[i] * cs[i] + (second ? other[i] : -other[i]) * sn[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = own[2 * i], b = own[2 * i + 1];
-              own[2 * i] = a * cs[i] - b * sn[i];
-              own[2 * i + 1] = b * cs[i] + a * sn[i];
-            }
-          }
-          y = make_uint4(pack_bf16(own[0], own[1]), pack_bf16(own[2], own[3]), pack_bf16(own[4], own[5]),
-                         pack_bf16(own[6], own[7]));
         }
-        if (h < A.Hq) {
-          if (mine) reinterpret_cast<uint4*>(A.q_out + ((size_t)row * A.Hq + h) * kD)[hl] = y;
-        } else if (place) {
-          const bool key = h < A.Hq + A.Hk;
-          const int kvh = h - A.Hq - (key ? 0 : A.Hk);
-          reinterpret_cast<uint4*>((key ? A.k_pool : A.v_pool) + slab + (size_t)kvh * kP * kD)[hl] = y;
+        for (; h - half < n; h += 2) {
+          const uint4 y = turn(h < n ? from[16 * h] : make_uint4(0, 0, 0, 0), wt != nullptr);
+          if (write && h < n) dst[(ptrdiff_t)h * step] = y;
         }
+      }
+      if (place) {      // values as they are
+        uint4* dst = reinterpret_cast<uint4*>(A.v_pool + slab) + hl;
+        for (int h = max(hs, turned_heads) + half; h < he; h += 2)
+          dst[(ptrdiff_t)(h - turned_heads) * (kP * kD / 8)] = src[(h - hs) * 16];
       }
     }
   }
@@ -174,17 +278,28 @@ rotate_kernel(RotateArgs A, int chunk, int chunks) {
 }  // namespace
 
 int launch_rotate(const RotateArgs& A, int num_sms, cudaStream_t stream) {
+  constexpr size_t smem = (size_t)kWarps * 2 * kStage * kD * 2;
+  const auto kern = A.layout == SA_ROPE_HALVES ? rotate_kernel<true> : rotate_kernel<false>;
+  const void* kernel = reinterpret_cast<const void*>(kern);
+  if (smem_limit_at_least(kernel, (int)smem) != cudaSuccess) return SA_ERR_CUDA;
   const int heads = A.Hq + 2 * A.Hk;
-  const long long pairs = (A.n_rows + 1) / 2;
-  // heads of a warp's run: all of them once the rows alone fill the device
-  // (a row's sines are then computed once), else as few as fill it
-  int chunk = heads;
-  while (chunk > kInFlight && pairs * ((heads + chunk - 1) / chunk) < (long long)num_sms * 16) chunk = (chunk + 1) / 2;
-  chunk = std::max(kInFlight, (chunk + kInFlight - 1) / kInFlight * kInFlight);
-  const int chunks = (heads + chunk - 1) / chunk;
-  const long long blocks = (pairs * chunks + kThreads / 32 - 1) / (kThreads / 32);
-  const int grid = (int)std::min<long long>(blocks, (long long)num_sms * 8);
-  const cudaError_t e = launch_pdl(rotate_kernel, dim3(grid), dim3(kThreads), 0, stream, A, chunk, chunks);
+  const int blocks_per_sm = ctas_per_sm(kernel, kThreads, smem);
+  const long long warps = (long long)num_sms * blocks_per_sm * kWarps;
+  // heads of a warp's run: all of them (a row's sines are then computed once),
+  // unless that leaves the last round of warps mostly idle: with few rows, or
+  // a little more than one round, the heads are spread over more warps
+  int runs = 1, run = heads;
+  for (int r = 1; r <= (heads + 3) / 4; ++r) {
+    const int each = ((heads + r - 1) / r + 3) / 4 * 4;
+    const long long items = (long long)A.n_rows * r, rounds = (items + warps - 1) / warps;
+    runs = r;
+    run = each;
+    if (items * 5 >= rounds * warps * 4) break;
+  }
+  runs = (heads + run - 1) / run;
+  const long long blocks = ((long long)A.n_rows * runs + kWarps - 1) / kWarps;
+  const int grid = (int)std::min<long long>(blocks, (long long)num_sms * blocks_per_sm);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, A, run, runs);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

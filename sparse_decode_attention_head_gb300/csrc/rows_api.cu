@@ -61,34 +61,6 @@ PageLayout page_layout(const Params& p) {
   return l;
 }
 
-// The last few maps that a host thread encoded, by address, shape and device: a
-// call needs three, and encoding is host work worth skipping in a loop that
-// keeps its buffers.  A map holds nothing but the address and the shape.
-template <typename Encode>
-int cached_map(CUtensorMap* m, const void* base, long long a, long long b, long long c, Encode encode) {
-  struct Entry {
-    const void* base;
-    long long a, b, c;
-    int dev;
-    CUtensorMap map;
-  };
-  thread_local Entry cache[12] = {};
-  thread_local int next = 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
-  for (const Entry& e : cache)
-    if (e.base == base && e.a == a && e.b == b && e.c == c && e.dev == dev) {
-      *m = e.map;
-      return SA_OK;
-    }
-  const int rc = encode(m);
-  if (rc == SA_OK) {
-    cache[next] = Entry{base, a, b, c, dev, *m};
-    next = (next + 1) % 12;
-  }
-  return rc;
-}
-
 // q [n_rows][Hq][D] as boxes of 64 dims x G heads x 128 / G tokens.
 int make_q_map(CUtensorMap* m, const void* q, int n_rows, const Params& p, int tpt) {
   auto fn = sa_host::encode_fn();
@@ -137,14 +109,9 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
   sa::RowsAttnArgs A{};
   A.tpt = 128 / p.G;
   CUtensorMap tmQ, tmK, tmV;
-  rc = cached_map(&tmQ, q, n_rows, p.Hq, p.G, [&](CUtensorMap* m) { return make_q_map(m, q, n_rows, p, A.tpt); });
-  if (rc != SA_OK) return rc;
-  for (int kv = 0; kv < 2; ++kv) {
-    const void* pool = kv == 0 ? k_pool : v_pool;
-    rc = cached_map(kv == 0 ? &tmK : &tmV, pool, p.num_pages, p.Hk, -1,
-                    [&](CUtensorMap* m) { return make_tile_map(m, pool, p); });
-    if (rc != SA_OK) return rc;
-  }
+  if ((rc = make_q_map(&tmQ, q, n_rows, p, A.tpt)) != SA_OK) return rc;
+  if ((rc = make_tile_map(&tmK, k_pool, p)) != SA_OK) return rc;
+  if ((rc = make_tile_map(&tmV, v_pool, p)) != SA_OK) return rc;
   const AttnLayout l = attn_layout();
   A.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
   A.page_table = page_table;

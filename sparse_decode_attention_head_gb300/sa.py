@@ -515,44 +515,47 @@ class Rope:
         return ctypes.byref(self._c)
 
 
-def _need_rows(t: torch.Tensor, name: str, heads: int, n: Optional[int] = None):
-    """Packed rows [n][heads][D] bf16, dense within a row; returns the row stride."""
+def _row_stride(t, name: str, heads: int, n: int, dev) -> int:
+    """Packed rows [n][heads][D] bf16, dense within a row, any distance between rows: that distance."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1:] != (heads, HEAD_DIM) or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must have shape ({'n' if n is None else n}, {heads}, {HEAD_DIM}), got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM)):
+    if t.shape != (n, heads, HEAD_DIM):
+        raise ValueError(f"{name} must have shape {(n, heads, HEAD_DIM)}, got {tuple(t.shape)}")
+    row, head, dim = t.stride()
+    if (dim != 1 or (head != HEAD_DIM and heads > 1)) and n > 0:
         raise ValueError(f"{name} must be dense within a row")
-    return t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the workspace's device, got {t.device}")
+    return row if n > 1 else heads * HEAD_DIM
 
 
 def _check_rows_args(ws: Workspace, args) -> int:
     """Tensors (tensor, dtype, shape, name) of a packed-row or page call: type, shape, dense, all on the workspace's
     device, and that device the current one.  These calls are a few microseconds long, so the checks that pass take
     the short way; one that does not is repeated by _need for its message.  Returns the current stream."""
-    dev = ws.device_index
+    dev = getattr(ws, "device_index", None)
     for t, dtype, shape, name in args:
-        if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
-            _need(t, dtype, name, shape)
-            raise ValueError(f"{name} must be on the workspace's device, got {t.device}")
-    return _rows_stream(ws)
-
-
-def _rows_stream(ws: Workspace) -> int:
+        try:
+            if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+                continue
+        except AttributeError:
+            pass
+        _need(t, dtype, name, shape)
+        raise ValueError(f"{name} must be on the workspace's device, got {t.device}")
     if not ws.rows:
         raise ValueError("the workspace must be made with rows=True")
-    if torch.cuda.current_device() != ws.device_index:
+    if torch.cuda.current_device() != dev:
         raise ValueError("the workspace's device must be the current one")
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _need_tensors(*named):
-    """Tensors on a GPU, before anything is read off them."""
-    for t, name in named:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
+def _rows_of(t, name: str) -> int:
+    """Rows of a packed tensor whose shape is checked later."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.shape[0] if t.dim() else 0
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -566,9 +569,9 @@ def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_ou
     q_out, keys and values appended to the pages (sa_qk_norm_rope).  q, k, v
     [n][heads][D] may be slices of one projection (any row stride that is a
     multiple of 8).  positions: int32 [axes][n], None: the cache positions."""
-    q_stride = _need_rows(q, "q", prob.Hq)
-    n = q.shape[0]
-    k_stride, v_stride = _need_rows(k, "k", prob.Hk, n), _need_rows(v, "v", prob.Hk, n)
+    n, dev = _rows_of(q, "q"), getattr(ws, "device_index", None)
+    q_stride = _row_stride(q, "q", prob.Hq, n, dev)
+    k_stride, v_stride = _row_stride(k, "k", prob.Hk, n, dev), _row_stride(v, "v", prob.Hk, n, dev)
     pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
     args = [(row_offsets, torch.int32, (prob.B + 1,), "row_offsets"), (seq_lens, torch.int32, (prob.B,), "seq_lens"),
             (page_table, torch.int32, (prob.B, prob.max_pages_per_seq), "page_table"),
@@ -586,10 +589,7 @@ def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_ou
             args.append((positions, torch.int32, (len(rope.axis_pairs), n), "positions"))
     else:
         inv_freq = positions = None
-    _need_tensors(*((t, name) for t, _, _, name in args))
     stream = _check_rows_args(ws, args)
-    if not q.get_device() == k.get_device() == v.get_device() == ws.device_index:
-        raise ValueError("q, k and v must be on the workspace's device")
     _check(lib().sa_qk_norm_rope(prob.ref, n, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
                                  _p(q_weight), _p(k_weight), eps, None if rope is None else rope.ref, _p(inv_freq),
                                  _p(positions), row_offsets.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
@@ -598,9 +598,7 @@ def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_ou
 
 
 def _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse):
-    _need_tensors((q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"), (page_table, "page_table"), (seq_lens, "seq_lens"),
-                  (row_offsets, "row_offsets"), (out, "out"))
-    rows = (q.shape[0] if q.dim() else 0, prob.Hq, prob.D)
+    rows = (_rows_of(q, "q"), prob.Hq, prob.D)
     pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
     args = [(q, torch.bfloat16, rows, "q"), (k_pool, torch.bfloat16, pool, "k_pool"),
             (v_pool, torch.bfloat16, pool, "v_pool"),
@@ -608,7 +606,6 @@ def _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, 
             (seq_lens, torch.int32, (prob.B,), "seq_lens"), (row_offsets, torch.int32, (prob.B + 1,), "row_offsets"),
             (out, torch.bfloat16, rows, "out")]
     if lse is not None:
-        _need_tensors((lse, "lse"))
         args.append((lse, torch.float32, rows[:2], "lse"))
     return args
 
@@ -628,7 +625,6 @@ def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_o
     rows, over the cache before them and the drafts whose bits are set in
     tree_mask [n_rows] int64 (sa_tree_attention)."""
     args = _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse)
-    _need_tensors((tree_mask, "tree_mask"))
     args.append((tree_mask, torch.int64, (q.shape[0],), "tree_mask"))
     stream = _check_rows_args(ws, args)
     _check(lib().sa_tree_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
@@ -640,9 +636,7 @@ def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_o
 def accept_rows(prob: Problem, k_pool, v_pool, page_table, base_lens, path, path_cnt, ws: Workspace):
     """The accepted nodes' K and V rows to the places behind base_lens
     (sa_accept_rows); path [B][max_path], path_cnt [B]."""
-    _need_tensors((k_pool, "k_pool"), (v_pool, "v_pool"), (page_table, "page_table"), (base_lens, "base_lens"),
-                  (path, "path"), (path_cnt, "path_cnt"))
-    most = path.shape[1] if path.dim() == 2 else 0
+    most = path.shape[1] if _rows_of(path, "path") and path.dim() == 2 else 0
     pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
     stream = _check_rows_args(ws, (
         (k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
@@ -664,7 +658,6 @@ def plan_pages(prob: Problem, table_in, parent, keep, lens, table_out, copy_src,
             (keep, torch.int32, rows, "keep"), (lens, torch.int32, rows, "lens"),
             (table_out, torch.int32, table, "table_out"), (copy_src, torch.int32, rows, "copy_src"),
             (copy_dst, torch.int32, rows, "copy_dst"), (counts, torch.int32, (2,), "counts")]
-    _need_tensors(*((t, name) for t, _, _, name in args))
     stream = _check_rows_args(ws, args)
     _check(lib().sa_plan_pages(prob.ref, *(t.data_ptr() for t, _, _, _ in args), ws.buf.data_ptr(), stream),
            "sa_plan_pages")
@@ -678,7 +671,6 @@ def compact_pages(prob: Problem, table_in, seq_lens, table_out, move_src, move_d
     args = [(table_in, torch.int32, table, "table_in"), (seq_lens, torch.int32, (prob.B,), "seq_lens"),
             (table_out, torch.int32, table, "table_out"), (move_src, torch.int32, pages, "move_src"),
             (move_dst, torch.int32, pages, "move_dst"), (counts, torch.int32, (2,), "counts")]
-    _need_tensors(*((t, name) for t, _, _, name in args))
     stream = _check_rows_args(ws, args)
     _check(lib().sa_compact_pages(prob.ref, *(t.data_ptr() for t, _, _, _ in args), ws.buf.data_ptr(), stream),
            "sa_compact_pages")
@@ -687,9 +679,8 @@ def compact_pages(prob: Problem, table_in, seq_lens, table_out, move_src, move_d
 def copy_pages(prob: Problem, k_pool, v_pool, src, dst, count, ws: Workspace):
     """Page src[i] to page dst[i] in both pools for i < count[0] (sa_copy_pages);
     count: int32 on the device (the counts of plan_pages or compact_pages)."""
-    _need_tensors((k_pool, "k_pool"), (v_pool, "v_pool"), (src, "src"), (dst, "dst"), (count, "count"))
-    n = src.numel()
-    if count.numel() < 1:
+    n = _rows_of(src, "src")
+    if _rows_of(count, "count") < 1:
         raise ValueError("count must hold a number")
     pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
     stream = _check_rows_args(ws, ((k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
