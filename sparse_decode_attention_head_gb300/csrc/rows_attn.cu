@@ -696,75 +696,96 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
       if (k0 < 0) break;
       if (ntp == 0) continue;
-      const int N = dual ? ntp : 2 * ntp;
       if (!(ok = wait_warp(&c->q_full, pieces & 1, c, A.status))) break;
       ++pieces;
-      // S of half h from the tile at kr; `last` of the tile's, of the piece's
-      auto issue_s = [&](int h, bool first_of_tile, bool last_of_tile, bool last) -> bool {
-        if (first_of_tile && !wait_warp(&c->full[kr.slot], kr.parity, c, A.status)) return false;
+      auto mma_s = [&](int h) {      // S of group h from the tile at kr
         const uint64_t q = dQ + (dual ? 0 : h * (kTileBytes / 16)), k = dK + kr.slot * (kTileBytes / 16);
         const uint32_t d = tmem + h * 128;
-        if (elect_one()) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2, k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS,
-                      x != 0);
-          tc_commit(&c->s_full[h]);
-          if (last_of_tile) tc_commit(&c->empty[kr.slot]);
-          if (last) tc_commit(&c->q_empty);
-        }
-        __syncwarp();
-        if (last_of_tile) kr.advance(2);
-        return true;
+        for (int x = 0; x < 8; ++x)
+          tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2, k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS,
+                    x != 0);
       };
-      // O of half h from the tile at vr
-      auto issue_o = [&](int h, int kt, bool first_of_tile, bool last_of_tile, bool first, bool last) -> bool {
-        if (first_of_tile) {
-          if (!wait_warp(&c->full[vr.slot], vr.parity, c, A.status)) return false;
-          if ((kt + 1) * kRows > edge) {
-            if (!wait_warp(&c->clean[vr.slot], (cleaned >> vr.slot) & 1, c, A.status)) return false;
-            cleaned ^= 1u << vr.slot;
-          }
-        }
+      // O of group h from the tile at vr: the tokens of one half of the weights
+      auto mma_o = [&](int h, int part, bool first) {
         const uint64_t v = dV + vr.slot * (kTileBytes / 16);
         const uint32_t d = tmem + 256 + h * 128, w = tmem + h * 128;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (!wait_warp(&c->p_full[h][part], p_par[h], c, A.status)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int x = 4 * part; x < 4 * part + 4; ++x)
-              tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
-            if (part == 1) {
-              if (last_of_tile) tc_commit(&c->empty[vr.slot]);
-              if (last) tc_commit(&c->o_done[h]);
-            }
-          }
+        for (int x = 4 * part; x < 4 * part + 4; ++x) tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
+      };
+      auto issue_s = [&](int h, bool k_done, bool q_done) {
+        mma_s(h);
+        tc_commit(&c->s_full[h]);
+        if (k_done) tc_commit(&c->empty[kr.slot]);
+        if (q_done) tc_commit(&c->q_empty);
+      };
+      auto wait_k = [&]() -> bool { return wait_warp(&c->full[kr.slot], kr.parity, c, A.status); };
+      // A step of group h: O from the tile at vr, then S from the tile at kr
+      // (`more`: there is one).  What is there already is seen by one look
+      // before, so that nothing stands between the instructions then; a K
+      // tile that is late is waited for behind O, whose V slot comes free.
+      // k_done, v_done: the tile has no other reader; q_done: nor has Q.
+      auto step = [&](int h, bool first, bool more, bool k_done, bool v_done, bool q_done) -> bool {
+        const bool k_there = more && __all_sync(0xffffffffu, mbar_test_wait(&c->full[kr.slot], kr.parity));
+        const bool late = !__all_sync(0xffffffffu, mbar_test_wait(&c->p_full[h][1], p_par[h]));
+        if (late && !wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;
+        tc_fence_after();
+        if (elect_one()) mma_o(h, 0, first);
+        __syncwarp();
+        if (late && !wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
+        if (late) tc_fence_after();
+        if (elect_one()) {
+          mma_o(h, 1, first);
+          if (v_done) tc_commit(&c->empty[vr.slot]);
+          if (!more) tc_commit(&c->o_done[h]);
+          if (k_there) issue_s(h, k_done, q_done);
+        }
+        __syncwarp();
+        if (more && !k_there) {
+          if (!wait_k()) return false;
+          if (elect_one()) issue_s(h, k_done, q_done);
           __syncwarp();
         }
         p_par[h] ^= 1;
-        if (last_of_tile) vr.advance(2);
+        if (v_done) vr.advance(2);
+        if (more && k_done) kr.advance(2);
         return true;
       };
-      if (dual) {
-        if (!(ok = issue_s(0, true, true, N == 1))) break;
-        if (N > 1 && !(ok = issue_s(1, true, true, N == 2))) break;
-#pragma unroll 1
-        for (int s = 0; s < N; ++s) {
-          if (!(ok = issue_o(s & 1, k0 + s, true, true, s < 2, s + 2 >= N))) break;
-          if (s + 2 < N && !(ok = issue_s(s & 1, true, true, s + 3 == N))) break;
+      auto wait_v = [&](int kt) -> bool {
+        if (!wait_warp(&c->full[vr.slot], vr.parity, c, A.status)) return false;
+        if ((kt + 1) * kRows > edge) {
+          if (!wait_warp(&c->clean[vr.slot], (cleaned >> vr.slot) & 1, c, A.status)) return false;
+          cleaned ^= 1u << vr.slot;
         }
-      } else {
-        if (!(ok = issue_s(0, true, false, false))) break;
-        if (!(ok = issue_s(1, false, true, ntp == 1))) break;
+        return true;
+      };
+      auto first_s = [&](int h, bool k_done, bool q_done) {
+        if (elect_one()) issue_s(h, k_done, q_done);
+        __syncwarp();
+        if (k_done) kr.advance(2);
+      };
+      if (!(ok = wait_k())) break;
+      if (dual) {      // a tile a step, the groups in turn
+        first_s(0, true, ntp == 1);
+        if (ntp > 1) {
+          if (!(ok = wait_k())) break;
+          first_s(1, true, ntp == 2);
+        }
+#pragma unroll 1
+        for (int s = 0; s < ntp; ++s) {
+          const bool more = s + 2 < ntp;
+          if (!(ok = wait_v(k0 + s))) break;
+          if (!(ok = step(s & 1, s < 2, more, true, true, s + 3 == ntp))) break;
+        }
+      } else {         // a tile two steps
+        first_s(0, false, false);
+        first_s(1, true, ntp == 1);
 #pragma unroll 1
         for (int t = 0; t < ntp; ++t) {
-          const bool first = t == 0, last = t == ntp - 1;
-          if (!(ok = issue_o(0, k0 + t, true, false, first, last))) break;
-          if (!last && !(ok = issue_s(0, true, false, false))) break;
-          if (!(ok = issue_o(1, k0 + t, false, true, first, last))) break;
-          if (!last && !(ok = issue_s(1, false, true, t + 2 == ntp))) break;
+          const bool first = t == 0, more = t + 1 < ntp;
+          if (!(ok = wait_v(k0 + t))) break;
+          if (!(ok = step(0, first, more, false, false, false))) break;
+          if (!(ok = step(1, first, more, true, true, t + 2 == ntp))) break;
         }
       }
       if (!ok) break;
