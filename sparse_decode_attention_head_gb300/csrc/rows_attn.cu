@@ -54,10 +54,10 @@ constexpr int kThreads = 384;
 // scores stay in the softmax threads' registers.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
-// What work weighs: a KV token of an item with one query tile (two tiles of
-// the cache at once) and with two, an item's query load and epilogue, and the
-// least a block is given.  A tile takes about 1.0 and 1.75 us.
-constexpr int kOneCost = 4, kTwoCost = 7, kItemCost = 1024, kMinRun = 2048;
+// What work weighs: a KV token of an item with one query tile (bound by the
+// loads: measured 1.45 us a tile of them) and with two (1.6 us), an item's
+// query load, first tile and epilogue (4.4 us), and the least a block is given.
+constexpr int kOneCost = 6, kTwoCost = 7, kItemCost = 2500, kMinRun = 2048;
 constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
