@@ -12,7 +12,8 @@
 // are laid end to end, weighted by the KV tokens they see, and cut into one
 // equal run for each block (one block an SM, persistent): many rows give
 // whole items, few rows over a long cache split an item's KV range over
-// blocks.  A cut item leaves (maximum, sum, unnormalised output) for each
+// blocks.  Where there are fewer items than blocks a block takes no more than
+// one (17 us in place of 21 for four prompts of at most 200 rows).  A cut item leaves (maximum, sum, unnormalised output) for each
 // row, and the merge kernel joins the pieces in order with the log-sum-exp
 // identity; blocks never wait on one another and nothing is added atomically,
 // so results do not depend on timing.
@@ -55,9 +56,9 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
 // What work weighs: a KV token of an item with one query tile (bound by the
-// loads: measured 1.45 us a tile of them) and with two (1.6 us), an item's
-// query load, first tile and epilogue (4.4 us), and the least a block is given.
-constexpr int kOneCost = 6, kTwoCost = 7, kItemCost = 2500, kMinRun = 2048;
+// loads: measured 1.45 us a tile of them) and with two (1.6 us), and an item's
+// query load, first tile and epilogue (4.4 us).
+constexpr int kOneCost = 6, kTwoCost = 7, kItemCost = 2500;
 constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
@@ -282,6 +283,55 @@ __device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine
   return make_int4(A.B, 0, 0, 0);
 }
 
+// Little work: every block takes one item or an equal part of one, of two KV
+// tiles or four, and none takes two.  `s` as above (B <= 32).  Answers false
+// where the blocks do not suffice for that.
+__device__ __forceinline__ int runs_of(const RowsAttnArgs& A, const Seq& s, int i, int tiles) {
+  return max(1, (tiles_of(item_end(A, s, i)) + tiles - 1) / tiles);
+}
+__device__ __forceinline__ bool locate_small(const RowsAttnArgs& A, int run, int blocks, const Seq& s, int4& r) {
+  const int lane = threadIdx.x & 31;
+  if (A.B > 32) return false;
+  auto sum = [](int x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  const int some = s.items > blocks ? blocks + 1 : s.items;
+  if ((long long)sum(some) * A.Hk > blocks) return false;
+  int tiles = 2, mine;
+  while (true) {
+    mine = 0;
+    for (int i = 0; i < s.items; ++i) mine += min(runs_of(A, s, i, tiles), blocks + 1);
+    mine = min(mine, blocks + 1) * A.Hk;
+    if (sum(mine) <= blocks) break;
+    if (tiles == 4) return false;
+    tiles = 4;
+  }
+  r = make_int4(A.B, 0, 0, 0);
+  const int upto = warp_incl_scan(mine);
+  const unsigned hit = __ballot_sync(0xffffffffu, run < upto);
+  if (hit == 0) return true;
+  const int src = __ffs(hit) - 1;
+  if (lane == src) {
+    int rem = run - (upto - mine);
+    const int each = mine / A.Hk;
+    r = make_int4(lane, rem / each, 0, 0);
+    rem -= each * r.y;
+    int n = runs_of(A, s, 0, tiles);
+    while (rem >= n) {
+      rem -= n;
+      n = runs_of(A, s, ++r.z, tiles);
+    }
+    r.w = rem * tiles_of(item_end(A, s, r.z)) / n;
+  }
+  r.x = __shfl_sync(0xffffffffu, r.x, src);
+  r.y = __shfl_sync(0xffffffffu, r.y, src);
+  r.z = __shfl_sync(0xffffffffu, r.z, src);
+  r.w = __shfl_sync(0xffffffffu, r.w, src);
+  return true;
+}
+
 // One thread walks a block's run, piece by piece.
 struct Walk {
   const RowsAttnArgs& A;
@@ -414,11 +464,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     Seq s;
     long long mine;
     const long long W = total_weight(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr, s, mine);
-    // as many runs as there are blocks, or fewer of at least kMinRun
     int4 r;
-    if (W < (1ll << 32) / kRowsMaxCtas) {     // in 32 bits, whose divisions are short
-      const uint32_t w = (uint32_t)W, runs = min(gridDim.x, max(1u, w / kMinRun));
-      r = locate<uint32_t>(A, min(w, w * (blockIdx.x + warp) / runs), s, (uint32_t)mine);
+    if (locate_small(A, blockIdx.x + warp, gridDim.x, s, r)) {
+    } else if (W < (1ll << 32) / kRowsMaxCtas) {     // in 32 bits, whose divisions are short
+      r = locate<uint32_t>(A, (uint32_t)W * (blockIdx.x + warp) / gridDim.x, s, (uint32_t)mine);
     } else {
       r = locate<long long>(A, W * (blockIdx.x + warp) / gridDim.x, s, mine);
     }
