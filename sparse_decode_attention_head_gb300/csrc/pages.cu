@@ -5,10 +5,11 @@
 // counts, so the order of the atomics leaves no trace); there is no state of
 // its own that could disagree with it.  Ranks of free, live and moved pages
 // come from a count of each chunk of 1024 pages and a sum over the chunks
-// before; four small launches, each waiting for the one before through
-// dependent launch, so a call is bound by their latency.  The copies are
-// bound by HBM: a page is read and written once, a warp moving a 4 KB slab
-// (one head of one page) with eight 16-byte loads a lane in flight.
+// before.  The steps hang on one another, so the whole of it runs in one
+// cluster of 8 blocks with a cluster barrier between them: bound by latency
+// (as five launches a table of 64 rows took 14 us).  The copies are bound by
+// HBM: a page is read and written once, a warp moving a 4 KB slab (one head
+// of one page) with eight 16-byte loads a lane in flight.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -56,27 +57,12 @@ __device__ __forceinline__ PlanRow plan_row(const PageArgs& A, int b, int* statu
   return r;
 }
 
-// Holders of every page; for a plan also the rows that will write inside it
-// and the lowest of them.
-template <bool PLAN>
-__global__ void __launch_bounds__(kThreads) count_kernel(PageArgs A) {
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.y;
-  const PlanRow r = plan_row<PLAN>(A, b, blockIdx.x == 0 && threadIdx.x == 0 ? A.status : nullptr);
-  const int held = pages_of(r.keep);
-  const int j = blockIdx.x * kThreads + threadIdx.x;
-  if (j >= held) return;
-  const int page = A.table_in[(size_t)r.parent * A.mpp + j];
-  if (page < 0 || page >= A.num_pages) {
-    set_status(A.status, SA_ERR_BAD_PAGE);
-    return;
-  }
-  atomicAdd(A.refs + page, 1);
-  if (PLAN && r.writes && j == held - 1) {
-    atomicAdd(A.writers + page, 1);
-    atomicMax(A.lowest + page, kMaxPlanRows - b);
-  }
+constexpr int kCluster = 8, kTableThreads = kPageChunk;
+
+// What one block of the cluster wrote is seen by the others behind this.
+__device__ __forceinline__ void cluster_sync() {
+  __threadfence();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Inclusive sum over a block of 1024 threads.
@@ -90,154 +76,173 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp) {
   __syncthreads();
   return x + (warp > 0 ? s_warp[warp - 1] : 0);
 }
+// The sum, for every thread.
+__device__ __forceinline__ int block_sum(int x, int* s_warp) {
+  block_scan(x, s_warp);
+  return s_warp[31];
+}
 
-// Free (plan) or live (compact) pages of each chunk; the last block of a plan
-// lines up what the rows need.
+// PLAN: the next table of a batch; else the packing of the pool.
 template <bool PLAN>
-__global__ void __launch_bounds__(kPageChunk) chunk_kernel(PageArgs A, int chunks) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads) table_kernel(PageArgs A) {
   __shared__ int s_warp[32];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.x < chunks) {
-    const int page = blockIdx.x * kPageChunk + tid;
-    const int n = __syncthreads_count(page < A.num_pages && (A.refs[page] == 0) == PLAN);
-    if (tid == 0) A.chunk[blockIdx.x] = n;
-    return;
-  }
-  int need = 0, copy = 0;
-  if (tid < A.B) {
-    const PlanRow r = plan_row<true>(A, tid, nullptr);
+  const int tid = threadIdx.x, cta = blockIdx.x;
+  const int chunks = (A.num_pages + kPageChunk - 1) / kPageChunk;
+  // a warp takes 128 entries of a table row at a time, four a lane, so that
+  // their loads do not wait on one another
+  const int lane = tid & 31, cols = (A.mpp + 127) / 128;
+  const long long pieces = (long long)A.B * cols, warps = kCluster * (kTableThreads / 32);
+  const long long piece0 = (long long)(tid >> 5) * kCluster + cta;
+
+  // no holders
+  const long long words = (long long)A.num_pages * (PLAN ? 3 : 1);   // refs, writers, lowest lie together
+  for (long long i = (long long)cta * kTableThreads + tid; i < words; i += kCluster * kTableThreads) A.refs[i] = 0;
+  cluster_sync();
+
+  // holders of every page; for a plan also the rows that will write inside it and the lowest of them
+  for (long long x = piece0; x < pieces; x += warps) {
+    const int b = (int)(x / cols), j0 = (int)(x % cols) * 128 + lane;
+    const PlanRow r = plan_row<PLAN>(A, b, j0 == 0 ? A.status : nullptr);
     const int held = pages_of(r.keep);
-    if (r.writes) {
-      const int page = A.table_in[(size_t)r.parent * A.mpp + held - 1];
-      if (page >= 0 && page < A.num_pages)
-        copy = !(A.writers[page] == A.refs[page] && A.lowest[page] == kMaxPlanRows - tid);
-    }
-    need = copy + pages_of(r.room) - held;
-  }
-  const int upto = block_scan(need, s_warp);
-  const int copies = block_scan(copy, s_warp);
-  if (tid < A.B) {
-    A.need[2 * tid] = upto - need;
-    A.need[2 * tid + 1] = 2 * (copies - copy) + copy;
-  }
-  if (tid == kPageChunk - 1) {
-    A.need[2 * A.B] = upto;
-    A.need[2 * A.B + 1] = 2 * copies;
-  }
-}
-
-// Ranks: the first free pages that the plan takes; or source and target of
-// every move.
-template <bool PLAN>
-__global__ void __launch_bounds__(kPageChunk) rank_kernel(PageArgs A, int chunks) {
-  __shared__ int s_warp[32];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, c = blockIdx.x;
-  int before = 0, all = 0;
-  for (int i = tid; i < chunks; i += kPageChunk) {
-    const int n = A.chunk[i];
-    all += n;
-    if (i < c) before += n;
-  }
-  // both sums at once: the counts of 1024 pages a chunk stay below 2^31
-  __shared__ int s_sum[2];
-  before = block_scan(before, s_warp);
-  if (tid == kPageChunk - 1) s_sum[0] = before;
-  all = block_scan(all, s_warp);
-  if (tid == kPageChunk - 1) s_sum[1] = all;
-  const int page = c * kPageChunk + tid;
-  const bool in = page < A.num_pages;
-  const bool hit = in && (A.refs[page] == 0) == PLAN;
-  const int upto = block_scan(hit, s_warp);
-  before = s_sum[0] + upto - hit;      // hits below this page
-  all = s_sum[1];
-  if (PLAN) {
-    const int take = A.need[2 * A.B];
-    if (hit && before < take) A.list[before] = page;
-    if (c == 0 && tid == 0) {
-      A.counts[0] = A.need[2 * A.B + 1] >> 1;
-      A.counts[1] = all - take;
-      if (all < take) set_status(A.status, SA_ERR_CAPACITY);
-      A.chunk[chunks] = all;
-    }
-    return;
-  }
-  // live pages below index `all`, the number of live pages
-  int low = 0;
-  for (int i = tid; i < min(chunks, all / kPageChunk); i += kPageChunk) low += A.chunk[i];
-  const int edge = all / kPageChunk * kPageChunk + tid;
-  low += edge < all && edge < A.num_pages && A.refs[edge] != 0;
-  low = block_scan(low, s_warp);
-  if (tid == kPageChunk - 1) s_sum[0] = low;
-  __syncthreads();
-  low = s_sum[0];
-  const int moves = all - low;
-  if (in) {
-    if (hit && page >= all) {
-      A.src[before - low] = page;
-      A.list[page] = before - low;
-    }
-    if (!hit && page < all) A.dst[page - before] = page;
-    if (page >= moves) A.src[page] = A.dst[page] = -1;
-  }
-  if (c == 0 && tid == 0) {
-    A.counts[0] = moves;
-    A.counts[1] = all;
-  }
-}
-
-// The next table, and a plan's list of copies.
-template <bool PLAN>
-__global__ void __launch_bounds__(kThreads) table_kernel(PageArgs A, int chunks) {
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.y;
-  const int j = blockIdx.x * kThreads + threadIdx.x;
-  if (j >= A.mpp) return;
-  const PlanRow r = plan_row<PLAN>(A, b, nullptr);
-  const int held = pages_of(r.keep);
-  int page = -1;
-  if (j < held) {
-    page = A.table_in[(size_t)r.parent * A.mpp + j];
-    if (page < 0 || page >= A.num_pages) page = -1;
-  }
-  if (PLAN) {
-    const int start = A.need[2 * b], copy = A.need[2 * b + 1] & 1, free_pages = A.chunk[chunks];
-    const bool copied = copy && j == held - 1;
-    if (copied || (j >= held && j < pages_of(r.room))) {
-      const int at = start + (copied ? 0 : copy + j - held);
-      const int fresh = at < free_pages ? A.list[at] : -1;
-      if (copied) {
-        const int rank = A.need[2 * b + 1] >> 1;
-        A.src[rank] = page;
-        A.dst[rank] = fresh;
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      page[k] = j0 + 32 * k < held ? __ldg(A.table_in + (size_t)r.parent * A.mpp + j0 + 32 * k) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (j0 + 32 * k >= held) continue;
+      if (page[k] < 0 || page[k] >= A.num_pages) {
+        set_status(A.status, SA_ERR_BAD_PAGE);
+        continue;
       }
-      page = fresh;
+      atomicAdd(A.refs + page[k], 1);
+      if (PLAN && r.writes && j0 + 32 * k == held - 1) {
+        atomicAdd(A.writers + page[k], 1);
+        atomicMax(A.lowest + page[k], kMaxPlanRows - b);
+      }
     }
-    if (j == 0) {     // rows behind the number of copies clear its entries
-      const int copies = A.need[2 * A.B + 1] >> 1;
-      if (b >= copies) A.src[b] = A.dst[b] = -1;
-    }
-  } else if (page >= A.counts[1]) {
-    page = A.dst[A.list[page]];
   }
-  A.table_out[(size_t)b * A.mpp + j] = page;
+  cluster_sync();
+
+  // free (plan) or live (compact) pages of each chunk
+  for (int c = cta; c < chunks; c += kCluster) {
+    const int page = c * kPageChunk + tid;
+    const int n = __syncthreads_count(page < A.num_pages && (__ldcg(A.refs + page) == 0) == PLAN);
+    if (tid == 0) A.chunk[c] = n;
+  }
+  if (PLAN && cta == kCluster - 1) {   // what the rows need, lined up
+    int need = 0, copy = 0;
+    if (tid < A.B) {
+      const PlanRow r = plan_row<true>(A, tid, nullptr);
+      const int held = pages_of(r.keep);
+      if (r.writes) {
+        const int page = A.table_in[(size_t)r.parent * A.mpp + held - 1];
+        if (page >= 0 && page < A.num_pages)
+          copy = !(__ldcg(A.writers + page) == __ldcg(A.refs + page) && __ldcg(A.lowest + page) == kMaxPlanRows - tid);
+      }
+      need = copy + pages_of(r.room) - held;
+    }
+    const int upto = block_scan(need, s_warp);
+    const int copies = block_scan(copy, s_warp);
+    if (tid < A.B) {
+      A.need[2 * tid] = upto - need;
+      A.need[2 * tid + 1] = 2 * (copies - copy) + copy;
+    }
+    if (tid == kTableThreads - 1) {
+      A.need[2 * A.B] = upto;
+      A.need[2 * A.B + 1] = 2 * copies;
+    }
+  }
+  cluster_sync();
+
+  // ranks: the first free pages that the plan takes; or source and target of every move
+  int all = 0;
+  for (int i = tid; i < chunks; i += kTableThreads) all += __ldcg(A.chunk + i);
+  all = block_sum(all, s_warp);
+  const int take = PLAN ? __ldcg(A.need + 2 * A.B) : 0;
+  int low = 0;                       // compact: live pages below index `all`, the number of live pages
+  if (!PLAN) {
+    for (int i = tid; i < min(chunks, all / kPageChunk); i += kTableThreads) low += __ldcg(A.chunk + i);
+    const int edge = all / kPageChunk * kPageChunk + tid;
+    low += edge < all && edge < A.num_pages && __ldcg(A.refs + edge) != 0;
+    low = block_sum(low, s_warp);
+  }
+  const int moves = all - low;
+  int before = 0;                    // in the chunks before this block's next one
+  for (int c = cta, seen = 0; c < chunks; c += kCluster) {
+    int sum = 0;
+    for (int i = seen + tid; i < c; i += kTableThreads) sum += __ldcg(A.chunk + i);
+    before += block_sum(sum, s_warp);
+    seen = c;
+    const int page = c * kPageChunk + tid;
+    const bool in = page < A.num_pages;
+    const bool hit = in && (__ldcg(A.refs + page) == 0) == PLAN;
+    const int rank = before + block_scan(hit, s_warp) - hit;      // hits below this page
+    if (PLAN) {
+      if (hit && rank < take) A.list[rank] = page;
+    } else if (in) {
+      if (hit && page >= all) {
+        A.src[rank - low] = page;
+        A.list[page] = rank - low;
+      }
+      if (!hit && page < all) A.dst[page - rank] = page;
+      if (page >= moves) A.src[page] = A.dst[page] = -1;
+    }
+  }
+  if (cta == 0 && tid == 0) {
+    A.counts[0] = PLAN ? __ldcg(A.need + 2 * A.B + 1) >> 1 : moves;
+    A.counts[1] = PLAN ? all - take : all;
+    if (PLAN && all < take) set_status(A.status, SA_ERR_CAPACITY);
+  }
+  cluster_sync();
+
+  // the next table, and a plan's list of copies
+  const int copies = PLAN ? __ldcg(A.need + 2 * A.B + 1) >> 1 : 0;
+  for (long long x = piece0; x < pieces; x += warps) {
+    const int b = (int)(x / cols), j0 = (int)(x % cols) * 128 + lane;
+    const PlanRow r = plan_row<PLAN>(A, b, nullptr);
+    const int held = pages_of(r.keep), room = pages_of(r.room);
+    const int start = PLAN ? __ldcg(A.need + 2 * b) : 0, mark = PLAN ? __ldcg(A.need + 2 * b + 1) : 0, copy = mark & 1;
+    int page[4], to[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 32 * k;
+      page[k] = j < held ? __ldg(A.table_in + (size_t)r.parent * A.mpp + j) : -1;
+      if (page[k] < 0 || page[k] >= A.num_pages) page[k] = -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {      // a fresh page of the plan, the place of a page that moves
+      const int j = j0 + 32 * k;
+      to[k] = page[k];
+      if (PLAN) {
+        const bool copied = copy && j == held - 1;
+        if (copied || (j >= held && j < room)) {
+          const int at = start + (copied ? 0 : copy + j - held);
+          to[k] = at < all ? __ldcg(A.list + at) : -1;
+        }
+      } else if (page[k] >= all) {
+        to[k] = __ldcg(A.dst + __ldcg(A.list + page[k]));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 32 * k;
+      if (PLAN && copy && j == held - 1) {
+        A.src[mark >> 1] = page[k];
+        A.dst[mark >> 1] = to[k];
+      }
+      if (j < A.mpp) A.table_out[(size_t)b * A.mpp + j] = to[k];
+    }
+    // rows behind the number of copies clear its entries
+    if (PLAN && j0 == 0 && b >= copies) A.src[b] = A.dst[b] = -1;
+  }
 }
 
 template <bool PLAN>
 int launch_table(const PageArgs& A, cudaStream_t stream) {
-  const int chunks = (A.num_pages + kPageChunk - 1) / kPageChunk;
-  const size_t zero = (size_t)A.num_pages * (PLAN ? 3 : 1) * sizeof(int);   // refs, writers, lowest lie together
-  if (cudaMemsetAsync(A.refs, 0, zero, stream) != cudaSuccess) return SA_ERR_CUDA;
-  const dim3 entries((A.mpp + kThreads - 1) / kThreads, A.B);
-  cudaError_t e = launch_pdl(count_kernel<PLAN>, entries, dim3(kThreads), 0, stream, A);
-  if (e == cudaSuccess)
-    e = launch_pdl(chunk_kernel<PLAN>, dim3(chunks + (PLAN ? 1 : 0)), dim3(kPageChunk), 0, stream, A, chunks);
-  if (e == cudaSuccess) e = launch_pdl(rank_kernel<PLAN>, dim3(chunks), dim3(kPageChunk), 0, stream, A, chunks);
-  if (e == cudaSuccess) e = launch_pdl(table_kernel<PLAN>, entries, dim3(kThreads), 0, stream, A, chunks);
+  const cudaError_t e = launch_pdl(table_kernel<PLAN>, dim3(kCluster), dim3(kTableThreads), 0, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

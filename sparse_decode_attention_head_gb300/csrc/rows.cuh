@@ -92,7 +92,7 @@ struct PageArgs {
   int* writers;           // [num_pages] rows that will write inside it (plan)
   int* lowest;            // [num_pages] kMaxPlanRows - the lowest of them (plan)
   int* list;              // [num_pages] plan: free pages; compact: a moved page's rank
-  int* chunk;             // per chunk of pages: free (plan) or live (compact) pages
+  int* chunk;             // per chunk of pages: free (plan) or live (compact) ones
   int* need;              // [B + 1] plan: new pages of the rows before
   int* status;
   int B, mpp, num_pages;

@@ -656,13 +656,13 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           if (mine) {
             tmem_ld32(tO + 32 * q4, o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = w0 == 0.f ? 0.f : o[j] * f0;
+            for (int j = 0; j < 32; ++j) o[j] *= f0;     // zeros where the row saw nothing
           }
           if (two) {
             float o1[32];
             tmem_ld32(tO + 128 + 32 * q4, o1);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] += w1 == 0.f ? 0.f : o1[j] * f1;
+            for (int j = 0; j < 32; ++j) o[j] = fmaf(o1[j], f1, o[j]);
           }
           if (whole) {
             uint32_t x[4][4];     // pieces of 16 bytes; then row j's piece lane % 4
