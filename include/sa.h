@@ -488,7 +488,8 @@ int sa_qk_norm_rope(const sa_problem* prob, int32_t n_rows, const void* q, int64
  * Products of bf16 in fp32 sums; the softmax weights are rounded to bf16 for
  * their product with V, the sum beneath them is of the unrounded ones.  A row
  * that sees nothing gets out = 0, lse = -inf.  What a row does not see cannot
- * change it, whatever is stored there (NaN and infinities included). */
+ * change it, whatever is stored there (NaN and infinities included).  out must
+ * not overlap q. */
 int sa_prompt_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
                         const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
                         const int32_t* row_offsets, void* out, float* lse_or_null, void* ws, void* stream);

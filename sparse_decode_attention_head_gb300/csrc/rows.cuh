@@ -51,7 +51,7 @@ struct RowsAttnArgs {
   int* status;
   int n_rows, B, Hq, Hk, G, mpp, num_pages;
   int tpt;                          // tokens of a query tile: 128 / G
-  float scale, scale_log2;
+  float scale_log2;                 // scale log2(e)
 };
 
 int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,

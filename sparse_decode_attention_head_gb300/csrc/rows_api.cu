@@ -23,6 +23,11 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + nb && y < x + na;
+}
+
 // The attention's partials and the page calls' counts share the space behind
 // the header: calls on one workspace are ordered on one stream.
 struct AttnLayout {
@@ -104,6 +109,8 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
   if (!q || !out) return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(ws))
     return SA_ERR_INVALID_ARG;
+  const size_t row_bytes = (size_t)n_rows * p.Hq * SA_HEAD_DIM * 2;
+  if (overlap(q, row_bytes, out, row_bytes)) return SA_ERR_INVALID_ARG;
   const int nsm = sa_host::num_sms_current();
   if (nsm <= 0) return SA_ERR_CUDA;
   sa::RowsAttnArgs A{};
@@ -131,14 +138,8 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
   A.G = p.G;
   A.mpp = p.mpp;
   A.num_pages = p.num_pages;
-  A.scale = p.scale;
   A.scale_log2 = p.scale * 1.4426950408889634f;
   return sa::launch_rows_attention(A, tmQ, tmK, tmV, nsm, as_stream(stream));
-}
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-  return x < y + nb && y < x + na;
 }
 
 int page_args(const sa_problem* prob, const int32_t* table_in, const int32_t* keep, int32_t* table_out, int32_t* src,

@@ -190,9 +190,10 @@ __device__ __forceinline__ int item_end(const RowsAttnArgs& A, const Seq& s, int
   if (A.tree != nullptr) return s.L;
   return max(0, min(s.L, s.a + min(s.n, (i + 1) * s.T)));
 }
-// The first position that some row of item i does not see (positions of a tree's drafts included).
+// The first position that some row of item i does not see (positions of a
+// tree's drafts included); at most item_end, behind which nobody sees any.
 __device__ __forceinline__ int item_edge(const RowsAttnArgs& A, const Seq& s, int i) {
-  return max(0, A.tree != nullptr ? s.a : s.a + i * s.T + 1);
+  return max(0, min(A.tree != nullptr ? s.a : s.a + i * s.T + 1, item_end(A, s, i)));
 }
 __device__ __forceinline__ int tiles_of(int end) { return (end + kRows - 1) / kRows; }
 

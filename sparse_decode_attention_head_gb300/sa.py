@@ -213,7 +213,7 @@ class Workspace:
             raise SAError(SA_ERR_INVALID_ARG, "sa_workspace_size")
         if rows:
             n = max(n, int(lib().sa_rows_workspace_size(prob.ref)))
-        self.rows = bool(rows)
+        self.rows = prob.num_pages if rows else 0    # pages that the page calls' counts have room for
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
         self.device_index = self.buf.get_device()
         _check(lib().sa_workspace_init(_ptr(self.buf), n, _stream()), "sa_workspace_init")
@@ -531,7 +531,7 @@ def _row_stride(t, name: str, heads: int, n: int, dev) -> int:
     return row if n > 1 else heads * HEAD_DIM
 
 
-def _check_rows_args(ws: Workspace, args) -> int:
+def _check_rows_args(prob: Problem, ws: Workspace, args) -> int:
     """Tensors (tensor, dtype, shape, name) of a packed-row or page call: type, shape, dense, all on the workspace's
     device, and that device the current one.  These calls are a few microseconds long, so the checks that pass take
     the short way; one that does not is repeated by _need for its message.  Returns the current stream."""
@@ -544,8 +544,8 @@ def _check_rows_args(ws: Workspace, args) -> int:
             pass
         _need(t, dtype, name, shape)
         raise ValueError(f"{name} must be on the workspace's device, got {t.device}")
-    if not ws.rows:
-        raise ValueError("the workspace must be made with rows=True")
+    if ws.rows < prob.num_pages:
+        raise ValueError("the workspace must be made with rows=True, for as many pages")
     if torch.cuda.current_device() != dev:
         raise ValueError("the workspace's device must be the current one")
     return torch._C._cuda_getCurrentRawStream(dev)
@@ -589,7 +589,7 @@ def qk_norm_rope(prob: Problem, q, k, v, row_offsets, seq_lens, page_table, q_ou
             args.append((positions, torch.int32, (len(rope.axis_pairs), n), "positions"))
     else:
         inv_freq = positions = None
-    stream = _check_rows_args(ws, args)
+    stream = _check_rows_args(prob, ws, args)
     _check(lib().sa_qk_norm_rope(prob.ref, n, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
                                  _p(q_weight), _p(k_weight), eps, None if rope is None else rope.ref, _p(inv_freq),
                                  _p(positions), row_offsets.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(),
@@ -613,7 +613,7 @@ def _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, 
 def prompt_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, ws: Workspace, lse=None):
     """Causal attention of packed prompt rows over the paged cache
     (sa_prompt_attention): row i of a sequence's n sees positions 0 .. L - n + i."""
-    stream = _check_rows_args(ws, _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse))
+    stream = _check_rows_args(prob, ws, _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse))
     _check(lib().sa_prompt_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                      page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
                                      out.data_ptr(), _p(lse), ws.buf.data_ptr(), stream), "sa_prompt_attention")
@@ -626,7 +626,7 @@ def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_o
     tree_mask [n_rows] int64 (sa_tree_attention)."""
     args = _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse)
     args.append((tree_mask, torch.int64, (q.shape[0],), "tree_mask"))
-    stream = _check_rows_args(ws, args)
+    stream = _check_rows_args(prob, ws, args)
     _check(lib().sa_tree_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                    page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
                                    tree_mask.data_ptr(), out.data_ptr(), _p(lse), ws.buf.data_ptr(), stream),
@@ -638,7 +638,7 @@ def accept_rows(prob: Problem, k_pool, v_pool, page_table, base_lens, path, path
     (sa_accept_rows); path [B][max_path], path_cnt [B]."""
     most = path.shape[1] if _rows_of(path, "path") and path.dim() == 2 else 0
     pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
-    stream = _check_rows_args(ws, (
+    stream = _check_rows_args(prob, ws, (
         (k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
         (page_table, torch.int32, (prob.B, prob.max_pages_per_seq), "page_table"),
         (base_lens, torch.int32, (prob.B,), "base_lens"), (path, torch.int32, (prob.B, most), "path"),
@@ -658,7 +658,7 @@ def plan_pages(prob: Problem, table_in, parent, keep, lens, table_out, copy_src,
             (keep, torch.int32, rows, "keep"), (lens, torch.int32, rows, "lens"),
             (table_out, torch.int32, table, "table_out"), (copy_src, torch.int32, rows, "copy_src"),
             (copy_dst, torch.int32, rows, "copy_dst"), (counts, torch.int32, (2,), "counts")]
-    stream = _check_rows_args(ws, args)
+    stream = _check_rows_args(prob, ws, args)
     _check(lib().sa_plan_pages(prob.ref, *(t.data_ptr() for t, _, _, _ in args), ws.buf.data_ptr(), stream),
            "sa_plan_pages")
 
@@ -671,7 +671,7 @@ def compact_pages(prob: Problem, table_in, seq_lens, table_out, move_src, move_d
     args = [(table_in, torch.int32, table, "table_in"), (seq_lens, torch.int32, (prob.B,), "seq_lens"),
             (table_out, torch.int32, table, "table_out"), (move_src, torch.int32, pages, "move_src"),
             (move_dst, torch.int32, pages, "move_dst"), (counts, torch.int32, (2,), "counts")]
-    stream = _check_rows_args(ws, args)
+    stream = _check_rows_args(prob, ws, args)
     _check(lib().sa_compact_pages(prob.ref, *(t.data_ptr() for t, _, _, _ in args), ws.buf.data_ptr(), stream),
            "sa_compact_pages")
 
@@ -683,7 +683,7 @@ def copy_pages(prob: Problem, k_pool, v_pool, src, dst, count, ws: Workspace):
     if _rows_of(count, "count") < 1:
         raise ValueError("count must hold a number")
     pool = (prob.num_pages, prob.Hk, prob.page_size, prob.D)
-    stream = _check_rows_args(ws, ((k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
+    stream = _check_rows_args(prob, ws, ((k_pool, torch.bfloat16, pool, "k_pool"), (v_pool, torch.bfloat16, pool, "v_pool"),
                                    (src, torch.int32, (n,), "src"), (dst, torch.int32, (n,), "dst"),
                                    (count, torch.int32, tuple(count.shape), "count")))
     _check(lib().sa_copy_pages(prob.ref, k_pool.data_ptr(), v_pool.data_ptr(), src.data_ptr(), dst.data_ptr(),

@@ -146,6 +146,19 @@ def test_later_values_cannot_change_a_row(kind):
     _check(r, words)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(8, 2), (28, 4)])
+def test_later_values_over_a_split_cache(Hq, Hk):
+    # the same where the item's KV range is cut over blocks, with one and two query tiles
+    for rows, prefix in (([40, 7], [1500, 2000]), ([64], [3000])):
+        r = R.Rows(rows, prefix, Hq, Hk, seed=25)
+        words = R.tree_words(rows, 9)
+        for b, n in enumerate(rows):
+            for t in (prefix[b] + n // 2, prefix[b] + n - 1):
+                r.v_pool[int(r.table[b, t // P]), :, t % P, 1::9] = math.inf
+        _check(r)
+        _check(r, words)
+
+
 def test_later_keys_cannot_change_a_row():
     r = R.Rows([100], [30], 8, 2, seed=14)
     base, _ = _run(r)
@@ -180,6 +193,16 @@ def test_a_length_behind_the_table():
     r = R.Rows([30], [50], 8, 2, seed=18, mpp=4)
     _check(r, status=sa.SA_ERR_CAPACITY)
     _check(r, R.tree_words([30], 6), status=sa.SA_ERR_CAPACITY)
+    # all rows behind the table: they see what the table has, and it ends inside a tile
+    r = R.Rows([30, 9], [170, 300], 8, 2, seed=23, mpp=5)
+    _check(r, status=sa.SA_ERR_CAPACITY)
+    _check(r, R.tree_words([30, 9], 6), status=sa.SA_ERR_CAPACITY)
+
+
+def test_tree_rows_that_are_more_than_the_tokens():
+    r = R.Rows([20, 6], [0, 5], 8, 2, seed=24)
+    r.lens[0] = 7
+    _check(r, R.tree_words([20, 6], 8))
 
 
 def test_bad_offsets_are_cut():
@@ -234,6 +257,32 @@ def test_other_stream_and_graphs():
             R.assert_within(outs[i], ref["out"], ref["tol"], "out")
             R.assert_within(lses[i], ref["lse"], ref["tol_lse"], "lse")
     assert ws.status() == sa.SA_OK
+
+
+def test_binding_refuses():
+    r = R.Rows([4], [10], 8, 2, seed=26)
+    out = torch.zeros_like(r.q)
+    small, ws = sa.Workspace(r.prob), sa.Workspace(r.prob, rows=True)
+    go = lambda **kw: sa.prompt_attention(**{**dict(prob=r.prob, q=r.q, k_pool=r.k_pool, v_pool=r.v_pool, page_table=r.table,  # noqa: E731
+                                                    seq_lens=r.lens, row_offsets=r.offsets, out=out, ws=ws), **kw})
+    go()
+    with pytest.raises(ValueError, match="rows=True"):
+        go(ws=small)
+    with pytest.raises(TypeError):
+        go(q=r.q.float())
+    with pytest.raises(ValueError):
+        go(out=out[:3])
+    with pytest.raises(ValueError):
+        go(row_offsets=r.offsets[:1])
+    with pytest.raises(ValueError):
+        go(q=torch.zeros(8, 4, 128, dtype=torch.bfloat16, device="cuda").transpose(0, 1))
+    with pytest.raises(sa.SAError) as e:
+        go(out=r.q)
+    assert e.value.code == sa.SA_ERR_INVALID_ARG
+    more = R.problem(1, 8, 2, r.mpp, r.k_pool.shape[0] + 1)     # a pool of more pages than the workspace is for
+    with pytest.raises(ValueError, match="as many pages"):
+        go(prob=more, k_pool=torch.zeros(more.num_pages, 2, 16, 128, dtype=torch.bfloat16, device="cuda"),
+           v_pool=torch.zeros(more.num_pages, 2, 16, 128, dtype=torch.bfloat16, device="cuda"))
 
 
 @pytest.mark.parametrize("scale", [1.0, 0.01])

@@ -67,7 +67,7 @@ def test_rotation_limits(lib):
     assert _rotate(lib, p, n=0, rope=_rope((20,))) == UNSUP        # settings are checked without rows too
 
 
-def _attend(lib, p, tree=None, n=4, q=A, kp=A, vp=A, table=A, lens=A, off=A, out=A, ws=A, words=A):
+def _attend(lib, p, tree=None, n=4, q=FAR[0], kp=A, vp=A, table=A, lens=A, off=A, out=FAR[1], ws=A, words=A):
     if tree:
         return lib.sa_tree_attention(p.ref, n, q, kp, vp, table, lens, off, words, out, None, ws, None)
     return lib.sa_prompt_attention(p.ref, n, q, kp, vp, table, lens, off, out, None, ws, None)
@@ -76,7 +76,8 @@ def _attend(lib, p, tree=None, n=4, q=A, kp=A, vp=A, table=A, lens=A, off=A, out
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("kw", [
     dict(n=-1), dict(q=None), dict(kp=None), dict(vp=None), dict(table=None), dict(lens=None), dict(off=None),
-    dict(out=None), dict(ws=None), dict(q=M), dict(kp=M), dict(vp=M), dict(out=M), dict(ws=M)])
+    dict(out=None), dict(ws=None), dict(q=M), dict(kp=M), dict(vp=M), dict(out=M), dict(ws=M), dict(out=FAR[0]),
+    dict(out=ctypes.c_void_p(FAR[0].value + 4096))])
 def test_attention_refusals(lib, kw, tree):
     assert _attend(lib, _prob(), tree, **kw) == BAD
 
