@@ -57,8 +57,8 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
 // What work weighs: a KV token of an item with one query tile (bound by the
 // loads: measured 1.45 us a tile of them) and with two (1.6 us), and an item's
-// query load, first tile and epilogue (4.4 us).
-constexpr int kOneCost = 6, kTwoCost = 7, kItemCost = 2500;
+// query load, first tile and epilogue (3.4 us).
+constexpr int kOneCost = 6, kTwoCost = 7, kItemCost = 2000;
 constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
@@ -516,45 +516,43 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         if (!(ok = wait_warp(&c->s_full[h], steps_done & 1, c, A.status))) break;
         ++steps_done;
         tc_fence_after();
-        float v[128];
-        tmem_ld64_start<0>(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
-        const bool masked = (kt + 1) * kRows > edge || bad != 0;
-        tmem_ld64_finish<0>(v);
-        tmem_ld64_start<64>(tS + 64, v);
-        float top[4] = {v[0], v[1], v[2], v[3]};
-        if (!masked) {   // the maximum of the first half while the second is on its way
-#pragma unroll
-          for (int j = 4; j < 60; j += 8) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) top[x] = fmaxf(fmaxf(top[x], v[j + x]), v[j + 4 + x]);
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], v[60 + x]);
-        }
-        tmem_ld64_finish<64>(v);
-        if (masked) {
-          // bit j of see[w]: column 32 w + j
-          const int base = kt * kRows;
-#pragma unroll
+        if ((kt + 1) * kRows > edge || bad != 0) {
+          // masked in TMEM, 32 columns at a time: once or twice an item, and
+          // a long piece of straight code would cost its instruction fetches
+#pragma unroll 1
           for (int w = 0; w < 4; ++w) {
-            const int c0 = base + 32 * w;
-            const int nlim = lim - c0;
-            uint32_t see = nlim >= 32 ? 0xffffffffu : nlim <= 0 ? 0u : (1u << nlim) - 1u;
+            const int c0 = kt * kRows + 32 * w;
+            const int nlim = lim - c0, nend = p.end - c0;
+            uint32_t see = nlim >= 32 ? 0xffffffffu : nlim <= 0 ? 0u : (1u << nlim) - 1u;   // bit j: column c0 + j
             const int sh = c0 - p.a;     // column c0 is bit sh of the word
             if (sh > -32 && sh < 64) see |= sh >= 0 ? (uint32_t)(word >> sh) : (uint32_t)(word << -sh);
-            const int nend = p.end - c0;
             see &= nend >= 32 ? 0xffffffffu : nend <= 0 ? 0u : (1u << nend) - 1u;
             if ((bad >> (2 * w)) & 1u) see &= 0xffff0000u;
             if ((bad >> (2 * w + 1)) & 1u) see &= 0x0000ffffu;
+            float x[32];
+            uint32_t y[32];
+            tmem_ld32(tS + 32 * w, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[32 * w + j] = (see >> j) & 1u ? v[32 * w + j] : -INFINITY;
+            for (int j = 0; j < 32; ++j) y[j] = (see >> j) & 1u ? __float_as_uint(x[j]) : 0xff800000u;
+            tmem_st32(tS + 32 * w, y);
           }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top[x] = v[x];
-#pragma unroll
-          for (int j = 4; j < 64; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+          tmem_wait_st();
         }
+        float v[128];
+        tmem_ld64_start<0>(tS, v);
+        tmem_ld64_finish<0>(v);
+        tmem_ld64_start<64>(tS + 64, v);
+        // the maximum of the first half while the second is on its way
+        float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < 60; j += 8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top[x] = fmaxf(fmaxf(top[x], v[j + x]), v[j + 4 + x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], v[60 + x]);
+        tmem_ld64_finish<64>(v);
 #pragma unroll
         for (int j = 64; j < 128; j += 8) {
 #pragma unroll
@@ -570,7 +568,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           m = mn;
           l *= alpha;
           if (s >= 2) {
-#pragma unroll
+#pragma unroll 1
             for (int q4 = 0; q4 < 4; ++q4) {
               float o[32];
               uint32_t ow[32];
