@@ -84,7 +84,7 @@ struct Ctl {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2][2], o_done[2];
+  uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t edge_go[kSlots], clean[kSlots];   // a V tile at the edge: its load is under way, it is clean
   uint64_t ml_full, ml_free;
   uint64_t drain;
@@ -438,8 +438,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     mbar_init(&c->q_empty, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&c->s_full[h], 1);
-      mbar_init(&c->p_full[h][0], kRows);
-      mbar_init(&c->p_full[h][1], kRows);
+      mbar_init(&c->p_full[h], kRows);
       mbar_init(&c->o_done[h], 1);
     }
     mbar_init(&c->ml_full, kRows);
@@ -516,7 +515,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         if (!(ok = wait_warp(&c->s_full[h], steps_done & 1, c, A.status))) break;
         ++steps_done;
         tc_fence_after();
+        float v[128];
+        tmem_ld64_start<0>(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
+        tmem_ld64_finish<0>(v);
         if ((kt + 1) * kRows > edge || bad != 0) {
           // masked in TMEM, 32 columns at a time: once or twice an item, and
           // a long piece of straight code would cost its instruction fetches
@@ -538,10 +540,9 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             tmem_st32(tS + 32 * w, y);
           }
           tmem_wait_st();
+          tmem_ld64_start<0>(tS, v);
+          tmem_ld64_finish<0>(v);
         }
-        float v[128];
-        tmem_ld64_start<0>(tS, v);
-        tmem_ld64_finish<0>(v);
         tmem_ld64_start<64>(tS + 64, v);
         // the maximum of the first half while the second is on its way
         float top[4] = {v[0], v[1], v[2], v[3]};
@@ -595,12 +596,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             pw[j] = pack_bf16(p0, p1);
           }
           tmem_st16(tS + 16 * q4, pw);
-          if (q4 & 1) {   // half of the weights are there: their product may begin
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&c->p_full[h][q4 >> 1]);
-          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&c->p_full[h]);
         float sum0, sum1;
         unpack2(add2(sum[0], sum[1]), sum0, sum1);
         l += sum0 + sum1;
@@ -612,7 +611,6 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         ++items_done;
         tc_fence_after();
       }
-      const bool poisoned = *(volatile int*)&c->poison[piece & 3] == piece + 1;
       const bool whole = p.k0 == 0 && p.k1 == p.nt;
       float m1 = -INFINITY, l1 = 0.f;
       if (p.dual) {
@@ -628,6 +626,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           l1 = x.y;
         }
       }
+      // every tile of the piece has been multiplied by now, so its edge is clean and known
+      const bool poisoned = *(volatile int*)&c->poison[piece & 3] == piece + 1;
       if (!(p.dual && h == 1)) {
         // the two groups' states of a row joined; a group without a tile, or without a position seen, has l = 0
         const bool two = p.dual && N > 1;
@@ -754,12 +754,11 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2, k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS,
                     x != 0);
       };
-      // O of group h from the tile at vr: the tokens of one half of the weights
-      auto mma_o = [&](int h, int part, bool first) {
+      auto mma_o = [&](int h, bool first) {      // O of group h from the tile at vr
         const uint64_t v = dV + vr.slot * (kTileBytes / 16);
         const uint32_t d = tmem + 256 + h * 128, w = tmem + h * 128;
 #pragma unroll
-        for (int x = 4 * part; x < 4 * part + 4; ++x) tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
+        for (int x = 0; x < 8; ++x) tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
       };
       auto issue_s = [&](int h, bool k_done, bool q_done) {
         mma_s(h);
@@ -769,21 +768,16 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       };
       auto wait_k = [&]() -> bool { return wait_warp(&c->full[kr.slot], kr.parity, c, A.status); };
       // A step of group h: O from the tile at vr, then S from the tile at kr
-      // (`more`: there is one).  What is there already is seen by one look
-      // before, so that nothing stands between the instructions then; a K
-      // tile that is late is waited for behind O, whose V slot comes free.
+      // (`more`: there is one).  A K tile that is there is seen by one look
+      // before, so that nothing stands between the instructions then; one
+      // that is late is waited for behind O, whose V slot comes free.
       // k_done, v_done: the tile has no other reader; q_done: nor has Q.
       auto step = [&](int h, bool first, bool more, bool k_done, bool v_done, bool q_done) -> bool {
         const bool k_there = more && __all_sync(0xffffffffu, mbar_test_wait(&c->full[kr.slot], kr.parity));
-        const bool late = !__all_sync(0xffffffffu, mbar_test_wait(&c->p_full[h][1], p_par[h]));
-        if (late && !wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;
+        if (!wait_warp(&c->p_full[h], p_par[h], c, A.status)) return false;
         tc_fence_after();
-        if (elect_one()) mma_o(h, 0, first);
-        __syncwarp();
-        if (late && !wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
-        if (late) tc_fence_after();
         if (elect_one()) {
-          mma_o(h, 1, first);
+          mma_o(h, first);
           if (v_done) tc_commit(&c->empty[vr.slot]);
           if (!more) tc_commit(&c->o_done[h]);
           if (k_there) issue_s(h, k_done, q_done);
