@@ -12,11 +12,11 @@
 // are laid end to end, weighted by the KV tokens they see, and cut into one
 // equal run for each block (one block an SM, persistent): many rows give
 // whole items, few rows over a long cache split an item's KV range over
-// blocks.  Where there are fewer items than blocks a block takes no more than
-// one (17 us in place of 21 for four prompts of at most 200 rows).  A cut item leaves (maximum, sum, unnormalised output) for each
-// row, and the merge kernel joins the pieces in order with the log-sum-exp
-// identity; blocks never wait on one another and nothing is added atomically,
-// so results do not depend on timing.
+// blocks.  With little work a block takes no more than one item (16 us in
+// place of 21 for four prompts of at most 200 rows).  A cut item leaves
+// (maximum, sum, unnormalised output) for each row, and the merge kernel joins
+// the pieces in order with the log-sum-exp identity; blocks never wait on one
+// another and nothing is added atomically, so results do not depend on timing.
 //
 // Block: 12 warps.
 //   warps 0-3, 4-7  softmax of query tile 0 and 1, a thread a row
@@ -39,6 +39,17 @@
 // tiles that hold positions some row of the item does not see, V rows behind
 // the item's last position become zero and non-finite values become zero in
 // shared memory; rows that do see such a value add it at the end.
+//
+// What bounds it, measured on one GB300 (1868 TFLOP/s bf16, 6.78 TB/s): with
+// two query tiles a KV tile takes 1.6 us, of which the tensor core works 60 %;
+// S reads 8 KB of shared memory an instruction and runs at about two thirds of
+// the rate of O, and a group's softmax (0.9 us) and its matrix products do not
+// overlap with each other, only with the other group's.  16384 causal rows of
+// 32 / 8 heads: 1.49 ms, 1.48 PFLOP/s.  2048 rows behind 30720: 1.51 PFLOP/s.
+// With one query tile the cache's bytes bound it: 32 drafted tokens for each
+// of 8 sequences of 32K: 182 us, 5.9 TB/s.  Two issuing warps, one a group,
+// were slower (1.94 ms: the groups' instructions interleave and both finish
+// late), so was one barrier for a tile's weights in place of two (1.51 ms).
 #include <algorithm>
 
 #include "rows.cuh"
@@ -84,7 +95,7 @@ struct Ctl {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2][2], o_done[2];
   uint64_t edge_go[kSlots], clean[kSlots];   // a V tile at the edge: its load is under way, it is clean
   uint64_t ml_full, ml_free;
   uint64_t drain;
@@ -438,7 +449,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     mbar_init(&c->q_empty, 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&c->s_full[h], 1);
-      mbar_init(&c->p_full[h], kRows);
+      mbar_init(&c->p_full[h][0], kRows);
+      mbar_init(&c->p_full[h][1], kRows);
       mbar_init(&c->o_done[h], 1);
     }
     mbar_init(&c->ml_full, kRows);
@@ -596,10 +608,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             pw[j] = pack_bf16(p0, p1);
           }
           tmem_st16(tS + 16 * q4, pw);
+          if (q4 & 1) {   // half of the weights are there: their product may begin
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&c->p_full[h][q4 >> 1]);
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&c->p_full[h]);
         float sum0, sum1;
         unpack2(add2(sum[0], sum[1]), sum0, sum1);
         l += sum0 + sum1;
@@ -754,11 +768,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2, k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS,
                     x != 0);
       };
-      auto mma_o = [&](int h, bool first) {      // O of group h from the tile at vr
+      // O of group h from the tile at vr: the tokens of one half of the weights
+      auto mma_o = [&](int h, int part, bool first) {
         const uint64_t v = dV + vr.slot * (kTileBytes / 16);
         const uint32_t d = tmem + 256 + h * 128, w = tmem + h * 128;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
+        for (int x = 4 * part; x < 4 * part + 4; ++x) tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
       };
       auto issue_s = [&](int h, bool k_done, bool q_done) {
         mma_s(h);
@@ -768,16 +783,24 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       };
       auto wait_k = [&]() -> bool { return wait_warp(&c->full[kr.slot], kr.parity, c, A.status); };
       // A step of group h: O from the tile at vr, then S from the tile at kr
-      // (`more`: there is one).  A K tile that is there is seen by one look
-      // before, so that nothing stands between the instructions then; one
-      // that is late is waited for behind O, whose V slot comes free.
+      // (`more`: there is one).  What is there already is seen by one look
+      // before, so that nothing stands between the instructions then; a K
+      // tile that is late is waited for behind O, whose V slot comes free.
       // k_done, v_done: the tile has no other reader; q_done: nor has Q.
       auto step = [&](int h, bool first, bool more, bool k_done, bool v_done, bool q_done) -> bool {
         const bool k_there = more && __all_sync(0xffffffffu, mbar_test_wait(&c->full[kr.slot], kr.parity));
-        if (!wait_warp(&c->p_full[h], p_par[h], c, A.status)) return false;
+        const bool late = !__all_sync(0xffffffffu, mbar_test_wait(&c->p_full[h][1], p_par[h]));
+        if (late) {      // the first half of the weights at least
+          if (!wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;
+          tc_fence_after();
+          if (elect_one()) mma_o(h, 0, first);
+          __syncwarp();
+          if (!wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
+        }
         tc_fence_after();
         if (elect_one()) {
-          mma_o(h, first);
+          if (!late) mma_o(h, 0, first);
+          mma_o(h, 1, first);
           if (v_done) tc_commit(&c->empty[vr.slot]);
           if (!more) tc_commit(&c->o_done[h]);
           if (k_there) issue_s(h, k_done, q_done);
