@@ -516,7 +516,7 @@ int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, con
  * must not be shared with another (sa_plan_pages sees to that).  A node
  * below 0 or position behind the table, or a count outside [0, max_path],
  * records SA_ERR_INVALID_ARG, a bad page SA_ERR_BAD_PAGE; that sequence is
- * then left as it was. */
+ * then left as it was.  B above 65535 gives SA_ERR_UNSUPPORTED. */
 int sa_accept_rows(const sa_problem* prob, void* k_pool, void* v_pool, const int32_t* page_table,
                    const int32_t* base_lens, const int32_t* path, int32_t max_path, const int32_t* path_cnt, void* ws,
                    void* stream);

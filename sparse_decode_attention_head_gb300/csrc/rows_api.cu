@@ -148,7 +148,6 @@ int page_args(const sa_problem* prob, const int32_t* table_in, const int32_t* ke
   if (rc != SA_OK) return rc;
   if (!table_in || !keep || !table_out || !src || !dst || !counts || !ws) return SA_ERR_INVALID_ARG;
   if (!aligned16(ws)) return SA_ERR_INVALID_ARG;
-  if (p->B > 65535) return SA_ERR_UNSUPPORTED;
   const size_t bytes = (size_t)p->B * p->mpp * sizeof(int32_t);
   if (overlap(table_in, bytes, table_out, bytes)) return SA_ERR_INVALID_ARG;
   const PageLayout l = page_layout(*p);
@@ -266,7 +265,7 @@ int sa_prompt_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
 int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool, const void* v_pool,
                       const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets,
                       const uint64_t* tree_mask, void* out, float* lse_or_null, void* ws, void* stream) {
-  if (tree_mask == nullptr) return SA_ERR_INVALID_ARG;
+  if (tree_mask == nullptr && n_rows != 0) return SA_ERR_INVALID_ARG;
   return rows_attention(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, tree_mask, out, lse_or_null,
                         ws, stream);
 }

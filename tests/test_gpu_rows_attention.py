@@ -89,6 +89,7 @@ def test_rows_of_nobody_and_no_rows():
     _check(R.Rows([0, 0], [5, 0], 8, 2, seed=7, extra_rows=4))
     r = R.Rows([0], [5], 8, 2, seed=7)
     _run(r)
+    _run(r, np.zeros(0, np.uint64))
 
 
 @pytest.mark.parametrize("Hq,Hk", HEADS)

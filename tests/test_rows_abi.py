@@ -88,7 +88,7 @@ def test_attention_limits(lib):
     assert _attend(lib, _prob(page_size=32)) == UNSUP
     assert _attend(lib, _prob(Hq=32, k_per_head=[1] * 32)) == UNSUP         # 16 query heads a KV head
     for tree in (False, True):
-        assert _attend(lib, _prob(), tree, n=0, q=None, out=None) == sa.SA_OK
+        assert _attend(lib, _prob(), tree, n=0, q=None, out=None, words=None) == sa.SA_OK
 
 
 def test_page_call_refusals(lib):
