@@ -786,9 +786,11 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       // (`more`: there is one).  What is there already is seen by one look
       // before, so that nothing stands between the instructions then; a K
       // tile that is late is waited for behind O, whose V slot comes free.
-      // k_done, v_done: the tile has no other reader; q_done: nor has Q.
-      auto step = [&](int h, bool first, bool more, bool k_done, bool v_done, bool q_done) -> bool {
-        const bool k_there = more && __all_sync(0xffffffffu, mbar_test_wait(&c->full[kr.slot], kr.parity));
+      // k_seen: the other group has waited for it; k_done, v_done: the tile
+      // has no other reader; q_done: nor has Q.
+      auto step = [&](int h, bool first, bool more, bool k_seen, bool k_done, bool v_done, bool q_done) -> bool {
+        const bool k_there =
+            more && (k_seen || __all_sync(0xffffffffu, mbar_test_wait(&c->full[kr.slot], kr.parity)));
         const bool late = !__all_sync(0xffffffffu, mbar_test_wait(&c->p_full[h][1], p_par[h]));
         if (late) {      // the first half of the weights at least
           if (!wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;
@@ -840,7 +842,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         for (int s = 0; s < ntp; ++s) {
           const bool more = s + 2 < ntp;
           if (!(ok = wait_v(k0 + s))) break;
-          if (!(ok = step(s & 1, s < 2, more, true, true, s + 3 == ntp))) break;
+          if (!(ok = step(s & 1, s < 2, more, false, true, true, s + 3 == ntp))) break;
         }
       } else {         // a tile two steps
         first_s(0, false, false);
@@ -849,8 +851,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         for (int t = 0; t < ntp; ++t) {
           const bool first = t == 0, more = t + 1 < ntp;
           if (!(ok = wait_v(k0 + t))) break;
-          if (!(ok = step(0, first, more, false, false, false))) break;
-          if (!(ok = step(1, first, more, true, true, t + 2 == ntp))) break;
+          if (!(ok = step(0, first, more, false, false, false, false))) break;
+          if (!(ok = step(1, first, more, true, true, true, t + 2 == ntp))) break;
         }
       }
       if (!ok) break;
