@@ -298,7 +298,7 @@ int launch_rotate(const RotateArgs& A, int num_sms, cudaStream_t stream) {
     const long long items = (long long)A.n_rows * r, rounds = (items + warps - 1) / warps;
     runs = r;
     run = each;
-    if (items * 5 >= rounds * warps * 4) break;
+    if (items * 4 >= rounds * warps * 3) break;
   }
   runs = (heads + run - 1) / run;
   const long long blocks = ((long long)A.n_rows * runs + kWarps - 1) / kWarps;

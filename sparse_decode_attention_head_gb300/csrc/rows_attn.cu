@@ -782,47 +782,59 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         if (q_done) tc_commit(&c->q_empty);
       };
       auto wait_k = [&]() -> bool { return wait_warp(&c->full[kr.slot], kr.parity, c, A.status); };
-      // A step of group h: O from the tile at vr, then S from the tile at kr
-      // (`more`: there is one).  What is there already is seen by one look
-      // before, so that nothing stands between the instructions then; a K
-      // tile that is late is waited for behind O, whose V slot comes free.
-      // k_seen: the other group has waited for it; k_done, v_done: the tile
-      // has no other reader; q_done: nor has Q.
-      auto step = [&](int h, bool first, bool more, bool k_seen, bool k_done, bool v_done, bool q_done) -> bool {
-        const bool k_there =
-            more && (k_seen || __all_sync(0xffffffffu, mbar_test_wait(&c->full[kr.slot], kr.parity)));
-        const bool late = !__all_sync(0xffffffffu, mbar_test_wait(&c->p_full[h][1], p_par[h]));
-        if (late) {      // the first half of the weights at least
-          if (!wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;
-          tc_fence_after();
-          if (elect_one()) mma_o(h, 0, first);
-          __syncwarp();
-          if (!wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          if (!late) mma_o(h, 0, first);
-          mma_o(h, 1, first);
-          if (v_done) tc_commit(&c->empty[vr.slot]);
-          if (!more) tc_commit(&c->o_done[h]);
-          if (k_there) issue_s(h, k_done, q_done);
-        }
-        __syncwarp();
-        if (more && !k_there) {
-          if (!wait_k()) return false;
-          if (elect_one()) issue_s(h, k_done, q_done);
-          __syncwarp();
-        }
-        p_par[h] ^= 1;
-        if (v_done) vr.advance(2);
-        if (more && k_done) kr.advance(2);
-        return true;
-      };
       auto wait_v = [&](int kt) -> bool {
         if (!wait_warp(&c->full[vr.slot], vr.parity, c, A.status)) return false;
         if ((kt + 1) * kRows > edge) {
           if (!wait_warp(&c->clean[vr.slot], (cleaned >> vr.slot) & 1, c, A.status)) return false;
           cleaned ^= 1u << vr.slot;
+        }
+        return true;
+      };
+      // A step of group h: O from the tile at vr, then S from the tile at kr
+      // (`more`: there is one).  What it needs is there as a rule: one look at
+      // all of it, and nothing stands between the instructions.  What is late
+      // is waited for in the order of its use, a K tile behind O, whose V
+      // slot comes free.
+      // seen: the other group has waited for both tiles; done: they have no
+      // other reader; q_done: nor has Q.
+      auto step = [&](int h, int kt, bool first, bool more, bool seen, bool done, bool q_done) -> bool {
+        const bool clean = (kt + 1) * kRows <= edge;
+        const bool v_there = seen || mbar_test_wait(&c->full[vr.slot], vr.parity);
+        const bool k_there = !more || seen || mbar_test_wait(&c->full[kr.slot], kr.parity);
+        const bool p_there = mbar_test_wait(&c->p_full[h][1], p_par[h]);
+        if (__all_sync(0xffffffffu, v_there && k_there && p_there && (seen || clean))) {
+          tc_fence_after();
+          if (elect_one()) {
+            mma_o(h, 0, first);
+            mma_o(h, 1, first);
+            if (done) tc_commit(&c->empty[vr.slot]);
+            if (more) issue_s(h, done, q_done);
+            else tc_commit(&c->o_done[h]);
+          }
+        } else {
+          if (!seen && !wait_v(kt)) return false;
+          if (!wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;   // half of the weights
+          tc_fence_after();
+          if (elect_one()) mma_o(h, 0, first);
+          __syncwarp();
+          if (!wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_o(h, 1, first);
+            if (done) tc_commit(&c->empty[vr.slot]);
+            if (!more) tc_commit(&c->o_done[h]);
+          }
+          __syncwarp();
+          if (more) {
+            if (!seen && !wait_k()) return false;
+            if (elect_one()) issue_s(h, done, q_done);
+          }
+        }
+        __syncwarp();
+        p_par[h] ^= 1;
+        if (done) {
+          vr.advance(2);
+          if (more) kr.advance(2);
         }
         return true;
       };
@@ -841,8 +853,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll 1
         for (int s = 0; s < ntp; ++s) {
           const bool more = s + 2 < ntp;
-          if (!(ok = wait_v(k0 + s))) break;
-          if (!(ok = step(s & 1, s < 2, more, false, true, true, s + 3 == ntp))) break;
+          if (!(ok = step(s & 1, k0 + s, s < 2, more, false, true, s + 3 == ntp))) break;
         }
       } else {         // a tile two steps
         first_s(0, false, false);
@@ -850,9 +861,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll 1
         for (int t = 0; t < ntp; ++t) {
           const bool first = t == 0, more = t + 1 < ntp;
-          if (!(ok = wait_v(k0 + t))) break;
-          if (!(ok = step(0, first, more, false, false, false, false))) break;
-          if (!(ok = step(1, first, more, true, true, true, t + 2 == ntp))) break;
+          if (!(ok = step(0, k0 + t, first, more, false, false, false))) break;
+          if (!(ok = step(1, k0 + t, first, more, true, true, t + 2 == ntp))) break;
         }
       }
       if (!ok) break;
