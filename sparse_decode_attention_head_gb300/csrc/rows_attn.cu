@@ -41,15 +41,18 @@
 // shared memory; rows that do see such a value add it at the end.
 //
 // What bounds it, measured on one GB300 (1868 TFLOP/s bf16, 6.78 TB/s): with
-// two query tiles a KV tile takes 1.6 us, of which the tensor core works 60 %;
-// S reads 8 KB of shared memory an instruction and runs at about two thirds of
-// the rate of O, and a group's softmax (0.9 us) and its matrix products do not
-// overlap with each other, only with the other group's.  16384 causal rows of
-// 32 / 8 heads: 1.49 ms, 1.48 PFLOP/s.  2048 rows behind 30720: 1.51 PFLOP/s.
-// With one query tile the cache's bytes bound it: 32 drafted tokens for each
-// of 8 sequences of 32K: 182 us, 5.9 TB/s.  Two issuing warps, one a group,
-// were slower (1.94 ms: the groups' instructions interleave and both finish
-// late), so was one barrier for a tile's weights in place of two (1.51 ms).
+// two query tiles a KV tile takes 1.55 us, of which the tensor core works two
+// thirds; S reads 8 KB of shared memory an instruction and runs slower than O,
+// and a group's softmax (0.8 us) and its matrix products do not overlap with
+// each other, only with the other group's.  The issuing warp stands between
+// them, so what it waits for is looked at once a step (1.40 ms in place of
+// 1.48).  16384 causal rows of 32 / 8 heads: 1.40 ms, 1.57 PFLOP/s.  2048 rows
+// behind 30720: 1.63 PFLOP/s.  With one query tile the cache's bytes bound it:
+// 32 drafted tokens for each of 8 sequences of 32K: 182 us, 5.9 TB/s.
+// Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
+// interleave and both finish late); one barrier for all of a tile's weights
+// in place of one for each half (2 %); two threads a row (1.90 ms: 104
+// registers do not hold what they need, and they meet once a tile).
 #include <algorithm>
 
 #include "rows.cuh"
