@@ -360,8 +360,8 @@ int launch_accept_rows(void* k_pool, void* v_pool, const int* page_table, const 
                        int max_path, const int* path_cnt, int B, int Hk, int mpp, int num_pages, int* status,
                        cudaStream_t stream) {
   const cudaError_t e = launch_pdl(accept_rows_kernel, dim3(Hk, B), dim3(kThreads), 0, stream,
-                                   static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), page_table, base_lens, path,
-                                   max_path, path_cnt, Hk, mpp, num_pages, status);
+                                   static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), page_table, base_lens,
+                                   path, max_path, path_cnt, Hk, mpp, num_pages, status);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

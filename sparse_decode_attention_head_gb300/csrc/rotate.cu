@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(RotateArgs A, int r
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hl = lane & 15, half = lane >> 4;
   const int heads = A.Hq + 2 * A.Hk, turned_heads = A.Hq + A.Hk;
   const long long items = (long long)A.n_rows * runs, stride = (long long)gridDim.x * kWarps;
-  uint8_t* stage[2] = {s_heads + (size_t)(warp * 2) * kStage * kD * 2, s_heads + (size_t)(warp * 2 + 1) * kStage * kD * 2};
+  uint8_t* stage[2] = {s_heads + (size_t)(warp * 2) * kStage * kD * 2,
+                       s_heads + (size_t)(warp * 2 + 1) * kStage * kD * 2};
   if (lane < 2) mbar_init(&s_full[warp][lane], 1);
   fence_mbar_init();
   __syncwarp();
@@ -199,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(RotateArgs A, int r
     auto turn = [&](uint4 y, bool norm) -> uint4 {
       uint32_t z[4] = {y.x, y.y, y.z, y.w};      // the partner's values; none where nothing turns
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = HALVES ? __shfl_sync(0xffffffffu, z[i], partner) : __funnelshift_l(z[i], z[i], 16);
+      for (int i = 0; i < 4; ++i)
+        z[i] = HALVES ? __shfl_sync(0xffffffffu, z[i], partner) : __funnelshift_l(z[i], z[i], 16);
       if (!all_turned) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = turned ? z[i] : 0u;

@@ -223,7 +223,8 @@ int sa_qk_norm_rope(const sa_problem* prob, int32_t n_rows, const void* q, int64
     return SA_ERR_INVALID_ARG;
   const size_t out_bytes = (size_t)n_rows * q_row * 2;
   auto span = [&](int64_t stride, int64_t row) { return (size_t)((n_rows - 1) * stride + row) * 2; };
-  if (!(q_out == q && q_stride == q_row) && overlap(q, span(q_stride, q_row), q_out, out_bytes)) return SA_ERR_INVALID_ARG;
+  if (!(q_out == q && q_stride == q_row) && overlap(q, span(q_stride, q_row), q_out, out_bytes))
+    return SA_ERR_INVALID_ARG;
   if (overlap(k, span(k_stride, kv_row), q_out, out_bytes) || overlap(v, span(v_stride, kv_row), q_out, out_bytes))
     return SA_ERR_INVALID_ARG;
   const int nsm = sa_host::num_sms_current();

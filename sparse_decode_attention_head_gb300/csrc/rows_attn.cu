@@ -504,7 +504,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     const int t_row = r / A.G, g = r - t_row * A.G;
     uint32_t steps_done = 0, items_done = 0, duals = 0, tiles = 0;
     bool ok = true;
-    for (int piece = 0; (ok = wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status)); ++piece) {
+    for (int piece = 0;; ++piece) {
+      if (!(ok = wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status))) break;
       const Piece& p = c->piece[piece % kPieces];
       const int k0 = p.k0, ntp = p.k1 - k0, edge = p.edge;
       const bool dual = p.dual;
@@ -741,256 +742,259 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     }
   } else {
     regs_dec<kOtherRegs>();
-  if (warp == 8) {
-    // ------------------------------------------------------------ matrix instructions
-    // The whole warp runs the loop and one elected lane issues; the others
-    // wait for it at the end of each group (spinning ahead at the next
-    // barrier they would take its issue slots).
-    constexpr uint32_t idS = bf16_idesc(128, 128, false), idO = bf16_idesc(128, 128, true);
-    const uint64_t dQ = smem_desc(smem_u32(s_q), 16, 1024);
-    const uint64_t dK = smem_desc(smem_u32(s_kv), 16, 2048), dV = smem_desc(smem_u32(s_kv), 1024, 2048);
-    Ring kr, vr;               // the next K and the next V tile
-    vr.advance(1);
-    uint32_t pieces = 0, cleaned = 0, p_par[2] = {0, 0};   // cleaned: a parity bit a slot
-    bool ok = true;
-    for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
-      const Piece* pp = &c->piece[piece % kPieces];
-      const int k0 = pp->k0, ntp = pp->k1 - k0, edge = pp->edge;
-      const bool dual = pp->dual;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
-      if (k0 < 0) break;
-      if (ntp == 0) continue;
-      if (!(ok = wait_warp(&c->q_full, pieces & 1, c, A.status))) break;
-      ++pieces;
-      auto mma_s = [&](int h) {      // S of group h from the tile at kr
-        const uint64_t q = dQ + (dual ? 0 : h * (kTileBytes / 16)), k = dK + kr.slot * (kTileBytes / 16);
-        const uint32_t d = tmem + h * 128;
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2, k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS,
-                    x != 0);
-      };
-      // O of group h from the tile at vr: the tokens of one half of the weights
-      auto mma_o = [&](int h, int part, bool first) {
-        const uint64_t v = dV + vr.slot * (kTileBytes / 16);
-        const uint32_t d = tmem + 256 + h * 128, w = tmem + h * 128;
-#pragma unroll
-        for (int x = 4 * part; x < 4 * part + 4; ++x) tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
-      };
-      auto issue_s = [&](int h, bool k_done, bool q_done) {
-        mma_s(h);
-        tc_commit(&c->s_full[h]);
-        if (k_done) tc_commit(&c->empty[kr.slot]);
-        if (q_done) tc_commit(&c->q_empty);
-      };
-      auto wait_k = [&]() -> bool { return wait_warp(&c->full[kr.slot], kr.parity, c, A.status); };
-      auto wait_v = [&](int kt) -> bool {
-        if (!wait_warp(&c->full[vr.slot], vr.parity, c, A.status)) return false;
-        if ((kt + 1) * kRows > edge) {
-          if (!wait_warp(&c->clean[vr.slot], (cleaned >> vr.slot) & 1, c, A.status)) return false;
-          cleaned ^= 1u << vr.slot;
-        }
-        return true;
-      };
-      // A step of group h: O from the tile at vr, then S from the tile at kr
-      // (`more`: there is one).  What it needs is there as a rule: one look at
-      // all of it, and nothing stands between the instructions.  What is late
-      // is waited for in the order of its use, a K tile behind O, whose V
-      // slot comes free.
-      // seen: the other group has waited for both tiles; done: they have no
-      // other reader; q_done: nor has Q.
-      auto step = [&](int h, int kt, bool first, bool more, bool seen, bool done, bool q_done) -> bool {
-        const bool clean = (kt + 1) * kRows <= edge;
-        const bool v_there = seen || mbar_test_wait(&c->full[vr.slot], vr.parity);
-        const bool k_there = !more || seen || mbar_test_wait(&c->full[kr.slot], kr.parity);
-        const bool p_there = mbar_test_wait(&c->p_full[h][1], p_par[h]);
-        if (__all_sync(0xffffffffu, v_there && k_there && p_there && (seen || clean))) {
-          tc_fence_after();
-          if (elect_one()) {
-            mma_o(h, 0, first);
-            mma_o(h, 1, first);
-            if (done) tc_commit(&c->empty[vr.slot]);
-            if (more) issue_s(h, done, q_done);
-            else tc_commit(&c->o_done[h]);
-          }
-        } else {
-          if (!seen && !wait_v(kt)) return false;
-          if (!wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;   // half of the weights
-          tc_fence_after();
-          if (elect_one()) mma_o(h, 0, first);
-          __syncwarp();
-          if (!wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            mma_o(h, 1, first);
-            if (done) tc_commit(&c->empty[vr.slot]);
-            if (!more) tc_commit(&c->o_done[h]);
-          }
-          __syncwarp();
-          if (more) {
-            if (!seen && !wait_k()) return false;
-            if (elect_one()) issue_s(h, done, q_done);
-          }
-        }
+    if (warp == 8) {
+      // ------------------------------------------------------------ matrix instructions
+      // The whole warp runs the loop and one elected lane issues; the others
+      // wait for it at the end of each group (spinning ahead at the next
+      // barrier they would take its issue slots).
+      constexpr uint32_t idS = bf16_idesc(128, 128, false), idO = bf16_idesc(128, 128, true);
+      const uint64_t dQ = smem_desc(smem_u32(s_q), 16, 1024);
+      const uint64_t dK = smem_desc(smem_u32(s_kv), 16, 2048), dV = smem_desc(smem_u32(s_kv), 1024, 2048);
+      Ring kr, vr;               // the next K and the next V tile
+      vr.advance(1);
+      uint32_t pieces = 0, cleaned = 0, p_par[2] = {0, 0};   // cleaned: a parity bit a slot
+      bool ok = true;
+      for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
+        const Piece* pp = &c->piece[piece % kPieces];
+        const int k0 = pp->k0, ntp = pp->k1 - k0, edge = pp->edge;
+        const bool dual = pp->dual;
         __syncwarp();
-        p_par[h] ^= 1;
-        if (done) {
-          vr.advance(2);
-          if (more) kr.advance(2);
-        }
-        return true;
-      };
-      auto first_s = [&](int h, bool k_done, bool q_done) {
-        if (elect_one()) issue_s(h, k_done, q_done);
-        __syncwarp();
-        if (k_done) kr.advance(2);
-      };
-      if (!(ok = wait_k())) break;
-      if (dual) {      // a tile a step, the groups in turn
-        first_s(0, true, ntp == 1);
-        if (ntp > 1) {
-          if (!(ok = wait_k())) break;
-          first_s(1, true, ntp == 2);
-        }
-#pragma unroll 1
-        for (int s = 0; s < ntp; ++s) {
-          const bool more = s + 2 < ntp;
-          if (!(ok = step(s & 1, k0 + s, s < 2, more, false, true, s + 3 == ntp))) break;
-        }
-      } else {         // a tile two steps
-        first_s(0, false, false);
-        first_s(1, true, ntp == 1);
-#pragma unroll 1
-        for (int t = 0; t < ntp; ++t) {
-          const bool first = t == 0, more = t + 1 < ntp;
-          if (!(ok = step(0, k0 + t, first, more, false, false, false))) break;
-          if (!(ok = step(1, k0 + t, first, more, true, true, t + 2 == ntp))) break;
-        }
-      }
-      if (!ok) break;
-    }
-    // nothing of this block is in flight when it frees its TMEM and ends
-    __syncwarp();
-    if (elect_one()) {
-      tc_commit(&c->drain);
-      wait_out(&c->drain, 0, A.status);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ loads
-    uint32_t tile = 0, pieces = 0, loads = 0;
-    const uint32_t q_bytes = (uint32_t)(A.tpt * A.G) * kD * 2;
-    bool ok = true;
-    Walk walk(A, c);
-    for (int piece = 0;; ++piece) {
-      Piece p;
-      if (!walk.next(p)) p.k0 = p.k1 = -1;
-      if (piece >= kPieces &&
-          !(ok = wait_warp(&c->piece_empty[piece % kPieces], (piece / kPieces - 1) & 1, c, A.status)))
-        break;
-      if (lane == 0) {
-        c->piece[piece % kPieces] = p;
-        mbar_arrive(&c->piece_full[piece % kPieces]);
-      }
-      if (p.k0 < 0) break;
-      const int ntp = p.k1 - p.k0;
-      if (ntp == 0) continue;
-      if (pieces > 0 && !(ok = wait_warp(&c->q_empty, (pieces - 1) & 1, c, A.status))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&c->q_full, p.dual ? q_bytes : 2 * q_bytes);
-        for (int x = 0; x < (p.dual ? 2 : 4); ++x)
-          tma_load_3d(s_q + x * (kTileBytes / 2), &tmQ, (x & 1) * 64, p.kvh * A.G, p.row0 + (x >> 1) * A.tpt, &c->q_full);
-      }
-      ++pieces;
-      const int* pt = A.page_table + (size_t)p.b * A.mpp;
-      for (int t = 0; t < ntp; ++t) {
-        const int page = (p.k0 + t) * (kRows / kP) + lane;
-        const bool there = lane < kRows / kP && page * kP < p.end;
-        const int phys = there ? __ldg(pt + page) : -1;
-        const bool good = phys >= 0 && phys < A.num_pages;
-        const unsigned goods = __ballot_sync(0xffffffffu, good), bads = __ballot_sync(0xffffffffu, there && !good);
-        if (bads != 0 && lane == 0) set_status(A.status, SA_ERR_BAD_PAGE);
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t idx = 2 * (tile + t) + kv, slot = idx % kSlots;
-          if (idx >= kSlots && !(ok = wait_warp(&c->empty[slot], (idx / kSlots - 1) & 1, c, A.status))) break;
-          uint8_t* dst = s_kv + slot * kTileBytes;
-          if (kv == 0) {
-            if (lane == 0) *(volatile uint32_t*)&c->bad[(tile + t) & 15] = bads;
-          } else if (bads != 0) {   // V of a page that is not there: zeros
-            for (int x = lane; x < kTileBytes / 16; x += 32)
-              if ((bads >> (x >> 8)) & 1u) reinterpret_cast<uint4*>(dst)[x] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
+        if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
+        if (k0 < 0) break;
+        if (ntp == 0) continue;
+        if (!(ok = wait_warp(&c->q_full, pieces & 1, c, A.status))) break;
+        ++pieces;
+        auto mma_s = [&](int h) {      // S of group h from the tile at kr
+          const uint64_t q = dQ + (dual ? 0 : h * (kTileBytes / 16)), k = dK + kr.slot * (kTileBytes / 16);
+          const uint32_t d = tmem + h * 128;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            tc_mma_ss(d, q + (x >> 2) * (kTileBytes / 2 / 16) + (x & 3) * 2,
+                      k + (x >> 2) * (1024 / 16) + (x & 3) * 2, idS, x != 0);
+        };
+        // O of group h from the tile at vr: the tokens of one half of the weights
+        auto mma_o = [&](int h, int part, bool first) {
+          const uint64_t v = dV + vr.slot * (kTileBytes / 16);
+          const uint32_t d = tmem + 256 + h * 128, w = tmem + h * 128;
+#pragma unroll
+          for (int x = 4 * part; x < 4 * part + 4; ++x)
+            tc_mma_ts(d, w + x * 8, v + x * (4096 / 16), idO, x != 0 || !first);
+        };
+        auto issue_s = [&](int h, bool k_done, bool q_done) {
+          mma_s(h);
+          tc_commit(&c->s_full[h]);
+          if (k_done) tc_commit(&c->empty[kr.slot]);
+          if (q_done) tc_commit(&c->q_empty);
+        };
+        auto wait_k = [&]() -> bool { return wait_warp(&c->full[kr.slot], kr.parity, c, A.status); };
+        auto wait_v = [&](int kt) -> bool {
+          if (!wait_warp(&c->full[vr.slot], vr.parity, c, A.status)) return false;
+          if ((kt + 1) * kRows > edge) {
+            if (!wait_warp(&c->clean[vr.slot], (cleaned >> vr.slot) & 1, c, A.status)) return false;
+            cleaned ^= 1u << vr.slot;
+          }
+          return true;
+        };
+        // A step of group h: O from the tile at vr, then S from the tile at kr
+        // (`more`: there is one).  What it needs is there as a rule: one look at
+        // all of it, and nothing stands between the instructions.  What is late
+        // is waited for in the order of its use, a K tile behind O, whose V
+        // slot comes free.
+        // seen: the other group has waited for both tiles; done: they have no
+        // other reader; q_done: nor has Q.
+        auto step = [&](int h, int kt, bool first, bool more, bool seen, bool done, bool q_done) -> bool {
+          const bool clean = (kt + 1) * kRows <= edge;
+          const bool v_there = seen || mbar_test_wait(&c->full[vr.slot], vr.parity);
+          const bool k_there = !more || seen || mbar_test_wait(&c->full[kr.slot], kr.parity);
+          const bool p_there = mbar_test_wait(&c->p_full[h][1], p_par[h]);
+          if (__all_sync(0xffffffffu, v_there && k_there && p_there && (seen || clean))) {
+            tc_fence_after();
+            if (elect_one()) {
+              mma_o(h, 0, first);
+              mma_o(h, 1, first);
+              if (done) tc_commit(&c->empty[vr.slot]);
+              if (more) issue_s(h, done, q_done);
+              else tc_commit(&c->o_done[h]);
+            }
+          } else {
+            if (!seen && !wait_v(kt)) return false;
+            if (!wait_warp(&c->p_full[h][0], p_par[h], c, A.status)) return false;   // half of the weights
+            tc_fence_after();
+            if (elect_one()) mma_o(h, 0, first);
+            __syncwarp();
+            if (!wait_warp(&c->p_full[h][1], p_par[h], c, A.status)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_o(h, 1, first);
+              if (done) tc_commit(&c->empty[vr.slot]);
+              if (!more) tc_commit(&c->o_done[h]);
+            }
+            __syncwarp();
+            if (more) {
+              if (!seen && !wait_k()) return false;
+              if (elect_one()) issue_s(h, done, q_done);
+            }
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&c->full[slot], __popc(goods) * 4096);
-            if (kv == 1 && (p.k0 + t + 1) * kRows > p.edge) mbar_arrive(&c->edge_go[slot]);
+          p_par[h] ^= 1;
+          if (done) {
+            vr.advance(2);
+            if (more) kr.advance(2);
           }
-          ++loads;
+          return true;
+        };
+        auto first_s = [&](int h, bool k_done, bool q_done) {
+          if (elect_one()) issue_s(h, k_done, q_done);
           __syncwarp();
-          if (good)
-            tma_load_4d(dst + lane * 4096, kv == 0 ? (const void*)&tmK : (const void*)&tmV, 0, 0, 0,
-                        (phys * A.Hk + p.kvh) * 2, &c->full[slot]);
+          if (k_done) kr.advance(2);
+        };
+        if (!(ok = wait_k())) break;
+        if (dual) {      // a tile a step, the groups in turn
+          first_s(0, true, ntp == 1);
+          if (ntp > 1) {
+            if (!(ok = wait_k())) break;
+            first_s(1, true, ntp == 2);
+          }
+#pragma unroll 1
+          for (int s = 0; s < ntp; ++s) {
+            const bool more = s + 2 < ntp;
+            if (!(ok = step(s & 1, k0 + s, s < 2, more, false, true, s + 3 == ntp))) break;
+          }
+        } else {         // a tile two steps
+          first_s(0, false, false);
+          first_s(1, true, ntp == 1);
+#pragma unroll 1
+          for (int t = 0; t < ntp; ++t) {
+            const bool first = t == 0, more = t + 1 < ntp;
+            if (!(ok = step(0, k0 + t, first, more, false, false, false))) break;
+            if (!(ok = step(1, k0 + t, first, more, true, true, t + 2 == ntp))) break;
+          }
         }
         if (!ok) break;
       }
-      if (!ok) break;
-      tile += ntp;
-    }
-    // copies in flight land before the block ends
-    for (uint32_t j = loads > kSlots ? loads - kSlots : 0; j < loads; ++j)
-      wait_out(&c->full[j % kSlots], (j / kSlots) & 1, A.status);
-    if (pieces > 0) wait_out(&c->q_full, (pieces - 1) & 1, A.status);
-  } else {
-    // ------------------------------------------------------------ the edge of V
-    const int w = warp - 10;
-    // edge_go orders these warps behind the loads: they skip most uses of a
-    // slot, so the parity of its full barrier alone would not tell which one
-    uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
-    bool ok = true;
-    for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
-      const Piece p = c->piece[piece % kPieces];
+      // nothing of this block is in flight when it frees its TMEM and ends
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
-      if (p.k0 < 0) break;
-      const int ntp = p.k1 - p.k0;
-      for (int t = max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
-        const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
-        if (!(ok = wait_warp(&c->edge_go[slot], (gone >> slot) & 1, c, A.status))) break;
-        gone ^= 1u << slot;
-        if (!(ok = wait_warp(&c->full[slot], (idx / kSlots) & 1, c, A.status))) break;
-        const int base = (p.k0 + t) * kRows;
-        uint4* sv = reinterpret_cast<uint4*>(s_kv + slot * kTileBytes);   // 16-byte chunk x: token group x / 128, row (x / 8) % 8
-        bool found = false;
-        for (int x = (max(0, p.edge - base) >> 3) * 128 + w * 32 + lane; x < kTileBytes / 16; x += 64) {
-          const int pos = base + (x >> 7) * 8 + ((x >> 3) & 7);
-          if (pos >= p.end) {
-            sv[x] = make_uint4(0, 0, 0, 0);
-          } else if (pos >= p.edge) {
-            uint4 q = sv[x];
-            uint32_t* e = reinterpret_cast<uint32_t*>(&q);
-            bool hit = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (!bf16_pair_nonfinite(e[j])) continue;
-              hit = true;
-              if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u;
-              if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0x0000ffffu;
-            }
-            if (hit) sv[x] = q;
-            found |= hit;
-          }
-        }
-        if (found) *(volatile int*)&c->poison[piece & 3] = piece + 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->clean[slot]);
+      if (elect_one()) {
+        tc_commit(&c->drain);
+        wait_out(&c->drain, 0, A.status);
       }
-      if (!ok) break;
-      tile += ntp;
+      __syncwarp();
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ loads
+      uint32_t tile = 0, pieces = 0, loads = 0;
+      const uint32_t q_bytes = (uint32_t)(A.tpt * A.G) * kD * 2;
+      bool ok = true;
+      Walk walk(A, c);
+      for (int piece = 0;; ++piece) {
+        Piece p;
+        if (!walk.next(p)) p.k0 = p.k1 = -1;
+        if (piece >= kPieces &&
+            !(ok = wait_warp(&c->piece_empty[piece % kPieces], (piece / kPieces - 1) & 1, c, A.status)))
+          break;
+        if (lane == 0) {
+          c->piece[piece % kPieces] = p;
+          mbar_arrive(&c->piece_full[piece % kPieces]);
+        }
+        if (p.k0 < 0) break;
+        const int ntp = p.k1 - p.k0;
+        if (ntp == 0) continue;
+        if (pieces > 0 && !(ok = wait_warp(&c->q_empty, (pieces - 1) & 1, c, A.status))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&c->q_full, p.dual ? q_bytes : 2 * q_bytes);
+          for (int x = 0; x < (p.dual ? 2 : 4); ++x)
+            tma_load_3d(s_q + x * (kTileBytes / 2), &tmQ, (x & 1) * 64, p.kvh * A.G, p.row0 + (x >> 1) * A.tpt,
+                        &c->q_full);
+        }
+        ++pieces;
+        const int* pt = A.page_table + (size_t)p.b * A.mpp;
+        for (int t = 0; t < ntp; ++t) {
+          const int page = (p.k0 + t) * (kRows / kP) + lane;
+          const bool there = lane < kRows / kP && page * kP < p.end;
+          const int phys = there ? __ldg(pt + page) : -1;
+          const bool good = phys >= 0 && phys < A.num_pages;
+          const unsigned goods = __ballot_sync(0xffffffffu, good), bads = __ballot_sync(0xffffffffu, there && !good);
+          if (bads != 0 && lane == 0) set_status(A.status, SA_ERR_BAD_PAGE);
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t idx = 2 * (tile + t) + kv, slot = idx % kSlots;
+            if (idx >= kSlots && !(ok = wait_warp(&c->empty[slot], (idx / kSlots - 1) & 1, c, A.status))) break;
+            uint8_t* dst = s_kv + slot * kTileBytes;
+            if (kv == 0) {
+              if (lane == 0) *(volatile uint32_t*)&c->bad[(tile + t) & 15] = bads;
+            } else if (bads != 0) {   // V of a page that is not there: zeros
+              for (int x = lane; x < kTileBytes / 16; x += 32)
+                if ((bads >> (x >> 8)) & 1u) reinterpret_cast<uint4*>(dst)[x] = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&c->full[slot], __popc(goods) * 4096);
+              if (kv == 1 && (p.k0 + t + 1) * kRows > p.edge) mbar_arrive(&c->edge_go[slot]);
+            }
+            ++loads;
+            __syncwarp();
+            if (good)
+              tma_load_4d(dst + lane * 4096, kv == 0 ? (const void*)&tmK : (const void*)&tmV, 0, 0, 0,
+                          (phys * A.Hk + p.kvh) * 2, &c->full[slot]);
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        tile += ntp;
+      }
+      // copies in flight land before the block ends
+      for (uint32_t j = loads > kSlots ? loads - kSlots : 0; j < loads; ++j)
+        wait_out(&c->full[j % kSlots], (j / kSlots) & 1, A.status);
+      if (pieces > 0) wait_out(&c->q_full, (pieces - 1) & 1, A.status);
+    } else {
+      // ------------------------------------------------------------ the edge of V
+      const int w = warp - 10;
+      // edge_go orders these warps behind the loads: they skip most uses of a
+      // slot, so the parity of its full barrier alone would not tell which one
+      uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
+      bool ok = true;
+      for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
+        const Piece p = c->piece[piece % kPieces];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
+        if (p.k0 < 0) break;
+        const int ntp = p.k1 - p.k0;
+        for (int t = max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
+          const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
+          if (!(ok = wait_warp(&c->edge_go[slot], (gone >> slot) & 1, c, A.status))) break;
+          gone ^= 1u << slot;
+          if (!(ok = wait_warp(&c->full[slot], (idx / kSlots) & 1, c, A.status))) break;
+          const int base = (p.k0 + t) * kRows;
+          // 16-byte chunk x: token group x / 128, row (x / 8) % 8
+          uint4* sv = reinterpret_cast<uint4*>(s_kv + slot * kTileBytes);
+          bool found = false;
+          for (int x = (max(0, p.edge - base) >> 3) * 128 + w * 32 + lane; x < kTileBytes / 16; x += 64) {
+            const int pos = base + (x >> 7) * 8 + ((x >> 3) & 7);
+            if (pos >= p.end) {
+              sv[x] = make_uint4(0, 0, 0, 0);
+            } else if (pos >= p.edge) {
+              uint4 q = sv[x];
+              uint32_t* e = reinterpret_cast<uint32_t*>(&q);
+              bool hit = false;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (!bf16_pair_nonfinite(e[j])) continue;
+                hit = true;
+                if ((e[j] & 0x7f80u) == 0x7f80u) e[j] &= 0xffff0000u;
+                if ((e[j] & 0x7f800000u) == 0x7f800000u) e[j] &= 0x0000ffffu;
+              }
+              if (hit) sv[x] = q;
+              found |= hit;
+            }
+          }
+          if (found) *(volatile int*)&c->poison[piece & 3] = piece + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->clean[slot]);
+        }
+        if (!ok) break;
+        tile += ntp;
+      }
     }
-  }
   }
   tc_fence_before();
   __syncthreads();
