@@ -906,11 +906,17 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
                         &c->q_full);
         }
         ++pieces;
+        // a lane a page of the tile; the next tile's pages are looked up while this one's are copied
         const int* pt = A.page_table + (size_t)p.b * A.mpp;
-        for (int t = 0; t < ntp; ++t) {
+        auto page_of = [&](int t) {
           const int page = (p.k0 + t) * (kRows / kP) + lane;
-          const bool there = lane < kRows / kP && page * kP < p.end;
-          const int phys = there ? __ldg(pt + page) : -1;
+          return lane < kRows / kP && page * kP < p.end ? __ldg(pt + page) : -1;
+        };
+        int next_phys = page_of(0);
+        for (int t = 0; t < ntp; ++t) {
+          const bool there = lane < kRows / kP && ((p.k0 + t) * (kRows / kP) + lane) * kP < p.end;
+          const int phys = next_phys;
+          next_phys = page_of(t + 1);
           const bool good = phys >= 0 && phys < A.num_pages;
           const unsigned goods = __ballot_sync(0xffffffffu, good), bads = __ballot_sync(0xffffffffu, there && !good);
           if (bads != 0 && lane == 0) set_status(A.status, SA_ERR_BAD_PAGE);
