@@ -48,7 +48,7 @@
 // them, so what it waits for is looked at once a step (1.40 ms in place of
 // 1.48).  16384 causal rows of 32 / 8 heads: 1.40 ms, 1.57 PFLOP/s.  2048 rows
 // behind 30720: 1.63 PFLOP/s.  With one query tile the cache's bytes bound it:
-// 32 drafted tokens for each of 8 sequences of 32K: 182 us, 5.9 TB/s.
+// 32 drafted tokens for each of 8 sequences of 32K: 178 us, 6.0 TB/s.
 // Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
 // interleave and both finish late); one barrier for all of a tile's weights
 // in place of one for each half (2 %); two threads a row (1.90 ms: 104
