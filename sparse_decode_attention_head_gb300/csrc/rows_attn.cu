@@ -47,7 +47,7 @@
 // each other, only with the other group's.  The issuing warp stands between
 // them, so what it waits for is looked at once a step (1.40 ms in place of
 // 1.48).  16384 causal rows of 32 / 8 heads: 1.40 ms, 1.57 PFLOP/s.  2048 rows
-// behind 30720: 1.63 PFLOP/s.  With one query tile the cache's bytes bound it:
+// behind 30K others: 1.63 PFLOP/s.  With one query tile the cache's bytes bound it:
 // 32 drafted tokens for each of 8 sequences of 32K: 178 us, 6.0 TB/s.
 // Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
 // interleave and both finish late); one barrier for all of a tile's weights
