@@ -578,11 +578,13 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         mx *= A.scale_log2;
         if (m == -INFINITY) m = mx;   // all zeros so far: nothing to rescale
-        const bool grow = mx > m + kLag;
+        // a warp rescales together, each row by what it grew itself: a factor of one
+        // for the others, whose bits depend on no neighbour, and no vote for lanes
+        // without a row, which hold another sequence's queries or an earlier call's
+        const bool grow = valid && mx > m + kLag;
         if (__any_sync(0xffffffffu, grow)) {
-          const float mn = fmaxf(m, mx);
-          const float alpha = ex2(m - mn);
-          m = mn;
+          const float alpha = grow ? ex2(m - mx) : 1.f;
+          m = grow ? mx : m;
           l *= alpha;
           if (s >= 2) {
 #pragma unroll 1
