@@ -430,11 +430,14 @@ int sa_decode_step_bypass(const sa_problem* prob, const void* q,
  *     counts them, row i sits at position L - n + i of the cache.  Rows
  *     before row_offsets[0] and from row_offsets[B] on belong to nobody and
  *     their outputs are left as they were.
- *   - Device errors: offsets that decrease or pass n_rows are cut to the rows
- *     there are and record SA_ERR_INVALID_ARG; L above max_pages_per_seq * P
+ *   - Device errors, of every sequence, with rows or without: offsets that
+ *     decrease or pass n_rows are cut to the rows there are and record
+ *     SA_ERR_INVALID_ARG (the outputs and cache rows of a row that two
+ *     sequences then claim are undefined); L above max_pages_per_seq * P
  *     records SA_ERR_CAPACITY and the positions behind the table are left
  *     out; a page outside the pool records SA_ERR_BAD_PAGE and its tokens are
- *     left out.
+ *     left out.  A call with n_rows = 0 checks its arguments and launches
+ *     nothing.
  *   - Their workspace has sa_rows_workspace_size bytes (one of
  *     max(sa_workspace_size, sa_rows_workspace_size) serves every call).  They
  *     use the problem's shapes and scale; selection settings play no part. */

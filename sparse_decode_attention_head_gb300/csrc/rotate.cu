@@ -107,6 +107,12 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(RotateArgs A, int r
     }
   };
   load();
+  // every sequence's offsets and length are looked at once, also of those that
+  // no row leads to; by a warp that has nothing to do with the frequencies
+  if (warp == kWarps - 1) {
+    for (int b = (int)blockIdx.x * 32 + lane; b < A.B; b += (int)gridDim.x * 32)
+      row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, A.status);
+  }
   if (tid < A.pairs) {
     const double turns = (double)A.inv_freq[tid] * 0.15915494309189533577;
     s_freq[tid] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(RotateArgs A, int r
         if (a == 0 || A.axis_end[a - 1] < A.pairs) axis_pos[a] = __ldg(A.positions + (size_t)a * A.n_rows + row);
     }
     const int b = seq_of_row(A.row_offsets, A.B, row, lane);
-    const RowSeq s = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, A.status);
+    const RowSeq s = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, nullptr);
     const bool mine = row >= s.row0 && row < s.row0 + s.n;
     const int pos = s.a + row - s.row0;
     bool place = false;
