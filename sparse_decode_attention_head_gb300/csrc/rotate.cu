@@ -247,7 +247,12 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(RotateArgs A, int r
       __syncwarp();                    // the stage that is loaded next has been read
       load();
       const uint32_t st = used & 1;
-      mbar_wait_bounded(&s_full[warp][st], (used >> 1) & 1, A.status);
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_full[warp][st], (used >> 1) & 1, A.status))) {
+        // nothing of a stage that did not arrive is stored; the copies that are
+        // under way are waited for, with the same limit, and the warp ends
+        for (; used < loads; ++used) (void)mbar_wait_bounded(&s_full[warp][used & 1], (used >> 1) & 1, A.status);
+        return;
+      }
       ++used;
       const uint4* src = reinterpret_cast<const uint4*>(stage[st]) + hl;      // head hs + i is src[16 i]
       const int he = min(h1, hs + kStage);

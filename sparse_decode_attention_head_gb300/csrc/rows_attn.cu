@@ -121,7 +121,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // Waits with a limit of kWaitNs; a wait that runs out, here or elsewhere in the
 // block, ends the block's work.
 constexpr unsigned long long kWaitNs = 2000000000ull;
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+[[nodiscard]] __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
   unsigned long long t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
@@ -150,7 +150,7 @@ __device__ __forceinline__ void wait_out(uint64_t* bar, uint32_t parity, int* st
 }
 
 // wait_bar by a whole warp: all lanes see the same answer.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+[[nodiscard]] __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, c, status));
 }
 

@@ -187,10 +187,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Wait with an iteration limit.  Returns false (and records SA_ERR_TIMEOUT)
-// if the phase did not complete; callers then skip the data.
+// if the phase did not complete; callers then skip the data (the build refuses
+// a call that does not look at the answer).
 constexpr uint32_t kWaitLimit = 1u << 22;
 
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int* status) {
+[[nodiscard]] __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int* status) {
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
   }
