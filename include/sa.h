@@ -449,10 +449,12 @@ size_t sa_rows_workspace_size(const sa_problem* prob);
 #define SA_ROPE_HALVES 0 /* dim j with dim j + R / 2, j < R / 2 */
 #define SA_ROPE_PAIRS 1  /* dim 2 j with dim 2 j + 1 */
 
-/* Rotary positions.  R / 2 = sum of axis_pairs dim pairs turn (R <= 128, a
- * multiple of 16; the dims from R on stay); the first axis_pairs[0] of them
- * by the position on axis 0, the next axis_pairs[1] by axis 1, and so on (one
- * axis for text; time, height and width for pictures). */
+/* Rotary positions.  R / 2 = sum of axis_pairs dim pairs turn (2 <= R <= 128;
+ * the dims from R on stay); the first axis_pairs[0] of them by the position on
+ * axis 0, the next axis_pairs[1] by axis 1, and so on (one axis for text;
+ * time, height and width for pictures).  The sections of several axes may have
+ * any sum; with one axis R is a multiple of 16 (SA_ERR_UNSUPPORTED otherwise).
+ * A sum of pairs that is a multiple of 8 is the fast form. */
 typedef struct sa_rope {
   int32_t layout;                  /* SA_ROPE_HALVES or SA_ROPE_PAIRS */
   int32_t axes;                    /* 1 .. SA_MAX_AXES */

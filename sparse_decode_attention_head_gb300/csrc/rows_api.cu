@@ -207,7 +207,7 @@ int sa_qk_norm_rope(const sa_problem* prob, int32_t n_rows, const void* q, int64
       A.axis_end[a] = (int)pairs;
     }
     if (pairs < 1) return SA_ERR_INVALID_ARG;
-    if (pairs % 8 != 0) return SA_ERR_UNSUPPORTED;
+    if (pairs % 8 != 0 && r.axes == 1) return SA_ERR_UNSUPPORTED;
     A.pairs = (int)pairs;
     A.layout = r.layout;
   }

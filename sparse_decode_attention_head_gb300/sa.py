@@ -501,7 +501,8 @@ class StepPlan:
 
 class Rope:
     """Rotary positions (sa_rope): dim pairs for each position axis and which
-    dims make a pair (ROPE_HALVES: j with j + R/2; ROPE_PAIRS: 2j with 2j + 1)."""
+    dims make a pair (ROPE_HALVES: j with j + R/2; ROPE_PAIRS: 2j with 2j + 1).
+    Several axes: pairs of any sum up to 64; one axis: a multiple of 8."""
 
     def __init__(self, axis_pairs: Sequence[int] = (HEAD_DIM // 2,), layout: int = ROPE_HALVES):
         self.axis_pairs, self.layout = [int(x) for x in axis_pairs], layout
