@@ -438,11 +438,15 @@ int sa_decode_step_bypass(const sa_problem* prob, const void* q,
  *     out; a page outside the pool records SA_ERR_BAD_PAGE and its tokens are
  *     left out.  A call with n_rows = 0 checks its arguments and launches
  *     nothing.
+ *   - A page table of 2^30 entries or more (B * max_pages_per_seq) gives
+ *     SA_ERR_UNSUPPORTED.
  *   - Their workspace has sa_rows_workspace_size bytes (one of
  *     max(sa_workspace_size, sa_rows_workspace_size) serves every call).  They
  *     use the problem's shapes and scale; selection settings play no part. */
 
-/* Workspace bytes of the packed-row and page calls (0 if prob is invalid). */
+/* Workspace bytes of the packed-row and page calls (0 if prob is invalid or
+ * its table too large): 51 MB for partial results, or four counts a page if
+ * that is more. */
 size_t sa_rows_workspace_size(const sa_problem* prob);
 
 /* which dims a rotation turns together */

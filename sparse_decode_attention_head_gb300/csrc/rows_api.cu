@@ -23,6 +23,14 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
+// Counts of table entries and loops over sequences are 32-bit on the device: a
+// table of 2^30 entries or more (4 GB) is refused by every call here.
+int make_params(const sa_problem* prob, Params* p) {
+  const int rc = sa_host::make_params(prob, p);
+  if (rc != SA_OK) return rc;
+  return (long long)p->B * p->mpp < (1ll << 30) ? SA_OK : SA_ERR_UNSUPPORTED;
+}
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
   return x < y + nb && y < x + na;
@@ -101,7 +109,7 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
                    const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets, const uint64_t* tree,
                    void* out, float* lse, void* ws, void* stream) {
   Params p;
-  int rc = sa_host::make_params(prob, &p);
+  int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (n_rows < 0) return SA_ERR_INVALID_ARG;
   if (!k_pool || !v_pool || !page_table || !seq_lens || !row_offsets || !ws) return SA_ERR_INVALID_ARG;
@@ -144,7 +152,7 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
 
 int page_args(const sa_problem* prob, const int32_t* table_in, const int32_t* keep, int32_t* table_out, int32_t* src,
               int32_t* dst, int32_t* counts, void* ws, Params* p, sa::PageArgs* A) {
-  const int rc = sa_host::make_params(prob, p);
+  const int rc = make_params(prob, p);
   if (rc != SA_OK) return rc;
   if (!table_in || !keep || !table_out || !src || !dst || !counts || !ws) return SA_ERR_INVALID_ARG;
   if (!aligned16(ws)) return SA_ERR_INVALID_ARG;
@@ -178,7 +186,7 @@ extern "C" {
 
 size_t sa_rows_workspace_size(const sa_problem* prob) {
   Params p;
-  if (sa_host::make_params(prob, &p) != SA_OK) return 0;
+  if (make_params(prob, &p) != SA_OK) return 0;
   return std::max(attn_layout().total, page_layout(p).total);
 }
 
@@ -188,7 +196,7 @@ int sa_qk_norm_rope(const sa_problem* prob, int32_t n_rows, const void* q, int64
                     const int32_t* positions_or_null, const int32_t* row_offsets, const int32_t* seq_lens,
                     const int32_t* page_table, void* q_out, void* k_pool, void* v_pool, void* ws, void* stream) {
   Params p;
-  int rc = sa_host::make_params(prob, &p);
+  int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (n_rows < 0 || !(eps >= 0.f) || !std::isfinite(eps)) return SA_ERR_INVALID_ARG;
   if (!row_offsets || !seq_lens || !page_table || !k_pool || !v_pool || !ws) return SA_ERR_INVALID_ARG;
@@ -275,7 +283,7 @@ int sa_accept_rows(const sa_problem* prob, void* k_pool, void* v_pool, const int
                    const int32_t* base_lens, const int32_t* path, int32_t max_path, const int32_t* path_cnt, void* ws,
                    void* stream) {
   Params p;
-  const int rc = sa_host::make_params(prob, &p);
+  const int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (!k_pool || !v_pool || !page_table || !base_lens || !path || !path_cnt || !ws) return SA_ERR_INVALID_ARG;
   if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(ws)) return SA_ERR_INVALID_ARG;
@@ -311,7 +319,7 @@ int sa_compact_pages(const sa_problem* prob, const int32_t* table_in, const int3
 int sa_copy_pages(const sa_problem* prob, void* k_pool, void* v_pool, const int32_t* src, const int32_t* dst,
                   const int32_t* count, int32_t max_pages, void* ws, void* stream) {
   Params p;
-  const int rc = sa_host::make_params(prob, &p);
+  const int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (!k_pool || !v_pool || !src || !dst || !count || !ws) return SA_ERR_INVALID_ARG;
   if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(ws)) return SA_ERR_INVALID_ARG;
