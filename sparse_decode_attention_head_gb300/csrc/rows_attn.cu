@@ -1089,8 +1089,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnAr
     if (i0 > 0) load(i0);
 #pragma unroll
     for (int k = 0; k < kMergeBatch; ++k) {
+      // a piece without weight is added too (its sums are zeros where the row saw
+      // nothing of it): a weight that underflows does not hide an infinite sum
       const float w = i0 + k < n ? s_ml[warp][i0 + k][j4].x : 0.f;
-      if (w == 0.f) continue;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         o[x].x = fmaf(v[k][x].x, w, o[x].x);
