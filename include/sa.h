@@ -28,6 +28,9 @@
  *   - Dtypes are fixed: Q, K, V and block summaries bf16 (passed as void*);
  *     scores, outputs, lse, logits and score tables fp32; indices, page tables,
  *     lengths and counts int32.  All tensors are dense, row-major, no padding.
+ *     The packed-row calls differ in three things, said there: their outputs
+ *     are bf16 (lse fp32), q, k and v of sa_qk_norm_rope may have any distance
+ *     between rows, and a tree's words are uint64.
  *   - Notation: B sequences, Hq query heads, Hk KV heads, G = Hq / Hk query
  *     heads per KV head (query head h uses KV head h / G), D = 128, P = page
  *     size (16), L = seq_lens[b] tokens in the cache INCLUDING the current
@@ -440,6 +443,14 @@ int sa_decode_step_bypass(const sa_problem* prob, const void* q,
  *     nothing.
  *   - A page table of 2^30 entries or more (B * max_pages_per_seq) gives
  *     SA_ERR_UNSUPPORTED.
+ *   - What the decode step keeps for a sequence (block summaries, kv_stats,
+ *     score tables) lies by the row of the table and is not moved by these
+ *     calls.  Behind sa_plan_pages the caller takes it from row parent[b], a
+ *     gather along B.  Summaries then hold for the blocks before keep[b] / Bs;
+ *     sa_block_summarize with block_begin = the lowest of them makes the rest
+ *     (with one new token a sequence the step's own refresh of the tail block
+ *     does).  kv_stats and score tables hold where keep[b] is all of the
+ *     parent's tokens.  Behind sa_accept_rows the same goes for base_lens.
  *   - Their workspace has sa_rows_workspace_size bytes (one of
  *     max(sa_workspace_size, sa_rows_workspace_size) serves every call).  They
  *     use the problem's shapes and scale; selection settings play no part. */
