@@ -524,6 +524,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           lim = p.a + p.first + tok + 1;
         }
       }
+      const float lag = valid ? kLag : INFINITY;   // a lane without a row never grows
       float m = -INFINITY, l = 0.f;
       for (int s = h; s < N; s += 2) {
         const int t = dual ? s : s >> 1;
@@ -581,7 +582,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         // a warp rescales together, each row by what it grew itself: a factor of one
         // for the others, whose bits depend on no neighbour, and no vote for lanes
         // without a row, which hold another sequence's queries or an earlier call's
-        const bool grow = valid && mx > m + kLag;
+        const bool grow = mx > m + lag;
         if (__any_sync(0xffffffffu, grow)) {
           const float alpha = grow ? ex2(m - mx) : 1.f;
           m = grow ? mx : m;
