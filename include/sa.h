@@ -482,9 +482,9 @@ typedef struct sa_rope {
  *                                            NULL: that one has no norm)
  *   pair j of axis a: angle = positions[a][i] * inv_freq[j],
  *   (x1, x2) <- (x1 cos - x2 sin, x2 cos + x1 sin)
- * in fp32, rounded to bf16 once; the angle is reduced to one turn from the
- * exact product of position and inv_freq (fp32 [R / 2]), so far positions
- * lose nothing.  q goes to q_out [n_rows][Hq][D], k and v to the row's
+ * in fp32, rounded to bf16 once; the angle is reduced to one turn from a
+ * product of position and inv_freq (fp32 [R / 2]) that is off by less than
+ * |position inv_freq| 2^-55 turns, so far positions keep their precision.  q goes to q_out [n_rows][Hq][D], k and v to the row's
  * position in the pools.  rope_or_null = NULL: no rotation.
  * positions_or_null: int32 [axes][n_rows], any values; NULL: the row's
  * position in the cache on every axis.
@@ -506,7 +506,8 @@ int sa_qk_norm_rope(const sa_problem* prob, int32_t n_rows, const void* q, int64
  *   out[row][h][:] = sum_t softmax(z)_t v_t (bf16), z_t = scale q.k_t,
  *   lse_or_null[row][h] = log sum_t e^{z_t} (fp32)
  * Products of bf16 in fp32 sums; the softmax weights are rounded to bf16 for
- * their product with V, the sum beneath them is of the unrounded ones.  A row
+ * their product with V (half a step, at most 2^-8 of each; sa_sparse_decode
+ * keeps about 16 bits), the sum beneath them is of the unrounded ones.  A row
  * that sees nothing gets out = 0, lse = -inf.  What a row does not see cannot
  * change it, whatever is stored there (NaN and infinities included).  out must
  * not overlap q. */

@@ -17,11 +17,12 @@
 // The angle: a frequency in turns is a 64-bit fraction F = frac(f / 2 pi) 2^64,
 // computed once a block in fp64, and position x F modulo 2^64 is the exact
 // fraction of a turn of that product; the top 32 bits, signed, go to
-// sincospi.  A far position therefore loses nothing, and no fp64 stands in
-// the loop over rows (its rate here is a fraction of fp32's).
+// sincospi.  What is lost is F's own rounding: position x frequency x 2^-55 of a
+// turn, 2^-24 at the farthest position with a frequency of one.  No fp64 stands
+// in the loop over rows (its rate here is a fraction of fp32's).
 //
 // Measured on one GB300: 65536 rows of 32 + 8 + 8 heads, norm and rotation,
-// 286 us, 5.6 TB/s (0.83 of a copy's rate; issue slots 59 % busy, which is what
+// 287 us, 5.6 TB/s (0.83 of a copy's rate; issue slots 59 % busy, which is what
 // is left to shorten); a row for each of 8 sequences 4.7 us.
 #include <algorithm>
 

@@ -33,7 +33,17 @@
 //
 // The running maximum is let lag: O and the sum are rescaled only when a row
 // maximum has grown by more than 2^8, which the fp32 sums and the bf16 of P
-// (whose relative precision does not depend on its size) hold with ease.
+// (whose relative precision does not depend on its size) hold with ease.  A row
+// is rescaled by its own growth alone, so its bits depend on the tiles and cuts
+// it is given, not on the values of other rows.
+//
+// The weights are rounded to bf16, the operand type of the tensor core, and
+// the sum beneath them is of the unrounded ones.  A second product with what
+// the rounding leaves (the decode step does that) would add half of the
+// kernel's matrix work; the rounding errors of thousands of weights average
+// out ahead of the one rounding of the result, which is to bf16 as well: the
+// error against 64 bits is 0.0017 of the norm with it and with fp32 weights
+// (16384 causal rows; trees at 32K).
 //
 // Masked places: a weight of zero times a non-finite V would be NaN, so in the
 // tiles that hold positions some row of the item does not see, V rows behind
@@ -45,10 +55,13 @@
 // thirds; S reads 8 KB of shared memory an instruction and runs slower than O,
 // and a group's softmax (0.8 us) and its matrix products do not overlap with
 // each other, only with the other group's.  The issuing warp stands between
-// them, so what it waits for is looked at once a step (1.40 ms in place of
-// 1.48).  16384 causal rows of 32 / 8 heads: 1.40 ms, 1.57 PFLOP/s.  2048 rows
-// behind 30K others: 1.63 PFLOP/s.  With one query tile the cache's bytes bound it:
-// 32 drafted tokens for each of 8 sequences of 32K: 178 us, 6.0 TB/s.
+// them, so what it waits for is looked at once a step (1.49 ms in place of
+// 1.56).  16384 causal rows of 32 / 8 heads: 1.43 ms, 1.54 PFLOP/s, for the first
+// 50 ms of a run (SM clock 2070 MHz), 1.50 ms, 1.46 PFLOP/s, under the power cap
+// of a longer one (1900 MHz); the same in calls and in graph replays.  2048 rows
+// behind 30K others: 0.68 ms, 1.56 PFLOP/s, and 0.72 ms, 1.48 PFLOP/s.  With one
+// query tile the cache's bytes bound it: 32 drafted tokens for each of 8
+// sequences of 32K: 177 us, 6.1 TB/s.
 // Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
 // interleave and both finish late); one barrier for all of a tile's weights
 // in place of one for each half (2 %); two threads a row (1.90 ms: 104
@@ -66,7 +79,10 @@ constexpr int kTileBytes = kRows * kD * 2;
 constexpr int kSlots = 5;                // K and V tiles in flight: what 227 KB leave beside two query tiles
 constexpr int kThreads = 384;
 // Registers a thread, out of the 168 the block is launched with: a row's 128
-// scores stay in the softmax threads' registers.
+// scores stay in the softmax threads' registers.  The compiler reports 80 bytes
+// of spill stores and 184 of loads, in the other warps at their 72 (fewer with
+// more there: none at 200 and 104; what that takes from the softmax is not
+// measured yet).
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
 // What work weighs: a KV token of an item with one query tile (bound by the
@@ -612,7 +628,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             p0 = ex2(p0);
             p1 = ex2(p1);
             sum[j & 1] = add2(sum[j & 1], pack2(p0, p1));
-            pw[j] = pack_bf16(p0, p1);
+            pw[j] = pack_bf16(p0, p1);      // half a step, 2^-9 to 2^-8, of each weight
           }
           tmem_st16(tS + 16 * q4, pw);
           if (q4 & 1) {   // half of the weights are there: their product may begin
