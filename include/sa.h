@@ -528,6 +528,49 @@ int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, con
                       const int32_t* row_offsets, const uint64_t* tree_mask, void* out, float* lse_or_null,
                       void* ws, void* stream);
 
+/* Rows behind a prefix that several sequences hold in the same pages (forked
+ * by sa_plan_pages: beams, samples of one prompt, conversations behind one
+ * system prompt).  Groups are neighbouring sequences: group g has those from
+ * group_offsets[g] to group_offsets[g + 1] - 1 (device int32 [n_groups + 1],
+ * non-decreasing; offsets that decrease or pass B are cut and record
+ * SA_ERR_INVALID_ARG).
+ *
+ * sa_shared_prefixes finds what each group shares: the longest run of leading
+ * table entries, all in the pool, that is the same for every sequence of the
+ * group that has rows, in whole pages ahead of all their rows.  Below
+ * min_tokens, or with fewer than two such sequences, it is none.
+ *   prefix_lens [B]: tokens of the group's prefix, a multiple of P; 0 for
+ *     sequences of no group.
+ *   members [B]: at the group's first sequence with rows, how many sequences
+ *     the group has from there on; 0 elsewhere and where nothing is shared.
+ * It reads the table alone, so one answer serves every layer of a step.
+ * Device errors as for other packed rows. */
+int sa_shared_prefixes(const sa_problem* prob, const int32_t* page_table, const int32_t* seq_lens,
+                       const int32_t* row_offsets, const int32_t* group_offsets, int32_t n_groups, int32_t min_tokens,
+                       int32_t* members, int32_t* prefix_lens, void* ws, void* stream);
+
+/* Workspace bytes of sa_shared_attention for up to max_rows rows (0 if prob is
+ * invalid, its table too large or max_rows negative); enough for every call
+ * that sa_rows_workspace_size serves too.  2 x (D + 2) x 4 bytes a row and
+ * head beyond that. */
+size_t sa_shared_workspace_size(const sa_problem* prob, int32_t max_rows);
+
+/* sa_prompt_attention, or with tree_mask sa_tree_attention, of rows behind
+ * shared prefixes: the same rows see the same positions, and the K and V of a
+ * group's prefix are read once for the rows of all its sequences, through the
+ * table row of the sequence that members names.  Prefix and own tokens are
+ * joined with the log-sum-exp identity in fp32; results are rounded to bf16
+ * once, as there.
+ * members and prefix_lens as sa_shared_prefixes writes them for the same
+ * table, lengths and offsets.  Written by hand they may name less than what is
+ * shared; a prefix_lens[b] that is negative, no multiple of P, or longer than
+ * what lies ahead of b's rows records SA_ERR_INVALID_ARG, and results of rows
+ * whose prefix no members entry covers are undefined. */
+int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
+                        const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
+                        const int32_t* row_offsets, const uint64_t* tree_mask_or_null, const int32_t* members,
+                        const int32_t* prefix_lens, void* out, float* lse_or_null, void* ws, void* stream);
+
 /* Takes over the accepted nodes of a tree: for every sequence b the K and V
  * rows at positions base_lens[b] + path[b][i] move to base_lens[b] + i,
  * i < path_cnt[b].  base_lens: tokens before the draft; path [B][max_path]

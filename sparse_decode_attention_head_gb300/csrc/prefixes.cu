@@ -1,0 +1,115 @@
+// What neighbouring sequences hold in the same pages (sa_shared_prefixes).
+//
+// A group's prefix is the longest run of leading table entries that every
+// member with rows has in common, in whole pages ahead of all their rows.  It
+// is found from the table alone: pages have no other owner than its rows, so
+// equal entries are the same tokens.
+//
+// A cluster of eight blocks takes a group: each block compares some members'
+// entries with the first member's, a stretch of pages at a time, and keeps the
+// first place where one differs; the eight answers are joined through
+// distributed shared memory.  A stretch behind a difference is not read.
+// Bound by the latency of its reads: offsets and lengths, then entries, then
+// the exchange.
+#include <cooperative_groups.h>
+
+#include <climits>
+
+#include "rows.cuh"
+
+namespace sa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kCluster = 8, kThreads = 256, kStretch = 4;   // entries a thread has in flight
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+shared_prefixes_kernel(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,
+                       int n_groups, int min_tokens, int* members, int* prefix_lens, int B, int mpp, int num_pages,
+                       int* status) {
+  __shared__ int s_first, s_with, s_pages, s_answer;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), g = blockIdx.x / kCluster;
+  pdl_wait();
+  pdl_trigger();
+  int b0 = B, b1 = B;
+  if (g < n_groups) {
+    const int o0 = __ldg(group_offsets + g), o1 = __ldg(group_offsets + g + 1);
+    b0 = min(max(o0, 0), B);
+    b1 = min(max(o1, b0), B);
+    if ((b0 != o0 || b1 != o1) && rank == 0 && tid == 0) set_status(status, SA_ERR_INVALID_ARG);
+  } else {   // the cluster behind the last group: sequences of none
+    const int lo = n_groups > 0 ? __ldg(group_offsets) : B, hi = n_groups > 0 ? __ldg(group_offsets + n_groups) : B;
+    for (int b = rank * kThreads + tid; b < B; b += kCluster * kThreads) {
+      if (b >= lo && b < hi) continue;
+      members[b] = 0;
+      prefix_lens[b] = 0;
+    }
+    return;   // all of the cluster
+  }
+  if (tid == 0) {
+    s_first = INT_MAX;
+    s_with = 0;
+    s_pages = mpp;
+  }
+  __syncthreads();
+  // the first member with rows, how many have some, and the whole pages ahead of all their rows
+  for (int b = b0 + tid; b < b1; b += kThreads) {
+    const RowSeq s = row_seq(row_offsets, seq_lens, b, INT_MAX, mpp, rank == 0 ? status : nullptr);
+    if (s.n == 0) continue;
+    atomicMin(&s_first, b);
+    atomicAdd(&s_with, 1);
+    atomicMin(&s_pages, max(s.a, 0) / kP);
+  }
+  __syncthreads();
+  const int first = s_first;
+  const int most = s_with > 1 ? s_pages : 0;
+  __syncthreads();
+  // s_pages becomes the first place at which a member of this block differs
+  if (first < b1) {
+    const int* mine = table + (size_t)first * mpp;
+    for (int b = first + rank; b < b1; b += kCluster) {
+      if (__ldg(row_offsets + b + 1) <= max(__ldg(row_offsets + b), 0)) continue;
+      const int* theirs = table + (size_t)b * mpp;
+      for (int j0 = 0; j0 < most; j0 += kStretch * kThreads) {
+        if (j0 >= *(volatile int*)&s_pages) break;
+        int x[kStretch], y[kStretch];
+#pragma unroll
+        for (int e = 0; e < kStretch; ++e) {
+          const int j = j0 + e * kThreads + tid;
+          x[e] = j < most ? __ldg(mine + j) : 0;
+          y[e] = j < most ? __ldg(theirs + j) : 0;
+        }
+#pragma unroll
+        for (int e = kStretch - 1; e >= 0; --e)
+          if (x[e] != y[e] || x[e] < 0 || x[e] >= num_pages) atomicMin(&s_pages, j0 + e * kThreads + tid);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) s_answer = min(most, s_pages);
+  cluster.sync();
+  int pages = most;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) pages = min(pages, *cluster.map_shared_rank(&s_answer, r));
+  const int prefix = pages * kP >= min_tokens ? pages * kP : 0;
+  for (int b = b0 + rank * kThreads + tid; b < b1; b += kCluster * kThreads) {
+    members[b] = b == first && prefix > 0 ? b1 - first : 0;
+    prefix_lens[b] = prefix;
+  }
+  cluster.sync();   // the others' answers are there until all have read them
+}
+
+}  // namespace
+
+int launch_shared_prefixes(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,
+                           int n_groups, int min_tokens, int* members, int* prefix_lens, int B, int mpp, int num_pages,
+                           int* status, cudaStream_t stream) {
+  const cudaError_t e = launch_pdl(shared_prefixes_kernel, dim3((n_groups + 1) * kCluster), dim3(kThreads), 0, stream,
+                                   table, seq_lens, row_offsets, group_offsets, n_groups, min_tokens, members,
+                                   prefix_lens, B, mpp, num_pages, status);
+  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // namespace sa

@@ -33,6 +33,30 @@ __device__ __forceinline__ RowSeq row_seq(const int* row_offsets, const int* seq
   return s;
 }
 
+// Sequence b's tokens in the pages of its group's prefix: whole pages ahead of
+// its rows, or none where the number is not that (a sequence without rows has
+// none to give).
+__device__ __forceinline__ int shared_prefix(const int* prefix_lens, int b, const RowSeq& s, int mpp, int* status) {
+  if (s.n == 0) return 0;
+  const int x = __ldg(prefix_lens + b);
+  if (x >= 0 && x % kP == 0 && x <= s.a && x <= mpp * kP) return x;
+  if (status != nullptr) set_status(status, SA_ERR_INVALID_ARG);
+  return 0;
+}
+
+// The rows of the members[b] sequences from b on, over the first prefix_lens[b]
+// tokens of b: all of them see all of these (a = L, as of rows behind them).
+__device__ __forceinline__ RowSeq shared_rows(const int* row_offsets, const int* members, const int* prefix_lens,
+                                              int B, int b, int n_rows, int mpp) {
+  const int m = min(__ldg(members + b), B - b), x = __ldg(prefix_lens + b), o0 = __ldg(row_offsets + b);
+  RowSeq s{0, 0, 0, 0};
+  if (m <= 0 || x <= 0 || x % kP != 0 || x > mpp * kP) return s;
+  s.row0 = min(max(o0, 0), n_rows);
+  s.n = min(max(__ldg(row_offsets + b + m), s.row0), n_rows) - s.row0;
+  s.a = s.L = x;
+  return s;
+}
+
 // ---------------------------------------------------------------- attention
 
 constexpr int kRowsMaxCtas = 192;   // one block an SM; bounds the workspace
@@ -49,6 +73,11 @@ struct RowsAttnArgs {
   float2* part_ml;                  // [cta][2][2][128] (maximum, sum), base 2
   int4* desc;                       // [cta][2] what the partials are of
   int* status;
+  // shared prefixes only
+  const int* members;               // [B] sequences of the group that b leads, 0 elsewhere
+  const int* prefix_lens;           // [B] tokens of the group's prefix
+  float* half;                      // [2][n_rows][Hq][kD] sums over the prefix and over a sequence's own tokens
+  float2* half_ml;                  // [2][n_rows][Hq] (maximum, sum), base 2
   int n_rows, B, Hq, Hk, G, mpp, num_pages;
   int tpt;                          // tokens of a query tile: 128 / G
   float scale_log2;                 // scale log2(e)
@@ -56,6 +85,12 @@ struct RowsAttnArgs {
 
 int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           int num_sms, cudaStream_t stream);
+int launch_shared_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                            const CUtensorMap& tmV, int num_sms, cudaStream_t stream);
+
+int launch_shared_prefixes(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,
+                           int n_groups, int min_tokens, int* members, int* prefix_lens, int B, int mpp, int num_pages,
+                           int* status, cudaStream_t stream);
 
 // ---------------------------------------------------------------- rotation
 

@@ -55,6 +55,22 @@ AttnLayout attn_layout() {
   return l;
 }
 
+// The two parts of rows behind a shared prefix, behind the partials.
+struct SharedLayout {
+  size_t ml, half, total;
+};
+SharedLayout shared_layout(const Params& p, int n_rows) {
+  const size_t rows = 2 * (size_t)n_rows * p.Hq;
+  SharedLayout l;
+  size_t off = attn_layout().total;
+  l.ml = off;
+  off = up(off + rows * sizeof(float2));
+  l.half = off;
+  off = up(off + rows * sa::kD * sizeof(float));
+  l.total = off;
+  return l;
+}
+
 struct PageLayout {
   size_t refs, list, chunk, need, total;
 };
@@ -105,10 +121,20 @@ int make_tile_map(CUtensorMap* m, const void* pool, const Params& p) {
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
-int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool, const void* v_pool,
-                   const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets, const uint64_t* tree,
-                   void* out, float* lse, void* ws, void* stream) {
+// The checks and arguments that the attention calls share; *launch says whether
+// there is anything to do.
+struct AttnCall {
   Params p;
+  sa::RowsAttnArgs A;
+  CUtensorMap tmQ, tmK, tmV;
+  int nsm;
+  bool launch;
+};
+int attention_args(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool, const void* v_pool,
+                   const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets, void* out, float* lse,
+                   void* ws, AttnCall* c) {
+  Params& p = c->p;
+  c->launch = false;
   int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (n_rows < 0) return SA_ERR_INVALID_ARG;
@@ -119,20 +145,19 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
     return SA_ERR_INVALID_ARG;
   const size_t row_bytes = (size_t)n_rows * p.Hq * SA_HEAD_DIM * 2;
   if (overlap(q, row_bytes, out, row_bytes)) return SA_ERR_INVALID_ARG;
-  const int nsm = sa_host::num_sms_current();
-  if (nsm <= 0) return SA_ERR_CUDA;
-  sa::RowsAttnArgs A{};
+  c->nsm = sa_host::num_sms_current();
+  if (c->nsm <= 0) return SA_ERR_CUDA;
+  sa::RowsAttnArgs& A = c->A;
+  A = sa::RowsAttnArgs{};
   A.tpt = 128 / p.G;
-  CUtensorMap tmQ, tmK, tmV;
-  if ((rc = make_q_map(&tmQ, q, n_rows, p, A.tpt)) != SA_OK) return rc;
-  if ((rc = make_tile_map(&tmK, k_pool, p)) != SA_OK) return rc;
-  if ((rc = make_tile_map(&tmV, v_pool, p)) != SA_OK) return rc;
+  if ((rc = make_q_map(&c->tmQ, q, n_rows, p, A.tpt)) != SA_OK) return rc;
+  if ((rc = make_tile_map(&c->tmK, k_pool, p)) != SA_OK) return rc;
+  if ((rc = make_tile_map(&c->tmV, v_pool, p)) != SA_OK) return rc;
   const AttnLayout l = attn_layout();
   A.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
   A.page_table = page_table;
   A.seq_lens = seq_lens;
   A.row_offsets = row_offsets;
-  A.tree = reinterpret_cast<const unsigned long long*>(tree);
   A.out = static_cast<__nv_bfloat16*>(out);
   A.lse = lse;
   A.part = at<float>(ws, l.part);
@@ -147,7 +172,19 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
   A.mpp = p.mpp;
   A.num_pages = p.num_pages;
   A.scale_log2 = p.scale * 1.4426950408889634f;
-  return sa::launch_rows_attention(A, tmQ, tmK, tmV, nsm, as_stream(stream));
+  c->launch = true;
+  return SA_OK;
+}
+
+int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool, const void* v_pool,
+                   const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets, const uint64_t* tree,
+                   void* out, float* lse, void* ws, void* stream) {
+  AttnCall c;
+  const int rc =
+      attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, &c);
+  if (rc != SA_OK || !c.launch) return rc;
+  c.A.tree = reinterpret_cast<const unsigned long long*>(tree);
+  return sa::launch_rows_attention(c.A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));
 }
 
 int page_args(const sa_problem* prob, const int32_t* table_in, const int32_t* keep, int32_t* table_out, int32_t* src,
@@ -277,6 +314,44 @@ int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, con
   if (tree_mask == nullptr && n_rows != 0) return SA_ERR_INVALID_ARG;
   return rows_attention(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, tree_mask, out, lse_or_null,
                         ws, stream);
+}
+
+size_t sa_shared_workspace_size(const sa_problem* prob, int32_t max_rows) {
+  Params p;
+  if (make_params(prob, &p) != SA_OK || max_rows < 0) return 0;
+  return std::max(sa_rows_workspace_size(prob), shared_layout(p, max_rows).total);
+}
+
+int sa_shared_prefixes(const sa_problem* prob, const int32_t* page_table, const int32_t* seq_lens,
+                       const int32_t* row_offsets, const int32_t* group_offsets, int32_t n_groups, int32_t min_tokens,
+                       int32_t* members, int32_t* prefix_lens, void* ws, void* stream) {
+  Params p;
+  const int rc = make_params(prob, &p);
+  if (rc != SA_OK) return rc;
+  if (!page_table || !seq_lens || !row_offsets || !group_offsets || !members || !prefix_lens || !ws)
+    return SA_ERR_INVALID_ARG;
+  if (!aligned16(ws) || n_groups < 0 || n_groups > p.B) return SA_ERR_INVALID_ARG;
+  return sa::launch_shared_prefixes(page_table, seq_lens, row_offsets, group_offsets, n_groups, min_tokens, members,
+                                    prefix_lens, p.B, p.mpp, p.num_pages, at<int>(ws, 0), as_stream(stream));
+}
+
+int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool, const void* v_pool,
+                        const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets,
+                        const uint64_t* tree_mask_or_null, const int32_t* members, const int32_t* prefix_lens, void* out,
+                        float* lse_or_null, void* ws, void* stream) {
+  AttnCall c;
+  const int rc =
+      attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse_or_null, ws, &c);
+  if (rc != SA_OK) return rc;
+  if (!members || !prefix_lens) return SA_ERR_INVALID_ARG;
+  if (!c.launch) return SA_OK;
+  const SharedLayout l = shared_layout(c.p, n_rows);
+  c.A.tree = reinterpret_cast<const unsigned long long*>(tree_mask_or_null);
+  c.A.members = members;
+  c.A.prefix_lens = prefix_lens;
+  c.A.half = at<float>(ws, l.half);
+  c.A.half_ml = at<float2>(ws, l.ml);
+  return sa::launch_shared_attention(c.A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));
 }
 
 int sa_accept_rows(const sa_problem* prob, void* k_pool, void* v_pool, const int32_t* page_table,

@@ -93,6 +93,12 @@ constexpr float kLag = 8.f;              // log2 of the growth of a row maximum 
 
 enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
 
+// What the kernel attends to, an instance each.
+enum Kind {
+  kPlain,     // prompts and trees, each sequence over all of its cache
+  kShared,    // the same, with the prefix of a group of sequences as an item of its own
+};
+
 // A piece of a block's run: KV tiles [k0, k1) of one item.  The loading warp
 // walks the run and hands the pieces to the other roles through a ring.
 struct Piece {
@@ -103,6 +109,8 @@ struct Piece {
   int end, edge;      // item_end, item_edge
   int a;              // tokens of the sequence ahead of its rows
   int first;          // the item's first row in the sequence
+  int to;             // Part: where the result goes
+  long long pt;       // entry of the page table with the item's position 0
   bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
 };
 
@@ -198,15 +206,49 @@ struct Ring {
 
 // ---------------------------------------------------------------- the items
 
+// What a sequence's rows are over: all they see, or one of two parts that
+// rows_join_kernel puts together.
+enum Part { kAll, kPrefix, kOwn };
+
 struct Seq : RowSeq {
   int items;      // of one KV head
   int T;          // tokens of an item
+  int to;         // Part
+  long long pt;   // entry of the page table with position 0
 };
 
-__device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int b, int* status) {
+// Sequence v.  With prefixes of groups (kShared) there are two for each of the
+// batch: 2 b, the rows of the group that b leads over its prefix (all of them
+// see all of it), and 2 b + 1, b's rows over what is behind the prefix; both
+// count positions from their own first token.
+template <int KIND>
+__device__ __forceinline__ int sequences(const RowsAttnArgs& A) {
+  return KIND == kShared ? 2 * A.B : A.B;
+}
+template <int KIND>
+__device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int v, int* status) {
+  const int b = KIND == kShared ? v >> 1 : v;
   Seq s;
-  static_cast<RowSeq&>(s) = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, status);
   s.T = 2 * A.tpt;
+  s.to = kAll;
+  s.pt = (long long)b * A.mpp;
+  if (KIND == kShared && (v & 1) == 0) {
+    const RowSeq g = shared_rows(A.row_offsets, A.members, A.prefix_lens, A.B, b, A.n_rows, A.mpp);
+    static_cast<RowSeq&>(s) = g;
+    s.to = kPrefix;
+    s.items = (s.n + s.T - 1) / s.T;
+    return s;
+  }
+  static_cast<RowSeq&>(s) = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, status);
+  if (KIND == kShared) {
+    const int x = shared_prefix(A.prefix_lens, b, s, A.mpp, status);
+    if (x > 0) {
+      s.to = kOwn;
+      s.pt += x / kP;
+      s.a -= x;
+      s.L -= x;
+    }
+  }
   s.items = (s.n + s.T - 1) / s.T;
   if (A.tree != nullptr && s.n > kMaxTree) {
     if (status != nullptr) set_status(status, SA_ERR_CAPACITY);
@@ -233,25 +275,27 @@ __device__ __forceinline__ int tiles_of(int end) { return (end + kRows - 1) / kR
 __device__ __forceinline__ long long weight_before(const RowsAttnArgs& A, const Seq& s, int k) {
   if (k == 0) return 0;
   const int full = min(k, s.items - 1);
-  const long long before = max(A.tree != nullptr ? s.L : s.a, 0);
-  long long w = (before * full + (A.tree != nullptr ? 0 : (long long)s.T * full * (full + 1) / 2)) * kTwoCost +
+  const bool flat = A.tree != nullptr || s.to == kPrefix;     // all rows see about the same
+  const long long before = max(flat ? s.L : s.a, 0);
+  long long w = (before * full + (flat ? 0 : (long long)s.T * full * (full + 1) / 2)) * kTwoCost +
                 (long long)k * kItemCost;
   if (k == s.items) {
     const int tokens = s.n - full * s.T;
-    w += (before + (A.tree != nullptr ? 0 : s.n)) * (tokens <= A.tpt ? kOneCost : kTwoCost);
+    w += (before + (flat ? 0 : s.n)) * (tokens <= A.tpt ? kOneCost : kTwoCost);
   }
   return w;
 }
 
 // One warp: the total weight of all items.  `s` and `mine` are the lane's own
 // sequence, of the first 32, and its weight.
+template <int KIND>
 __device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* status, Seq& s, long long& mine) {
   const int lane = threadIdx.x & 31;
   long long w = 0;
   mine = 0;
   s = Seq{};
-  for (int b = lane; b < A.B; b += 32) {
-    const Seq x = load_seq(A, b, status);
+  for (int b = lane; b < sequences<KIND>(A); b += 32) {
+    const Seq x = load_seq<KIND>(A, b, status);
     const long long m = weight_before(A, x, x.items) * A.Hk;
     w += m;
     if (b < 32) {
@@ -264,17 +308,17 @@ __device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* st
   return w;
 }
 
-// One warp: the item and KV tile at weight w (the end: sequence B).
-template <typename T>
+// One warp: the item and KV tile at weight w (the end: a sequence behind the last).
+template <int KIND, typename T>
 __device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, n_seq = sequences<KIND>(A);
   T before = 0;
-  for (int b0 = 0; b0 < A.B; b0 += 32) {
+  for (int b0 = 0; b0 < n_seq; b0 += 32) {
     const int b = b0 + lane;
     if (b0 > 0) {
       mine = 0;
-      if (b < A.B) {
-        s = load_seq(A, b, nullptr);
+      if (b < n_seq) {
+        s = load_seq<KIND>(A, b, nullptr);
         mine = (T)weight_before(A, s, s.items) * A.Hk;
       }
     }
@@ -311,18 +355,19 @@ __device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine
     r.w = __shfl_sync(0xffffffffu, r.w, src);
     return r;
   }
-  return make_int4(A.B, 0, 0, 0);
+  return make_int4(n_seq, 0, 0, 0);
 }
 
 // Little work: every block takes one item or an equal part of one, of two KV
-// tiles or four, and none takes two.  `s` as above (B <= 32).  Answers false
+// tiles or four, and none takes two.  `s` as above (at most 32 sequences).  Answers false
 // where the blocks do not suffice for that.
 __device__ __forceinline__ int runs_of(const RowsAttnArgs& A, const Seq& s, int i, int tiles) {
   return max(1, (tiles_of(item_end(A, s, i)) + tiles - 1) / tiles);
 }
+template <int KIND>
 __device__ __forceinline__ bool locate_small(const RowsAttnArgs& A, int run, int blocks, const Seq& s, int4& r) {
   const int lane = threadIdx.x & 31;
-  if (A.B > 32) return false;
+  if (sequences<KIND>(A) > 32) return false;
   auto sum = [](int x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -339,7 +384,7 @@ __device__ __forceinline__ bool locate_small(const RowsAttnArgs& A, int run, int
     if (tiles == 4) return false;
     tiles = 4;
   }
-  r = make_int4(A.B, 0, 0, 0);
+  r = make_int4(sequences<KIND>(A), 0, 0, 0);
   const int upto = warp_incl_scan(mine);
   const unsigned hit = __ballot_sync(0xffffffffu, run < upto);
   if (hit == 0) return true;
@@ -364,6 +409,7 @@ __device__ __forceinline__ bool locate_small(const RowsAttnArgs& A, int run, int
 }
 
 // One thread walks a block's run, piece by piece.
+template <int KIND>
 struct Walk {
   const RowsAttnArgs& A;
   int b, kvh, i, kt;
@@ -374,8 +420,8 @@ struct Walk {
     const int4 r = c->range[0];
     b = r.x; kvh = r.y; i = r.z; kt = r.w;
     end = c->range[1];
-    done = b >= A.B;
-    if (!done) s = load_seq(A, b, nullptr);
+    done = b >= sequences<KIND>(A);
+    if (!done) s = load_seq<KIND>(A, b, nullptr);
   }
   __device__ bool next(Piece& p) {
     while (!done) {
@@ -387,6 +433,8 @@ struct Walk {
       p.k0 = kt;
       p.k1 = at_end ? end.w : p.nt;
       p.a = s.a;
+      p.to = s.to;
+      p.pt = s.pt;
       p.first = i * s.T;
       p.row0 = s.row0 + i * s.T;
       p.tokens = min(s.T, s.n - i * s.T);
@@ -400,8 +448,8 @@ struct Walk {
         if (++kvh == A.Hk) {
           kvh = 0;
           do {
-            if (++b >= A.B) { done = true; break; }
-            s = load_seq(A, b, nullptr);
+            if (++b >= sequences<KIND>(A)) { done = true; break; }
+            s = load_seq<KIND>(A, b, nullptr);
           } while (s.items == 0);
         }
       }
@@ -425,7 +473,8 @@ struct EdgeRow {
   unsigned long long word;
   int t0, t1, lim, a;           // sees t < lim, and bit t - a of word
 };
-__device__ __noinline__ void add_poison(const RowsAttnArgs& A, EdgeRow e, int kvh, __nv_bfloat16* out, float* part) {
+__device__ __noinline__ void add_poison(const RowsAttnArgs& A, EdgeRow e, int kvh, __nv_bfloat16* out, float* part,
+                                        int step) {   // part: dims in fours, `step` values apart
   for (int t = e.t0; t < e.t1; ++t) {
     const int bit = t - e.a;
     if (!(t < e.lim || (bit >= 0 && bit < 64 && ((e.word >> bit) & 1ull)))) continue;
@@ -436,7 +485,25 @@ __device__ __noinline__ void add_poison(const RowsAttnArgs& A, EdgeRow e, int kv
       const float x = __bfloat162float(v[d]);
       if (isfinite(x)) continue;
       if (out != nullptr) out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
-      else part[(d >> 2) * (4 * kRows) + (d & 3)] += x;
+      else part[(d >> 2) * step + (d & 3)] += x;
+    }
+  }
+}
+
+// Four neighbouring lanes exchange 16-byte pieces: lane l's piece j for lane
+// j's piece l, so that each row's pieces lie in four lanes.
+__device__ __forceinline__ void swap_rows4(uint32_t (&x)[4][4], int lane) {
+#pragma unroll
+  for (int step = 1; step <= 2; step <<= 1) {
+    const bool upper = lane & step;
+#pragma unroll
+    for (int a0 = 0; a0 < 4; ++a0) {
+      if (a0 & step) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[a0][j] : x[a0 + step][j], step);
+        if (upper) x[a0][j] = got; else x[a0 + step][j] = got;
+      }
     }
   }
 }
@@ -447,6 +514,7 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
 
 // ---------------------------------------------------------------- the kernel
 
+template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
@@ -494,13 +562,13 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   if (warp < 2) {   // where this block's run begins (warp 0) and ends (warp 1)
     Seq s;
     long long mine;
-    const long long W = total_weight(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr, s, mine);
+    const long long W = total_weight<KIND>(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr, s, mine);
     int4 r;
-    if (locate_small(A, blockIdx.x + warp, gridDim.x, s, r)) {
+    if (locate_small<KIND>(A, blockIdx.x + warp, gridDim.x, s, r)) {
     } else if (W < (1ll << 32) / kRowsMaxCtas) {     // in 32 bits, whose divisions are short
-      r = locate<uint32_t>(A, (uint32_t)W * (blockIdx.x + warp) / gridDim.x, s, (uint32_t)mine);
+      r = locate<KIND, uint32_t>(A, (uint32_t)W * (blockIdx.x + warp) / gridDim.x, s, (uint32_t)mine);
     } else {
-      r = locate<long long>(A, W * (blockIdx.x + warp) / gridDim.x, s, mine);
+      r = locate<KIND, long long>(A, W * (blockIdx.x + warp) / gridDim.x, s, mine);
     }
     if (lane == 0) c->range[warp] = r;
   }
@@ -671,11 +739,15 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         const float M = two ? fmaxf(m, m1) : m;
         const float w0 = l == 0.f ? 0.f : two ? ex2(m - M) : 1.f, w1 = two && l1 != 0.f ? ex2(m1 - M) : 0.f;
         const float lt = l * w0 + (two ? l1 * w1 : 0.f);
-        const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
+        // a whole item's rows are done; those of a part of two wait for the other, as 32-bit sums
+        const bool final_out = whole && (KIND != kShared || p.to == kAll);
+        const float inv = final_out ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
         const int which = p.k0 > 0 ? 0 : 1;
         const size_t slot = ((size_t)blockIdx.x * 2 + which) * 2 + h;
         float* part = A.part + slot * kRows * kD + 4 * r;     // [dims / 4][row][4]
         const long long row = (long long)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
+        const size_t half_row = KIND == kShared ? (p.to == kOwn ? (size_t)A.n_rows * A.Hq : 0) + row : 0;
+        float* half = KIND == kShared ? A.half + half_row * kD : nullptr;
         // a row's result lies in one lane: four lanes exchange theirs, so that
         // a store covers 64 bytes of each of 8 rows and not 16 of 32
         long long rows4[4];
@@ -700,28 +772,29 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = fmaf(o1[j], f1, o[j]);
           }
-          if (whole) {
-            uint32_t x[4][4];     // pieces of 16 bytes; then row j's piece lane % 4
+          if (final_out) {
+            uint32_t x[4][4];
 #pragma unroll
             for (int j = 0; j < 16; ++j) x[j >> 2][j & 3] = pack_bf16(o[2 * j], o[2 * j + 1]);
-#pragma unroll
-            for (int step = 1; step <= 2; step <<= 1) {
-              const bool upper = lane & step;
-#pragma unroll
-              for (int a0 = 0; a0 < 4; ++a0) {
-                if (a0 & step) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[a0][j] : x[a0 + step][j], step);
-                  if (upper) x[a0][j] = got; else x[a0 + step][j] = got;
-                }
-              }
-            }
+            swap_rows4(x, lane);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (rows4[j] >= 0)
                 reinterpret_cast<uint4*>(A.out + rows4[j] * kD + 32 * q4)[lane & 3] =
                     make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+          } else if (KIND == kShared && whole) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t x[4][4];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j >> 2][j & 3] = __float_as_uint(o[16 * e + j]);
+              swap_rows4(x, lane);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (rows4[j] >= 0)
+                  reinterpret_cast<uint4*>(A.half + (half_row - row + rows4[j]) * kD + 32 * q4 + 16 * e)[lane & 3] =
+                      make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -732,11 +805,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         if (poisoned) {
           __syncwarp();     // the row was stored by its neighbours too
           if (valid)
-            add_poison(A, EdgeRow{A.page_table + (size_t)p.b * A.mpp, word, max(p.edge, p.k0 * kRows),
-                                  min(p.end, p.k1 * kRows), lim, p.a},
-                       p.kvh, whole ? A.out + row * kD : nullptr, whole ? nullptr : part);
+            add_poison(A, EdgeRow{A.page_table + p.pt, word, max(p.edge, p.k0 * kRows), min(p.end, p.k1 * kRows), lim, p.a},
+                       p.kvh, final_out ? A.out + row * kD : nullptr, whole ? half : part, whole ? 4 : 4 * kRows);
         }
-        if (whole) {
+        if (KIND == kShared && whole && !final_out) {
+          if (valid) A.half_ml[half_row] = make_float2(M, lt);
+        } else if (whole) {
           if (valid && A.lse != nullptr) A.lse[row] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.693147180559945309f;
         } else {
           if (valid) A.part_ml[slot * kRows + r] = make_float2(M, lt);
@@ -903,7 +977,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       uint32_t tile = 0, pieces = 0, loads = 0;
       const uint32_t q_bytes = (uint32_t)(A.tpt * A.G) * kD * 2;
       bool ok = true;
-      Walk walk(A, c);
+      Walk<KIND> walk(A, c);
       for (int piece = 0;; ++piece) {
         Piece p;
         if (!walk.next(p)) p.k0 = p.k1 = -1;
@@ -926,7 +1000,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         }
         ++pieces;
         // a lane a page of the tile; the next tile's pages are looked up while this one's are copied
-        const int* pt = A.page_table + (size_t)p.b * A.mpp;
+        const int* pt = A.page_table + p.pt;
         auto page_of = [&](int t) {
           const int page = (p.k0 + t) * (kRows / kP) + lane;
           return lane < kRows / kP && page * kP < p.end ? __ldg(pt + page) : -1;
@@ -1033,6 +1107,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 // rows, eight lanes a row.  Bound by latency: what the pieces are is one look
 // at all of them, and no load waits for another's value after that.
 constexpr int kMergeWarps = 4, kMergeRows = 4 * kMergeWarps, kMergeBatch = 4;
+template <int KIND>
 __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnArgs A) {
   __shared__ int s_last;
   __shared__ unsigned s_there[kRowsMaxCtas / 32 + 1];
@@ -1079,7 +1154,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnAr
     }
   };
   load(0);
-  const Seq s = load_seq(A, d.x, nullptr);
+  const Seq s = load_seq<KIND>(A, d.x, nullptr);
   float M = -INFINITY;
   for (int i = part; i < n; i += 8) {
     const size_t slot = ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * 2 + half;
@@ -1123,6 +1198,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnAr
   if (t_row >= A.tpt || tok >= s.n) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t row = (size_t)(s.row0 + tok) * A.Hq + (size_t)d.y * A.G + g;
+  if (KIND == kShared && s.to != kAll) {
+    const size_t half_row = (s.to == kOwn ? (size_t)A.n_rows * A.Hq : 0) + row;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) reinterpret_cast<float4*>(A.half + half_row * kD)[8 * x + part] = o[x];
+    if (part == 0) A.half_ml[half_row] = make_float2(M, l);
+    return;
+  }
 #pragma unroll
   for (int x = 0; x < 4; ++x)
     reinterpret_cast<uint2*>(A.out + row * kD)[8 * x + part] =
@@ -1130,16 +1212,68 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnAr
   if (part == 0 && A.lse != nullptr) A.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
 }
 
+// Joins the two parts of rows behind a shared prefix.  A block takes a packed
+// row, a warp each of its heads in turn; rows that had no prefix are done.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32) rows_join_kernel(RowsAttnArgs A) {
+  pdl_wait();
+  pdl_trigger();
+  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the row's sequence: the last whose rows begin at or ahead of it
+  int lo = 0, hi = A.B;      // row_offsets[lo] <= row < row_offsets[hi]
+  if (row < __ldg(A.row_offsets) || row >= __ldg(A.row_offsets + A.B)) return;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + step * (lane + 1);
+    const unsigned up = __ballot_sync(0xffffffffu, at < hi && __ldg(A.row_offsets + at) <= row);
+    const int n = __popc(up);
+    hi = min(hi, lo + step * (n + 1));
+    lo += step * n;
+  }
+  const RowSeq s = row_seq(A.row_offsets, A.seq_lens, lo, A.n_rows, A.mpp, nullptr);
+  if (row < s.row0 || row >= s.row0 + s.n || shared_prefix(A.prefix_lens, lo, s, A.mpp, nullptr) == 0) return;
+  if (A.tree != nullptr && s.n > kMaxTree) return;
+  const size_t own = (size_t)A.n_rows * A.Hq;
+  for (int h = warp; h < A.Hq; h += kJoinWarps) {
+    const size_t r = (size_t)row * A.Hq + h;
+    const float4 a = reinterpret_cast<const float4*>(A.half + r * kD)[lane];
+    const float4 b = reinterpret_cast<const float4*>(A.half + (own + r) * kD)[lane];
+    const float2 ma = A.half_ml[r], mb = A.half_ml[own + r];
+    const float M = ma.y == 0.f ? mb.x : mb.y == 0.f ? ma.x : fmaxf(ma.x, mb.x);
+    const float wa = ma.y == 0.f ? 0.f : ex2(ma.x - M), wb = mb.y == 0.f ? 0.f : ex2(mb.x - M);
+    const float l = wa * ma.y + wb * mb.y;
+    const float inv = l == 0.f ? 0.f : 1.f / l, fa = wa * inv, fb = wb * inv;
+    reinterpret_cast<uint2*>(A.out + r * kD)[lane] =
+        make_uint2(pack_bf16(fmaf(a.x, fa, b.x * fb), fmaf(a.y, fa, b.y * fb)),
+                   pack_bf16(fmaf(a.z, fa, b.z * fb), fmaf(a.w, fa, b.w * fb)));
+    if (lane == 0 && A.lse != nullptr) A.lse[r] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
+  }
+}
+
+template <int KIND>
+int launch(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
+           cudaStream_t stream) {
+  const int ctas = std::min(num_sms, kRowsMaxCtas);
+  if (smem_limit_at_least(reinterpret_cast<const void*>(rows_attention_kernel<KIND>), (int)kSmemBytes) != cudaSuccess)
+    return SA_ERR_CUDA;
+  cudaError_t e =
+      launch_pdl(rows_attention_kernel<KIND>, dim3(ctas), dim3(kThreads), kSmemBytes, stream, A, tmQ, tmK, tmV);
+  if (e != cudaSuccess) return SA_ERR_CUDA;
+  e = launch_pdl(rows_merge_kernel<KIND>, dim3(ctas, 2 * kRows / kMergeRows), dim3(kMergeWarps * 32), 0, stream, A);
+  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
 }  // namespace
 
 int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           int num_sms, cudaStream_t stream) {
-  const int ctas = std::min(num_sms, kRowsMaxCtas);
-  if (smem_limit_at_least(reinterpret_cast<const void*>(rows_attention_kernel), (int)kSmemBytes) != cudaSuccess)
-    return SA_ERR_CUDA;
-  cudaError_t e = launch_pdl(rows_attention_kernel, dim3(ctas), dim3(kThreads), kSmemBytes, stream, A, tmQ, tmK, tmV);
-  if (e != cudaSuccess) return SA_ERR_CUDA;
-  e = launch_pdl(rows_merge_kernel, dim3(ctas, 2 * kRows / kMergeRows), dim3(kMergeWarps * 32), 0, stream, A);
+  return launch<kPlain>(A, tmQ, tmK, tmV, num_sms, stream);
+}
+
+int launch_shared_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                            const CUtensorMap& tmV, int num_sms, cudaStream_t stream) {
+  const int rc = launch<kShared>(A, tmQ, tmK, tmV, num_sms, stream);
+  if (rc != SA_OK) return rc;
+  const cudaError_t e = launch_pdl(rows_join_kernel, dim3(A.n_rows), dim3(kJoinWarps * 32), 0, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

@@ -105,6 +105,9 @@ def lib():
                                                ctypes.POINTER(_Rope), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sa_prompt_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sa_tree_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_shared_workspace_size": (sz, [P, i32]),
+            "sa_shared_prefixes": (ctypes.c_int, [P, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]),
+            "sa_shared_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sa_accept_rows": (ctypes.c_int, [P, vp, vp, vp, vp, vp, i32, vp, vp, vp]),
             "sa_plan_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sa_compact_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp]),
@@ -205,14 +208,18 @@ class Problem:
 
 class Workspace:
     """Device scratch for one problem (sa_workspace_size bytes), zeroed once.
-    rows: also large enough for the packed-row and page calls."""
+    rows: also large enough for the packed-row and page calls.
+    max_rows: with rows, also for shared_attention of up to that many rows."""
 
-    def __init__(self, prob: Problem, device="cuda", rows: bool = False):
+    def __init__(self, prob: Problem, device="cuda", rows: bool = False, max_rows: int = 0):
         n = prob.workspace_size()
         if n == 0:
             raise SAError(SA_ERR_INVALID_ARG, "sa_workspace_size")
         if rows:
             n = max(n, int(lib().sa_rows_workspace_size(prob.ref)))
+            if max_rows > 0:
+                n = max(n, int(lib().sa_shared_workspace_size(prob.ref, max_rows)))
+        self.max_rows = max_rows * prob.Hq if rows else 0   # heads of rows that there is room for
         self.rows = prob.num_pages if rows else 0    # pages that the page calls' counts have room for
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
         self.device_index = self.buf.get_device()
@@ -632,6 +639,46 @@ def tree_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_o
                                    page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
                                    tree_mask.data_ptr(), out.data_ptr(), _p(lse), ws.buf.data_ptr(), stream),
            "sa_tree_attention")
+
+
+def shared_prefixes(prob: Problem, page_table, seq_lens, row_offsets, group_offsets, members, prefix_lens,
+                    ws: Workspace, min_tokens: int = 0):
+    """What groups of neighbouring sequences hold in the same pages ahead of
+    their rows (sa_shared_prefixes): group_offsets [groups + 1]; members and
+    prefix_lens [B] for shared_attention.  Prefixes below min_tokens are none."""
+    n, rows = _rows_of(group_offsets, "group_offsets"), (prob.B,)
+    if n < 1:
+        raise ValueError("group_offsets must hold a number")
+    stream = _check_rows_args(prob, ws, (
+        (page_table, torch.int32, (prob.B, prob.max_pages_per_seq), "page_table"), (seq_lens, torch.int32, rows, "seq_lens"),
+        (row_offsets, torch.int32, (prob.B + 1,), "row_offsets"), (group_offsets, torch.int32, (n,), "group_offsets"),
+        (members, torch.int32, rows, "members"), (prefix_lens, torch.int32, rows, "prefix_lens")))
+    _check(lib().sa_shared_prefixes(prob.ref, page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
+                                    group_offsets.data_ptr(), n - 1, min_tokens, members.data_ptr(),
+                                    prefix_lens.data_ptr(), ws.buf.data_ptr(), stream), "sa_shared_prefixes")
+
+
+def _check_room(prob: Problem, ws: Workspace, n: int):
+    if n * prob.Hq > ws.max_rows:
+        raise ValueError("the workspace must be made with max_rows, for as many rows")
+
+
+def shared_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, members, prefix_lens, out,
+                     ws: Workspace, lse=None, tree_mask=None):
+    """prompt_attention, or with tree_mask tree_attention, of rows behind
+    prefixes that groups of sequences share; a prefix is read once for all of
+    its group (sa_shared_attention).  members and prefix_lens [B]: as
+    shared_prefixes writes them.  The workspace is made with max_rows."""
+    args = _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse)
+    args += [(members, torch.int32, (prob.B,), "members"), (prefix_lens, torch.int32, (prob.B,), "prefix_lens")]
+    if tree_mask is not None:
+        args.append((tree_mask, torch.int64, (q.shape[0],), "tree_mask"))
+    stream = _check_rows_args(prob, ws, args)
+    _check_room(prob, ws, q.shape[0])
+    _check(lib().sa_shared_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                     page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(), _p(tree_mask),
+                                     members.data_ptr(), prefix_lens.data_ptr(), out.data_ptr(), _p(lse),
+                                     ws.buf.data_ptr(), stream), "sa_shared_attention")
 
 
 def accept_rows(prob: Problem, k_pool, v_pool, page_table, base_lens, path, path_cnt, ws: Workspace):
