@@ -121,8 +121,8 @@ int make_tile_map(CUtensorMap* m, const void* pool, const Params& p) {
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
 }
 
-// The checks and arguments that the attention calls share; *launch says whether
-// there is anything to do.
+// The checks and arguments that the attention calls share; launch says whether
+// there is anything to do, `rest` whether a call's other arguments are there.
 struct AttnCall {
   Params p;
   sa::RowsAttnArgs A;
@@ -132,13 +132,13 @@ struct AttnCall {
 };
 int attention_args(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool, const void* v_pool,
                    const int32_t* page_table, const int32_t* seq_lens, const int32_t* row_offsets, void* out, float* lse,
-                   void* ws, AttnCall* c) {
+                   void* ws, bool rest, AttnCall* c) {
   Params& p = c->p;
   c->launch = false;
   int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (n_rows < 0) return SA_ERR_INVALID_ARG;
-  if (!k_pool || !v_pool || !page_table || !seq_lens || !row_offsets || !ws) return SA_ERR_INVALID_ARG;
+  if (!k_pool || !v_pool || !page_table || !seq_lens || !row_offsets || !ws || !rest) return SA_ERR_INVALID_ARG;
   if (n_rows == 0) return SA_OK;
   if (!q || !out) return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(ws))
@@ -181,7 +181,7 @@ int rows_attention(const sa_problem* prob, int32_t n_rows, const void* q, const 
                    void* out, float* lse, void* ws, void* stream) {
   AttnCall c;
   const int rc =
-      attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, &c);
+      attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse, ws, true, &c);
   if (rc != SA_OK || !c.launch) return rc;
   c.A.tree = reinterpret_cast<const unsigned long long*>(tree);
   return sa::launch_rows_attention(c.A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));
@@ -340,11 +340,9 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
                         const uint64_t* tree_mask_or_null, const int32_t* members, const int32_t* prefix_lens, void* out,
                         float* lse_or_null, void* ws, void* stream) {
   AttnCall c;
-  const int rc =
-      attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse_or_null, ws, &c);
-  if (rc != SA_OK) return rc;
-  if (!members || !prefix_lens) return SA_ERR_INVALID_ARG;
-  if (!c.launch) return SA_OK;
+  const int rc = attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse_or_null, ws,
+                                members != nullptr && prefix_lens != nullptr, &c);
+  if (rc != SA_OK || !c.launch) return rc;
   const SharedLayout l = shared_layout(c.p, n_rows);
   c.A.tree = reinterpret_cast<const unsigned long long*>(tree_mask_or_null);
   c.A.members = members;
