@@ -571,6 +571,44 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
                         const int32_t* row_offsets, const uint64_t* tree_mask_or_null, const int32_t* members,
                         const int32_t* prefix_lens, void* out, float* lse_or_null, void* ws, void* stream);
 
+/* The selection of sa_select_topk for packed rows: the row at position p (of
+ * q [n_rows][Hq][D]) gets the list that sa_select_topk writes for it when the
+ * sequence has p + 1 tokens: the same candidates (seen from p), the same
+ * scores bit for bit, budgets, ties and order.  Only summaries of whole blocks
+ * are looked at (the window, at least a block long, is behind them), so those
+ * of the cache with all rows in it serve every row.
+ * sel_idx: [n_rows][Hq][kcap] int32, entries behind the count are left as they
+ * were; sel_cnt: [n_rows][Hq] int32.  Rows of nobody are left as they were; a
+ * row without a position (more rows than tokens) has count 0.
+ * max_rows rows need a workspace of
+ * sa_sparse_workspace_size; more than about 2^30 / Hk rows give
+ * SA_ERR_UNSUPPORTED. */
+int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const void* summaries,
+                   const int32_t* seq_lens, const int32_t* row_offsets, int32_t* sel_idx, int32_t* sel_cnt, void* ws,
+                   void* stream);
+
+/* Workspace bytes of sa_select_rows and sa_sparse_row_attention for up to
+ * max_rows rows (0 if prob is invalid, its table or max_rows too large or
+ * max_rows negative); enough for every call that sa_rows_workspace_size serves
+ * too. */
+size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows);
+
+/* sa_sparse_decode for packed rows: the row at position p attends the sinks
+ * [0, S), its window (p - W, p] and, of the blocks of its list, every position
+ * up to p (where a block reaches into sinks or window, positions count once).
+ * sel_idx [n_rows][Hq][kcap], sel_cnt [n_rows][Hq] as sa_select_rows writes
+ * them: blocks of the KV head's size, ascending (with entries out of order the
+ * row's result is undefined; equal, negative and later ones than p's are
+ * ignored; a count outside [0, kcap] is cut to it).  out (bf16) and lse as
+ * sa_prompt_attention, rounded alike; a row that sees nothing gets out = 0,
+ * lse = -inf; what a row does not see cannot change it.  Pages that several
+ * neighbouring rows see are read once for all of them.
+ * A page table with more than 1638400 columns gives SA_ERR_UNSUPPORTED. */
+int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
+                            const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
+                            const int32_t* row_offsets, const int32_t* sel_idx, const int32_t* sel_cnt, void* out,
+                            float* lse_or_null, void* ws, void* stream);
+
 /* Takes over the accepted nodes of a tree: for every sequence b the K and V
  * rows at positions base_lens[b] + path[b][i] move to base_lens[b] + i,
  * i < path_cnt[b].  base_lens: tokens before the draft; path [B][max_path]

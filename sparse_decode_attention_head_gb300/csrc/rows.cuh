@@ -59,6 +59,15 @@ __device__ __forceinline__ RowSeq shared_rows(const int* row_offsets, const int*
 
 // ---------------------------------------------------------------- attention
 
+// One KV head of a sequence with up to a query tile of its rows, and the
+// tiles of eight pages each that they see some of.
+struct __align__(16) SparseItem {
+  int b, kvh, i, tiles;
+  int row0, tokens, pos0, end;      // first packed row, rows, position of the first, first position that none sees
+};
+// What work weighs: a tile, and an item's query load, first tile and epilogue.
+constexpr int kSparseTileCost = 3, kSparseItemCost = 8;
+
 constexpr int kRowsMaxCtas = 192;   // one block an SM; bounds the workspace
 
 struct RowsAttnArgs {
@@ -81,6 +90,17 @@ struct RowsAttnArgs {
   int n_rows, B, Hq, Hk, G, mpp, num_pages;
   int tpt;                          // tokens of a query tile: 128 / G
   float scale_log2;                 // scale log2(e)
+  // selected blocks only
+  const __nv_bfloat16* q;           // [n_rows][Hq][kD]
+  const __nv_bfloat16* k_pool;
+  const int* sel_idx;               // [n_rows][Hq][kcap] blocks, ascending
+  const int* sel_cnt;               // [n_rows][Hq]
+  SparseItem* items;                // [n_items]
+  long long* before;                // [n_items + 1] weight of the items before
+  uint32_t* pages;                  // [n_items][words] a bit for each page that some row of the item sees
+  int n_items, words;               // at most that many; ceil(mpp / 32)
+  int kcap, S, W;
+  unsigned char bs_shift[SA_MAX_HK];
 };
 
 int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
@@ -88,9 +108,76 @@ int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const C
 int launch_shared_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, int num_sms, cudaStream_t stream);
 
+int launch_sparse_items(const RowsAttnArgs& A, cudaStream_t stream);
+int launch_sparse_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                            const CUtensorMap& tmV, int num_sms, cudaStream_t stream);
 int launch_shared_prefixes(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,
                            int n_groups, int min_tokens, int* members, int* prefix_lens, int B, int mpp, int num_pages,
                            int* status, cudaStream_t stream);
+
+// ---------------------------------------------------------------- items
+
+// Where item u lies when each KV head of a sequence's n rows is ceil(n / T)
+// items: sequences in order, their KV heads in order, runs of T rows in order.
+struct ItemPlace {
+  int b, kvh, i;     // b < 0: there is no such item
+};
+
+// A whole block of THREADS; the answer is in *place behind the call.  Item 0's
+// block looks at every sequence, for their errors.
+template <int THREADS>
+__device__ __forceinline__ void find_item(const int* row_offsets, const int* seq_lens, int B, int n_rows, int mpp,
+                                          int Hk, int T, int u, int* status, ItemPlace* place) {
+  __shared__ int s_sum[THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) *place = ItemPlace{-1, 0, 0};
+  __syncthreads();
+  int carry = 0;
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
+    const int b = b0 + tid;
+    int runs = 0;
+    if (b < B) {
+      const RowSeq s = row_seq(row_offsets, seq_lens, b, n_rows, mpp, u == 0 ? status : nullptr);
+      runs = (s.n + T - 1) / T;
+    }
+    const int mine = runs * Hk, incl = warp_incl_scan(mine);
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int upto = carry + incl, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) upto += s_sum[w];
+      total += s_sum[w];
+    }
+    if (u >= upto - mine && u < upto) {
+      const int rem = u - (upto - mine);
+      *place = ItemPlace{b, rem / runs, rem % runs};
+    }
+    __syncthreads();
+    carry += total;
+    if (u > 0 && place->b >= 0) break;
+  }
+}
+
+// ---------------------------------------------------------------- selection
+
+struct SelectArgs {
+  const __nv_bfloat16* q;           // [n_rows][Hq][kD]
+  const __nv_bfloat16* summaries;   // [B][Hk][slots][2][kD] or [B][Hk][slots][kD]
+  const int *row_offsets, *seq_lens;
+  int* sel_idx;                     // [n_rows][Hq][kcap]
+  int* sel_cnt;                     // [n_rows][Hq]
+  float* scores;                    // [block][rows][slots]
+  int* status;
+  int n_rows, n_items, B, Hq, Hk, G, mpp, slots, kcap, S, W;
+  bool minmax, group;
+  int bs[SA_MAX_HK];
+  int k[SA_MAX_HQ];
+};
+
+int launch_select_rows(const SelectArgs& A, int num_sms, cudaStream_t stream);
+int select_rows_blocks(int num_sms);     // of the scratch
+int select_rows_scratch_rows();          // rows of scores a block has
 
 // ---------------------------------------------------------------- rotation
 

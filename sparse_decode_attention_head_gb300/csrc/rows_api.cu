@@ -31,6 +31,9 @@ int make_params(const sa_problem* prob, Params* p) {
   return (long long)p->B * p->mpp < (1ll << 30) ? SA_OK : SA_ERR_UNSUPPORTED;
 }
 
+constexpr long long kMaxItems = 1 << 30;     // indices of items are 32-bit
+constexpr int kMaxSparsePages = 200 * 1024 * 8;   // an item's bitmap of pages lies in shared memory: 26 M tokens
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
   return x < y + nb && y < x + na;
@@ -69,6 +72,37 @@ SharedLayout shared_layout(const Params& p, int n_rows) {
   off = up(off + rows * sa::kD * sizeof(float));
   l.total = off;
   return l;
+}
+
+// Items of the calls with selected blocks, `rows` rows and heads each.
+long long max_items(const Params& p, int n_rows, int rows) {
+  const int T = rows / p.G;
+  return ((long long)n_rows / T + std::min(p.B, n_rows)) * p.Hk;
+}
+
+// The sparse attention's items behind the partials.
+struct SparseLayout {
+  size_t items, before, pages, total;
+  int words;
+};
+SparseLayout sparse_layout(const Params& p, int n_rows) {
+  const size_t n = (size_t)max_items(p, n_rows, 128);
+  SparseLayout l;
+  l.words = (p.mpp + 31) / 32;
+  size_t off = attn_layout().total;
+  l.items = off;
+  off = up(off + n * sizeof(sa::SparseItem));
+  l.before = off;
+  off = up(off + (n + 1) * sizeof(long long));
+  l.pages = off;
+  off = up(off + n * l.words * sizeof(uint32_t));
+  l.total = off;
+  return l;
+}
+
+size_t select_rows_bytes(const Params& p) {
+  return up(sizeof(sa::WsHeader)) + (size_t)sa::select_rows_blocks(sa::kRowsMaxCtas) * sa::select_rows_scratch_rows() *
+                                        p.slots * sizeof(float);
 }
 
 struct PageLayout {
@@ -350,6 +384,81 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
   c.A.half = at<float>(ws, l.half);
   c.A.half_ml = at<float2>(ws, l.ml);
   return sa::launch_shared_attention(c.A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));
+}
+
+size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows) {
+  Params p;
+  if (make_params(prob, &p) != SA_OK || max_rows < 0 || max_items(p, max_rows, 32) > kMaxItems) return 0;
+  return std::max({sa_rows_workspace_size(prob), sparse_layout(p, max_rows).total, select_rows_bytes(p)});
+}
+
+int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const void* summaries,
+                   const int32_t* seq_lens, const int32_t* row_offsets, int32_t* sel_idx, int32_t* sel_cnt, void* ws,
+                   void* stream) {
+  Params p;
+  const int rc = make_params(prob, &p);
+  if (rc != SA_OK) return rc;
+  if (n_rows < 0 || !summaries || !seq_lens || !row_offsets || !ws) return SA_ERR_INVALID_ARG;
+  if (max_items(p, n_rows, 32) > kMaxItems) return SA_ERR_UNSUPPORTED;
+  if (n_rows == 0) return SA_OK;
+  if (!q || !sel_idx || !sel_cnt) return SA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(summaries) || !aligned16(ws)) return SA_ERR_INVALID_ARG;
+  const int nsm = sa_host::num_sms_current();
+  if (nsm <= 0) return SA_ERR_CUDA;
+  sa::SelectArgs A{};
+  A.q = static_cast<const __nv_bfloat16*>(q);
+  A.summaries = static_cast<const __nv_bfloat16*>(summaries);
+  A.row_offsets = row_offsets;
+  A.seq_lens = seq_lens;
+  A.sel_idx = sel_idx;
+  A.sel_cnt = sel_cnt;
+  A.scores = at<float>(ws, up(sizeof(sa::WsHeader)));
+  A.status = at<int>(ws, 0);
+  A.n_rows = n_rows;
+  A.n_items = (int)max_items(p, n_rows, 32);
+  A.B = p.B;
+  A.Hq = p.Hq;
+  A.Hk = p.Hk;
+  A.G = p.G;
+  A.mpp = p.mpp;
+  A.slots = p.slots;
+  A.kcap = p.kcap;
+  A.S = p.S;
+  A.W = p.W;
+  A.minmax = p.mode == SA_SUMMARY_MINMAX;
+  A.group = p.sel_mode == SA_SELECT_GROUP;
+  std::copy(p.bs, p.bs + p.Hk, A.bs);
+  std::copy(p.k, p.k + p.Hq, A.k);
+  return sa::launch_select_rows(A, std::min(nsm, sa::kRowsMaxCtas), as_stream(stream));
+}
+
+int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
+                            const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
+                            const int32_t* row_offsets, const int32_t* sel_idx, const int32_t* sel_cnt, void* out,
+                            float* lse_or_null, void* ws, void* stream) {
+  AttnCall c;
+  const int rc = attention_args(prob, n_rows, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse_or_null, ws,
+                                sel_idx != nullptr && sel_cnt != nullptr, &c);
+  if (rc != SA_OK) return rc;
+  const Params& p = c.p;
+  if (max_items(p, n_rows, 32) > kMaxItems || p.mpp > kMaxSparsePages) return SA_ERR_UNSUPPORTED;
+  if (!c.launch) return SA_OK;
+  const SparseLayout l = sparse_layout(p, n_rows);
+  sa::RowsAttnArgs& A = c.A;
+  A.q = static_cast<const __nv_bfloat16*>(q);
+  A.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
+  A.sel_idx = sel_idx;
+  A.sel_cnt = sel_cnt;
+  A.items = at<sa::SparseItem>(ws, l.items);
+  A.before = at<long long>(ws, l.before);
+  A.pages = at<uint32_t>(ws, l.pages);
+  A.n_items = (int)max_items(p, n_rows, 128);
+  A.words = l.words;
+  A.kcap = p.kcap;
+  A.S = std::min(p.S, 1 << 30);
+  A.W = std::min(p.W, 1 << 30);
+  for (int h = 0; h < p.Hk; ++h) A.bs_shift[h] = (unsigned char)(p.bs[h] == 8 ? 3 : p.bs[h] == 16 ? 4 : p.bs[h] == 32 ? 5 : 6);
+  return sa::launch_sparse_attention(A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));
 }
 
 int sa_accept_rows(const sa_problem* prob, void* k_pool, void* v_pool, const int32_t* page_table,

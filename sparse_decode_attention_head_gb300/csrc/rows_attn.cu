@@ -97,7 +97,11 @@ enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
 enum Kind {
   kPlain,     // prompts and trees, each sequence over all of its cache
   kShared,    // the same, with the prefix of a group of sequences as an item of its own
+  kSparse,    // causal rows over sinks, window and the blocks of their lists
 };
+// Query tiles of an item; with selected blocks one, whose rows see more alike.
+template <int KIND>
+constexpr int kQTiles = KIND == kSparse ? 1 : 2;
 
 // A piece of a block's run: KV tiles [k0, k1) of one item.  The loading warp
 // walks the run and hands the pieces to the other roles through a ring.
@@ -111,13 +115,14 @@ struct Piece {
   int first;          // the item's first row in the sequence
   int to;             // Part: where the result goes
   long long pt;       // entry of the page table with the item's position 0
+  int u;              // kSparse: the item
   bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
 };
 
 constexpr int kPieces = 4;
 constexpr int kPieceReaders = 11;        // warps: softmax, matrix instructions, edge
 
-struct Ctl {
+struct alignas(16) Ctl {
   Piece piece[kPieces];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t full[kSlots], empty[kSlots];
@@ -133,8 +138,21 @@ struct Ctl {
   int poison[4];             // 1 + the piece that met a non-finite V at its edge
   float2 ml[kRows];          // (maximum, sum) of the second softmax group
 };
-constexpr size_t kSmemBytes = 1024 + 2 * kTileBytes + kSlots * kTileBytes + sizeof(Ctl);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// kSparse: what the rows see of a tile, a ring.  The loading warp names the
+// tile's pages, two warps look each row up in its list and leave 16 bits a
+// row, a bit for 8 tokens.
+constexpr int kMaskDepth = 8;            // K and V slots let the loads run at most four tiles ahead of the softmax
+struct alignas(16) MaskCtl {
+  uint64_t page_full[kMaskDepth], mask_full[kMaskDepth];
+  int page[kMaskDepth][8];               // ascending; -1 behind the item's last
+  int cut[kMaskDepth];                   // some row's view begins or ends inside 8 of its tokens
+  uint16_t mask[kMaskDepth][kRows];
+};
+template <int KIND>
+constexpr size_t kSmemBytes = 1024 + (kQTiles<KIND> + kSlots) * kTileBytes + sizeof(Ctl) +
+                              (KIND == kSparse ? sizeof(MaskCtl) : 0);
+static_assert(kSmemBytes<kPlain> <= 227 * 1024 && kSmemBytes<kSparse> <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -229,7 +247,7 @@ template <int KIND>
 __device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int v, int* status) {
   const int b = KIND == kShared ? v >> 1 : v;
   Seq s;
-  s.T = 2 * A.tpt;
+  s.T = kQTiles<KIND> * A.tpt;
   s.to = kAll;
   s.pt = (long long)b * A.mpp;
   if (KIND == kShared && (v & 1) == 0) {
@@ -459,6 +477,213 @@ struct Walk {
   }
 };
 
+// With selected blocks: the items lie one behind the other with the weight of
+// those before them.
+template <>
+struct Walk<kSparse> {
+  const RowsAttnArgs& A;
+  int u, kt;
+  int4 end;
+  SparseItem it;
+  __device__ Walk(const RowsAttnArgs& a, const Ctl* c) : A(a) {
+    u = c->range[0].x;
+    kt = c->range[0].y;
+    end = c->range[1];
+    load();
+  }
+  __device__ void load() {
+    if (u < A.n_items) {
+      const int4* x = reinterpret_cast<const int4*>(A.items + u);
+      const int4 a = __ldg(x), b = __ldg(x + 1);
+      it = SparseItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    }
+  }
+  __device__ bool next(Piece& p) {
+    while (u < end.x || (u == end.x && kt < end.y)) {
+      const bool at_end = u == end.x;
+      p.b = it.b; p.kvh = it.kvh; p.i = it.i;
+      p.nt = it.tiles;
+      p.k0 = kt;
+      p.k1 = at_end ? end.y : it.tiles;
+      p.row0 = it.row0;
+      p.tokens = it.tokens;
+      p.end = it.end;
+      p.edge = (it.tiles - 1) * kRows + 1;       // the last tile alone holds positions that no row sees
+      p.a = it.pos0;
+      p.first = 0;
+      p.to = kAll;
+      p.pt = (long long)it.b * A.mpp;
+      p.u = u;
+      p.dual = true;
+      const bool some = p.k0 < p.k1 || (p.nt == 0 && p.tokens > 0 && !at_end);
+      kt = 0;
+      if (at_end) {
+        end.y = 0;
+      } else {
+        ++u;
+        load();
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+};
+
+// One warp: the item and tile at weight w of all items (w = total: behind the last).
+__device__ __forceinline__ int4 locate_item(const RowsAttnArgs& A, long long w) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = A.n_items;      // before[lo] <= w < before[hi]
+  if (w >= __ldg(A.before + hi)) return make_int4(hi, 0, 0, 0);
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + step * (lane + 1);
+    const int n = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(A.before + at) <= w));
+    hi = min(hi, lo + step * (n + 1));
+    lo += step * n;
+  }
+  const long long w0 = __ldg(A.before + lo), w1 = __ldg(A.before + lo + 1);
+  return make_int4(lo, (int)((w - w0) * A.items[lo].tiles / (w1 - w0)), 0, 0);
+}
+
+// ---------------------------------------------------------------- what a row sees of selected blocks
+
+// Eight pages of an item's bitmap at a time, by a whole warp.
+template <int KIND>
+struct PageWalk {
+  __device__ __forceinline__ PageWalk(const RowsAttnArgs&, const Piece&, int) {}
+};
+template <>
+struct PageWalk<kSparse> {
+  const uint32_t* bits;
+  int words, base;       // base: the first of the 32 words that the lanes hold
+  uint32_t mine;         // pages not given yet
+  __device__ __forceinline__ void load() {
+    const int w = base + (threadIdx.x & 31);
+    mine = w < words ? __ldg(bits + w) : 0u;
+  }
+  // ahead: pages to pass over
+  __device__ __forceinline__ PageWalk(const RowsAttnArgs& A, const Piece& p, int ahead)
+      : bits(A.pages + (size_t)p.u * A.words), words((p.end + 32 * kP - 1) / (32 * kP)), base(0) {
+    load();
+    while (true) {
+      const int n = __popc(mine), upto = warp_incl_scan(n), total = __shfl_sync(0xffffffffu, upto, 31);
+      if (ahead < total || base + 32 >= words) {
+        for (int d = min(ahead - (upto - n), n); d > 0; --d) mine &= mine - 1;
+        return;
+      }
+      ahead -= total;
+      base += 32;
+      load();
+    }
+  }
+  __device__ __forceinline__ void next(int* page) {
+    const int lane = threadIdx.x & 31;
+    if (lane < 8) page[lane] = -1;
+    __syncwarp();
+    int got = 0;
+    while (true) {
+      const int n = __popc(mine), upto = warp_incl_scan(n), total = __shfl_sync(0xffffffffu, upto, 31);
+      for (int at = got + upto - n; mine != 0 && at < 8; ++at) {
+        page[at] = (base + lane) * 32 + __ffs(mine) - 1;
+        mine &= mine - 1;
+      }
+      got += total;
+      if (got >= 8 || base + 32 >= words) break;
+      base += 32;
+      load();
+    }
+    __syncwarp();
+  }
+};
+
+// A row's list, walked along ascending blocks.
+struct ListWalk {
+  const int* list;
+  int n, at;            // entries, the next to load
+  int cur, nxt;
+  __device__ __forceinline__ int get(int j) const { return j < n ? __ldg(list + j) : 0x7fffffff; }
+  __device__ __forceinline__ void start(const int* l, int count, int from) {   // from: the first block asked for
+    list = l;
+    n = count;
+    int lo = 0, hi = n;
+    if (from > 0) {
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(l + mid) < from) lo = mid + 1; else hi = mid;
+      }
+    }
+    cur = get(lo);
+    nxt = get(lo + 1);
+    at = lo + 2;
+  }
+  __device__ __forceinline__ bool has(int e) {
+    while (cur < e) {
+      cur = nxt;
+      nxt = get(at++);
+    }
+    return cur == e;
+  }
+};
+
+// The sums of one row over one piece from its definition, by a whole warp:
+// dims 4 lane on.  Taken where the product of a tile with V is not finite: a
+// weight of zero times such a value is NaN for rows that do not see it.
+struct SeenRow {
+  size_t row;           // packed row and head
+  int kvh, pos;
+  float M;
+};
+__device__ __noinline__ float4 sums_of_row(const RowsAttnArgs& A, const Piece& p, SeenRow s) {
+  const int lane = threadIdx.x & 31;
+  const int shift = A.bs_shift[s.kvh];
+  const int n = min(max(__ldg(A.sel_cnt + s.row), 0), A.kcap);
+  const int* list = A.sel_idx + s.row * A.kcap;
+  const uint32_t* bits = A.pages + (size_t)p.u * A.words;
+  const int words = (p.end + 32 * kP - 1) / (32 * kP);
+  const int half = lane >> 4, tk = lane & 15;      // a token's dims 64 half on
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  int rank = 0;
+  for (int w = 0; w < words && rank < 8 * p.k1; ++w) {
+    uint32_t x = __ldg(bits + w);
+    if (rank + __popc(x) <= 8 * p.k0) {
+      rank += __popc(x);
+      continue;
+    }
+    for (; x != 0; x &= x - 1, ++rank) {
+      if (rank < 8 * p.k0 || rank >= 8 * p.k1) continue;
+      const int page = w * 32 + __ffs(x) - 1;
+      const int phys = __ldg(A.page_table + p.pt + page);
+      if (phys < 0 || phys >= A.num_pages) continue;
+      const int t = page * kP + tk, e = t >> shift;
+      int lo = 0, hi = n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(list + mid) < e) lo = mid + 1; else hi = mid;
+      }
+      const bool seen = t <= s.pos && (t < A.S || t > s.pos - A.W || (lo < n && __ldg(list + lo) == e));
+      const size_t at = (((size_t)phys * A.Hk + s.kvh) * kP + tk) * kD;
+      float z = 0.f;
+      if (seen)
+        for (int d = 64 * half; d < 64 * half + 64; ++d)
+          z = fmaf(__bfloat162float(A.q[s.row * kD + d]), __bfloat162float(A.k_pool[at + d]), z);
+      z += __shfl_xor_sync(0xffffffffu, z, 16);
+      const float weight = __bfloat162float(__float2bfloat16_rn(ex2(fmaf(z, A.scale_log2, -s.M))));
+      unsigned who = __ballot_sync(0xffffffffu, seen) & 0xffffu;
+      for (; who != 0; who &= who - 1) {
+        const int j = __ffs(who) - 1;
+        const float f = __shfl_sync(0xffffffffu, weight, j);
+        const uint2 q = *reinterpret_cast<const uint2*>(
+            A.v_pool + (((size_t)phys * A.Hk + s.kvh) * kP + j) * kD + 4 * lane);
+        auto add = [f](float& o, float v) { o = isfinite(v) ? fmaf(f, v, o) : o + v; };
+        add(acc.x, bf16_lo(q.x));
+        add(acc.y, bf16_hi(q.x));
+        add(acc.z, bf16_lo(q.y));
+        add(acc.w, bf16_hi(q.y));
+      }
+    }
+  }
+  return acc;
+}
+
 // ---------------------------------------------------------------- epilogue
 
 __device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
@@ -521,11 +746,18 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;                                  // two tiles: [half of the dims][128 rows][64]
-  uint8_t* s_kv = smem + 2 * kTileBytes;                // kSlots tiles: [16 groups of 8 tokens][half][8][64]
+  uint8_t* s_kv = smem + kQTiles<KIND> * kTileBytes;    // kSlots tiles: [16 groups of 8 tokens][half][8][64]
   Ctl* c = reinterpret_cast<Ctl*>(s_kv + kSlots * kTileBytes);
+  MaskCtl* mc = reinterpret_cast<MaskCtl*>(c + 1);      // kSparse
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
+    if constexpr (KIND == kSparse) {
+      for (int i = 0; i < kMaskDepth; ++i) {
+        mbar_init(&mc->page_full[i], 1);
+        mbar_init(&mc->mask_full[i], 2);
+      }
+    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&c->full[i], 1);
       mbar_init(&c->empty[i], 1);
@@ -559,7 +791,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   }
   pdl_wait();
   pdl_trigger();
-  if (warp < 2) {   // where this block's run begins (warp 0) and ends (warp 1)
+  if constexpr (KIND == kSparse) {
+    if (warp < 2) {
+      const int4 r = locate_item(A, __ldg(A.before + A.n_items) * (blockIdx.x + warp) / gridDim.x);
+      if (lane == 0) c->range[warp] = r;
+    }
+  } else if (warp < 2) {   // where this block's run begins (warp 0) and ends (warp 1)
     Seq s;
     long long mine;
     const long long W = total_weight<KIND>(A, blockIdx.x == 0 && warp == 0 ? A.status : nullptr, s, mine);
@@ -600,7 +837,9 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       // what the row sees: positions below lim, and bit j of its word for position p.a + j
       int lim = 0;
       unsigned long long word = 0;
-      if (valid) {
+      if (KIND == kSparse) {
+        lim = valid ? p.a + tok + 1 : 0;      // and of those what its mask has
+      } else if (valid) {
         if (A.tree != nullptr) {
           lim = p.a;
           word = __ldg(A.tree + p.row0 + tok);
@@ -613,6 +852,14 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       for (int s = h; s < N; s += 2) {
         const int t = dual ? s : s >> 1;
         const int kt = k0 + t;
+        uint32_t mask = 0;
+        bool cut = false;
+        const int place = (int)((tiles + t) % kMaskDepth);
+        if constexpr (KIND == kSparse) {
+          if (!(ok = wait_warp(&mc->mask_full[place], ((tiles + t) / kMaskDepth) & 1, c, A.status))) break;
+          mask = mc->mask[place][r];
+          cut = mc->cut[place] != 0;
+        }
         if (!(ok = wait_warp(&c->s_full[h], steps_done & 1, c, A.status))) break;
         ++steps_done;
         tc_fence_after();
@@ -620,7 +867,35 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         tmem_ld64_start<0>(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
         tmem_ld64_finish<0>(v);
-        if ((kt + 1) * kRows > edge || bad != 0) {
+        if constexpr (KIND == kSparse) {
+          if (cut || bad != 0) {
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              uint32_t see = 0;            // bit j: column 32 w + j
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int page = mc->page[place][2 * w + (e >> 1)], t0 = page * kP + 8 * (e & 1);
+                auto below = [t0](int x) { return (1u << min(max(x - t0, 0), 8)) - 1u; };   // of 8 tokens, those before x
+                uint32_t x = (mask >> (4 * w + e)) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
+                x &= page < 0 || ((bad >> (2 * w + (e >> 1))) & 1u) ? 0u : below(lim);
+                see |= x << (8 * e);
+              }
+              float x[32];
+              uint32_t y[32];
+              tmem_ld32(tS + 32 * w, x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] = (see >> j) & 1u ? __float_as_uint(x[j]) : 0xff800000u;
+              tmem_st32(tS + 32 * w, y);
+            }
+            tmem_wait_st();
+            tmem_ld64_start<0>(tS, v);
+            tmem_ld64_finish<0>(v);
+            mask = 0xffffu;
+          }
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (!((mask >> (j >> 3)) & 1u)) v[j] = -INFINITY;
+        } else if ((kt + 1) * kRows > edge || bad != 0) {
           // masked in TMEM, 32 columns at a time: once or twice an item, and
           // a long piece of straight code would cost its instruction fetches
 #pragma unroll 1
@@ -655,6 +930,11 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
         for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], v[60 + x]);
         tmem_ld64_finish<64>(v);
+        if constexpr (KIND == kSparse) {
+#pragma unroll
+          for (int j = 64; j < 128; ++j)
+            if (!((mask >> (j >> 3)) & 1u)) v[j] = -INFINITY;
+        }
 #pragma unroll
         for (int j = 64; j < 128; j += 8) {
 #pragma unroll
@@ -754,6 +1034,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
         for (int j = 0; j < 4; ++j) rows4[j] = __shfl_sync(0xffffffffu, valid ? row : -1ll, (lane & 28) + j);
         const float f0 = w0 * inv, f1 = w1 * inv;
+        float zero = 0.f;     // kSparse: NaN where a sum is not finite
         // kept short (a loop over 32 columns): it runs once an item, and the
         // fetch of its instructions costs more than the work
 #pragma unroll 1
@@ -771,6 +1052,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             tmem_ld32(tO + 128 + 32 * q4, o1);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = fmaf(o1[j], f1, o[j]);
+          }
+          if constexpr (KIND == kSparse) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) zero = fmaf(o[j], 0.f, zero);
           }
           if (final_out) {
             uint32_t x[4][4];
@@ -802,7 +1087,25 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
                   make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
-        if (poisoned) {
+        if constexpr (KIND == kSparse) {
+          unsigned again = __ballot_sync(0xffffffffu, valid && zero != 0.f);
+          for (; again != 0; again &= again - 1) {
+            const int src = __ffs(again) - 1;
+            __syncwarp();     // the row was stored by its neighbours too
+            SeenRow s;
+            s.row = (size_t)__shfl_sync(0xffffffffu, row, src);
+            s.kvh = p.kvh;
+            s.pos = __shfl_sync(0xffffffffu, lim, src) - 1;
+            s.M = __shfl_sync(0xffffffffu, M == -INFINITY ? 0.f : M, src);
+            const float f = __shfl_sync(0xffffffffu, inv, src);
+            const float4 x = sums_of_row(A, p, s);
+            if (whole)
+              reinterpret_cast<uint2*>(A.out + s.row * kD)[lane] =
+                  make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+            else
+              *reinterpret_cast<float4*>(part + 4 * (src - lane) + lane * (4 * kRows)) = x;
+          }
+        } else if (poisoned) {
           __syncwarp();     // the row was stored by its neighbours too
           if (valid)
             add_poison(A, EdgeRow{A.page_table + p.pt, word, max(p.edge, p.k0 * kRows), min(p.end, p.k1 * kRows), lim, p.a},
@@ -1001,13 +1304,26 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         ++pieces;
         // a lane a page of the tile; the next tile's pages are looked up while this one's are copied
         const int* pt = A.page_table + p.pt;
+        PageWalk<KIND> pages(A, p, 8 * p.k0);
+        bool next_there = false;
         auto page_of = [&](int t) {
-          const int page = (p.k0 + t) * (kRows / kP) + lane;
-          return lane < kRows / kP && page * kP < p.end ? __ldg(pt + page) : -1;
+          int page;
+          if constexpr (KIND == kSparse) {
+            if (t == ntp) return -1;
+            const int place = (int)((tile + t) % kMaskDepth);
+            pages.next(mc->page[place]);
+            if (lane == 0) mbar_arrive(&mc->page_full[place]);
+            page = lane < kRows / kP ? mc->page[place][lane] : -1;
+            next_there = page >= 0;
+          } else {
+            page = (p.k0 + t) * (kRows / kP) + lane;
+            next_there = lane < kRows / kP && page * kP < p.end;
+          }
+          return next_there ? __ldg(pt + page) : -1;
         };
         int next_phys = page_of(0);
         for (int t = 0; t < ntp; ++t) {
-          const bool there = lane < kRows / kP && ((p.k0 + t) * (kRows / kP) + lane) * kP < p.end;
+          const bool there = next_there;
           const int phys = next_phys;
           next_phys = page_of(t + 1);
           const bool good = phys >= 0 && phys < A.num_pages;
@@ -1051,13 +1367,69 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       // slot, so the parity of its full barrier alone would not tell which one
       uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
       bool ok = true;
+      const int bit = w * 32 + lane;         // kSparse: rows bit and 64 + bit
       for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
         const Piece p = c->piece[piece % kPieces];
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
         if (p.k0 < 0) break;
         const int ntp = p.k1 - p.k0;
-        for (int t = max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
+        ListWalk walk[2];
+        int pos[2];
+        if constexpr (KIND == kSparse) {
+          if (ntp > 0) {
+            if (!(ok = wait_warp(&mc->page_full[tile % kMaskDepth], (tile / kMaskDepth) & 1, c, A.status))) break;
+            const int from = p.k0 > 0 ? mc->page[tile % kMaskDepth][0] * kP >> A.bs_shift[p.kvh] : 0;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int r = bit + 64 * x, tok = r / A.G;
+              pos[x] = tok < A.tpt && tok < p.tokens ? p.a + tok : -1;
+              const size_t row = (size_t)(p.row0 + tok) * A.Hq + p.kvh * A.G + (r - tok * A.G);
+              if (pos[x] >= 0)
+                walk[x].start(A.sel_idx + row * A.kcap, min(max(__ldg(A.sel_cnt + row), 0), A.kcap), from);
+            }
+          }
+        }
+        for (int t = KIND == kSparse ? 0 : max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
+          if constexpr (KIND == kSparse) {
+            const int place = (int)((tile + t) % kMaskDepth);
+            if (!(ok = wait_warp(&mc->page_full[place], ((tile + t) / kMaskDepth) & 1, c, A.status))) break;
+            const int shift = A.bs_shift[p.kvh];
+            // views that begin or end inside 8 tokens: in the page with the sinks' end, and where rows' windows and
+            // the rows themselves begin
+            const int w0 = p.a + 1 - A.W, w1 = w0 + p.tokens - 1;
+            int page[8];
+            *reinterpret_cast<int4*>(page) = *reinterpret_cast<const int4*>(mc->page[place]);
+            *reinterpret_cast<int4*>(page + 4) = *reinterpret_cast<const int4*>(mc->page[place] + 4);
+            uint32_t seen[2] = {0, 0};
+            bool cut = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (page[j] < 0) continue;
+              const int t0 = page[j] * kP;
+              cut |= ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) || t0 + kP > p.a;
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                if (pos[x] < 0) continue;
+                uint32_t two;
+                if (shift == 3) {
+                  two = walk[x].has(2 * page[j]) ? 1u : 0u;
+                  two |= walk[x].has(2 * page[j] + 1) ? 2u : 0u;
+                } else {
+                  two = walk[x].has(t0 >> shift) ? 3u : 0u;
+                }
+                if (t0 + 8 <= A.S || (t0 > pos[x] - A.W && t0 + 7 <= pos[x])) two |= 1u;
+                if (t0 + 16 <= A.S || (t0 + 8 > pos[x] - A.W && t0 + 15 <= pos[x])) two |= 2u;
+                seen[x] |= two << (2 * j);
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) mc->mask[place][bit + 64 * x] = (uint16_t)seen[x];
+            if (bit == 0) mc->cut[place] = cut;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mc->mask_full[place]);
+            if (p.k0 + t + 1 < p.nt) continue;
+          }
           const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
           if (!(ok = wait_warp(&c->edge_go[slot], (gone >> slot) & 1, c, A.status))) break;
           gone ^= 1u << slot;
@@ -1065,6 +1437,17 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           const int base = (p.k0 + t) * kRows;
           // 16-byte chunk x: token group x / 128, row (x / 8) % 8
           uint4* sv = reinterpret_cast<uint4*>(s_kv + slot * kTileBytes);
+          if constexpr (KIND == kSparse) {
+            const int* page = mc->page[(tile + t) % kMaskDepth];
+            for (int x = w * 32 + lane; x < kTileBytes / 16; x += 64) {
+              const int at = page[x >> 8];
+              if (at < 0 || at * kP + ((x >> 7) & 1) * 8 + ((x >> 3) & 7) >= p.end) sv[x] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->clean[slot]);
+            continue;
+          }
           bool found = false;
           for (int x = (max(0, p.edge - base) >> 3) * 128 + w * 32 + lane; x < kTileBytes / 16; x += 64) {
             const int pos = base + (x >> 7) * 8 + ((x >> 3) & 7);
@@ -1253,10 +1636,10 @@ template <int KIND>
 int launch(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
            cudaStream_t stream) {
   const int ctas = std::min(num_sms, kRowsMaxCtas);
-  if (smem_limit_at_least(reinterpret_cast<const void*>(rows_attention_kernel<KIND>), (int)kSmemBytes) != cudaSuccess)
+  if (smem_limit_at_least(reinterpret_cast<const void*>(rows_attention_kernel<KIND>), (int)kSmemBytes<KIND>) != cudaSuccess)
     return SA_ERR_CUDA;
   cudaError_t e =
-      launch_pdl(rows_attention_kernel<KIND>, dim3(ctas), dim3(kThreads), kSmemBytes, stream, A, tmQ, tmK, tmV);
+      launch_pdl(rows_attention_kernel<KIND>, dim3(ctas), dim3(kThreads), kSmemBytes<KIND>, stream, A, tmQ, tmK, tmV);
   if (e != cudaSuccess) return SA_ERR_CUDA;
   e = launch_pdl(rows_merge_kernel<KIND>, dim3(ctas, 2 * kRows / kMergeRows), dim3(kMergeWarps * 32), 0, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
@@ -1275,6 +1658,12 @@ int launch_shared_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const
   if (rc != SA_OK) return rc;
   const cudaError_t e = launch_pdl(rows_join_kernel, dim3(A.n_rows), dim3(kJoinWarps * 32), 0, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+int launch_sparse_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                            const CUtensorMap& tmV, int num_sms, cudaStream_t stream) {
+  const int rc = launch_sparse_items(A, stream);
+  return rc == SA_OK ? launch<kSparse>(A, tmQ, tmK, tmV, num_sms, stream) : rc;
 }
 
 }  // namespace sa

@@ -108,6 +108,9 @@ def lib():
             "sa_shared_workspace_size": (sz, [P, i32]),
             "sa_shared_prefixes": (ctypes.c_int, [P, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]),
             "sa_shared_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_sparse_workspace_size": (sz, [P, i32]),
+            "sa_select_rows": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "sa_sparse_row_attention": (ctypes.c_int, [P, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sa_accept_rows": (ctypes.c_int, [P, vp, vp, vp, vp, vp, i32, vp, vp, vp]),
             "sa_plan_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sa_compact_pages": (ctypes.c_int, [P, vp, vp, vp, vp, vp, vp, vp, vp]),
@@ -209,7 +212,8 @@ class Problem:
 class Workspace:
     """Device scratch for one problem (sa_workspace_size bytes), zeroed once.
     rows: also large enough for the packed-row and page calls.
-    max_rows: with rows, also for shared_attention of up to that many rows."""
+    max_rows: with rows, also for shared_attention, select_rows and
+    sparse_row_attention of up to that many rows."""
 
     def __init__(self, prob: Problem, device="cuda", rows: bool = False, max_rows: int = 0):
         n = prob.workspace_size()
@@ -218,8 +222,9 @@ class Workspace:
         if rows:
             n = max(n, int(lib().sa_rows_workspace_size(prob.ref)))
             if max_rows > 0:
-                n = max(n, int(lib().sa_shared_workspace_size(prob.ref, max_rows)))
-        self.max_rows = max_rows * prob.Hq if rows else 0   # heads of rows that there is room for
+                n = max(n, int(lib().sa_shared_workspace_size(prob.ref, max_rows)),
+                        int(lib().sa_sparse_workspace_size(prob.ref, max_rows)))
+        self.max_rows = max_rows if rows else 0
         self.rows = prob.num_pages if rows else 0    # pages that the page calls' counts have room for
         self.buf = torch.empty(n, dtype=torch.uint8, device=device)
         self.device_index = self.buf.get_device()
@@ -659,7 +664,7 @@ def shared_prefixes(prob: Problem, page_table, seq_lens, row_offsets, group_offs
 
 
 def _check_room(prob: Problem, ws: Workspace, n: int):
-    if n * prob.Hq > ws.max_rows:
+    if n > ws.max_rows:
         raise ValueError("the workspace must be made with max_rows, for as many rows")
 
 
@@ -679,6 +684,38 @@ def shared_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row
                                      page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(), _p(tree_mask),
                                      members.data_ptr(), prefix_lens.data_ptr(), out.data_ptr(), _p(lse),
                                      ws.buf.data_ptr(), stream), "sa_shared_attention")
+
+
+def select_rows(prob: Problem, q, summaries, seq_lens, row_offsets, sel_idx, sel_cnt, ws: Workspace):
+    """Every packed row's selected blocks, as select_topk has them for a cache
+    that ends with the row (sa_select_rows): sel_idx [n][Hq][kcap], sel_cnt
+    [n][Hq].  The workspace is made with max_rows."""
+    n = _rows_of(q, "q")
+    stream = _check_rows_args(prob, ws, (
+        (q, torch.bfloat16, (n, prob.Hq, prob.D), "q"), (summaries, torch.bfloat16, prob.summary_shape(), "summaries"),
+        (seq_lens, torch.int32, (prob.B,), "seq_lens"), (row_offsets, torch.int32, (prob.B + 1,), "row_offsets"),
+        (sel_idx, torch.int32, (n, prob.Hq, prob.kcap), "sel_idx"), (sel_cnt, torch.int32, (n, prob.Hq), "sel_cnt")))
+    _check_room(prob, ws, n)
+    _check(lib().sa_select_rows(prob.ref, n, q.data_ptr(), summaries.data_ptr(), seq_lens.data_ptr(),
+                                row_offsets.data_ptr(), sel_idx.data_ptr(), sel_cnt.data_ptr(), ws.buf.data_ptr(),
+                                stream), "sa_select_rows")
+
+
+def sparse_row_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, sel_idx, sel_cnt, out,
+                         ws: Workspace, lse=None):
+    """Causal attention of packed rows over sinks, window and each row's
+    selected blocks (sa_sparse_row_attention): sel_idx [n][Hq][kcap] ascending,
+    sel_cnt [n][Hq], as select_rows writes them.  The workspace is made with
+    max_rows."""
+    args = _attention_args(prob, q, k_pool, v_pool, page_table, seq_lens, row_offsets, out, lse)
+    args += [(sel_idx, torch.int32, (q.shape[0], prob.Hq, prob.kcap), "sel_idx"),
+             (sel_cnt, torch.int32, (q.shape[0], prob.Hq), "sel_cnt")]
+    stream = _check_rows_args(prob, ws, args)
+    _check_room(prob, ws, q.shape[0])
+    _check(lib().sa_sparse_row_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                         page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
+                                         sel_idx.data_ptr(), sel_cnt.data_ptr(), out.data_ptr(), _p(lse),
+                                         ws.buf.data_ptr(), stream), "sa_sparse_row_attention")
 
 
 def accept_rows(prob: Problem, k_pool, v_pool, page_table, base_lens, path, path_cnt, ws: Workspace):

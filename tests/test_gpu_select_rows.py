@@ -1,0 +1,181 @@
+"""The selection of packed rows (sa_select_rows) against the canonical scores
+step by step in 32 bits and a sort, entry for entry."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_decode_attention_head_gb300 import sa
+from tests import rows_ref as R
+from tests import sparse_ref as Z
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(rows, prefix, Hq, Hk, seed=0, **kw):
+    """Rows without pools that matter: the selection reads summaries alone."""
+    r = R.Rows([0] * len(rows), [0] * len(rows), Hq, Hk, seed=seed)
+    r.rows, r.prefix = list(rows), list(prefix)
+    lead, extra = kw.get("lead", 0), kw.get("extra", 0)
+    r.n_rows = lead + sum(rows) + extra
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r.q = torch.randn(r.n_rows, Hq, 128, generator=g, device="cuda").to(torch.bfloat16)
+    r.offsets = torch.tensor(np.concatenate([[0], np.cumsum(rows)]) + lead, dtype=torch.int32, device="cuda")
+    lens = [a + n for a, n in zip(prefix, rows)]
+    r.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    r.mpp = kw.get("mpp") or max(1, max(-(-n // 16) for n in lens))
+    return r
+
+
+def _summaries(prob, seed=0, kind="normal"):
+    g = torch.Generator(device="cuda").manual_seed(seed + 1000)
+    x = torch.randn(prob.summary_shape(), generator=g, device="cuda")
+    if kind == "coarse":           # few different values: many scores are equal
+        x = x.sign()
+    if kind == "equal":
+        x = torch.ones_like(x)
+    if prob.mode == sa.SUMMARY_MINMAX:
+        lo, hi = x.amin(3, keepdim=True), x.amax(3, keepdim=True)
+        x = torch.cat([lo, hi], 3)
+    return x.to(torch.bfloat16).contiguous()
+
+
+def _run(r, prob, summ, status=sa.SA_OK, ws=None):
+    ws = ws or sa.Workspace(prob, rows=True, max_rows=r.n_rows)
+    ws.buf[256:].fill_(255)
+    idx = torch.full((r.n_rows, r.Hq, prob.kcap), -7, dtype=torch.int32, device="cuda")
+    cnt = torch.full((r.n_rows, r.Hq), -7, dtype=torch.int32, device="cuda")
+    sa.select_rows(prob, r.q, summ, r.lens, r.offsets, idx, cnt, ws)
+    torch.cuda.synchronize()
+    assert ws.status() == status
+    return idx, cnt
+
+
+def _check(r, prob, summ, **kw):
+    idx, cnt = _run(r, prob, summ, **kw)
+    want = Z.select(r, prob, summ)
+    i, c = idx.cpu().numpy(), cnt.cpu().numpy()
+    for (row, h), w in want.items():
+        assert c[row, h] == len(w), (row, h)
+        assert i[row, h, :len(w)].tolist() == w, (row, h)
+        assert (i[row, h, len(w):] == -7).all()
+    mine = R.owned(r).numpy()
+    assert (i[~mine] == -7).all() and (c[~mine] == -7).all(), "rows of nobody were written"
+    return idx, cnt
+
+
+HEADS = [(8, 2), (28, 4), (8, 1), (4, 4), (12, 4), (5, 1), (12, 2)]
+
+
+@pytest.mark.parametrize("mode", [sa.SUMMARY_MINMAX, sa.SUMMARY_MEAN])
+@pytest.mark.parametrize("group", [False, True])
+@pytest.mark.parametrize("Hq,Hk", HEADS)
+def test_ragged(Hq, Hk, mode, group):
+    r = _rows([40, 1, 0, 9], [300, 5000, 20, 1200], Hq, Hk, seed=Hq)
+    bs = [(16, 8, 64, 32)[h % 4] for h in range(Hk)]
+    k = [5] * Hq if group else [(h * 3) % 11 for h in range(Hq)]
+    prob = Z.problem(r, bs, k, 4, 64, mode=mode, selection=sa.SELECT_GROUP if group else sa.SELECT_PER_HEAD)
+    _check(r, prob, _summaries(prob, Hq))
+
+
+@pytest.mark.parametrize("kind", ["coarse", "equal"])
+@pytest.mark.parametrize("mode", [sa.SUMMARY_MINMAX, sa.SUMMARY_MEAN])
+def test_ties_go_to_the_lowest(kind, mode):
+    r = _rows([20], [3000], 8, 2, seed=3)
+    if kind == "coarse":
+        r.q.sign_()
+    prob = Z.problem(r, [8, 16], 37, 4, 64, mode=mode)
+    _check(r, prob, _summaries(prob, 3, kind))
+
+
+@pytest.mark.parametrize("S,W", [(0, 64), (1, 64), (63, 64), (64, 65), (200, 300)])
+@pytest.mark.parametrize("bs", [8, 64])
+def test_candidates(S, W, bs):
+    r = _rows([150, 3], [230, 600], 8, 2, seed=S)
+    prob = Z.problem(r, bs, 3, S, W)
+    _check(r, prob, _summaries(prob, 4))
+
+
+@pytest.mark.parametrize("k", [0, 1, 2, 31, 32, 33, 63, 64, 200, 1000])
+def test_budgets(k):
+    r = _rows([5], [2000], 4, 2, seed=k)
+    prob = Z.problem(r, 16, k, 4, 64)
+    _check(r, prob, _summaries(prob, 5))
+
+
+def test_long():
+    r = _rows([2, 3], [150000, 70000], 4, 1, seed=6)
+    prob = Z.problem(r, 8, 700, 4, 1024)
+    _check(r, prob, _summaries(prob, 6))
+    r = _rows([600], [8000], 4, 1, seed=7)
+    prob = Z.problem(r, 16, 24, 4, 256, mode=sa.SUMMARY_MEAN)
+    _check(r, prob, _summaries(prob, 7))
+
+
+def test_close_scores():
+    # scores that differ in the last bits: the order of their sums decides
+    r = _rows([64], [4000], 8, 2, seed=8)
+    prob = Z.problem(r, 16, 20, 4, 64, mode=sa.SUMMARY_MEAN)
+    summ = _summaries(prob, 8)
+    summ[:] = summ[:, :, :1]
+    perm = torch.randperm(128, generator=torch.Generator().manual_seed(1)).tolist()
+    for j in range(0, summ.shape[2], 2):      # every other block with dims swapped in pairs and tiny changes
+        summ[:, :, j, perm[j % 128]] *= 1 + 2.0 ** -7
+    _check(r, prob, summ)
+
+
+@pytest.mark.parametrize("mode", [sa.SUMMARY_MINMAX, sa.SUMMARY_MEAN])
+def test_values_at_the_ends(mode):
+    # zeros of both signs, the largest and smallest values, infinite summaries
+    r = _rows([24], [1000], 8, 2, seed=9)
+    r.q[0] = 0.0
+    r.q[1] = -0.0
+    r.q[2, :, ::2] = 0
+    r.q[3] = 0
+    r.q[3, :, 5] = 3e38       # one product alone: infinities of both signs would make NaN
+    r.q[4] *= 2.0 ** -100
+    prob = Z.problem(r, [8, 16], 9, 4, 64, mode=mode)
+    summ = _summaries(prob, 9)
+    summ[0, 0, 3, ..., 5] = 3e38
+    summ[0, 0, 7, ..., 5] = -3e38
+    summ[0, 1, 5] *= 2.0 ** -60
+    _check(r, prob, summ)
+    # an infinity among blocks that rows with positive queries take first
+    r.q.abs_().clamp_(min=0.125, max=4)
+    summ = summ.clamp(-4, 4)
+    (summ[0, 0, 11, 1] if mode == sa.SUMMARY_MINMAX else summ[0, 0, 11])[20] = float("inf")
+    idx, cnt = _check(r, prob, summ)
+    assert bool((idx[:, :4] == 11).any(-1).all())
+
+
+def test_rows_of_nobody_and_rows_without_a_position():
+    r = _rows([12, 5], [400, 300], 8, 2, seed=10, lead=5, extra=30)
+    prob = Z.problem(r, 16, 4, 4, 64)
+    _check(r, prob, _summaries(prob, 10))
+    r = _rows([300], [0], 8, 2, seed=11)
+    r.lens[0] = 270
+    prob = Z.problem(r, 16, 4, 4, 64)
+    idx, cnt = _check(r, prob, _summaries(prob, 11))
+    assert bool((cnt[:30] == 0).all())
+
+
+def test_behind_the_table():
+    r = _rows([40], [700], 8, 2, seed=12, mpp=40)
+    prob = Z.problem(r, 16, 4, 4, 64)
+    _check(r, prob, _summaries(prob, 12), status=sa.SA_ERR_CAPACITY)
+
+
+def test_many_sequences_and_replay():
+    rows = [(i * 5) % 4 for i in range(300)]
+    r = _rows(rows, [200 + (i * 37) % 900 for i in range(300)], 4, 2, seed=13)
+    prob = Z.problem(r, [16, 32], 6, 4, 64)
+    summ = _summaries(prob, 13)
+    idx, cnt = _check(r, prob, summ)
+    ws = sa.Workspace(prob, rows=True, max_rows=r.n_rows)
+    i2, c2 = torch.full_like(idx, -7), torch.full_like(cnt, -7)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.select_rows(prob, r.q, summ, r.lens, r.offsets, i2, c2, ws)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(i2, idx) and torch.equal(c2, cnt)
