@@ -603,7 +603,7 @@ size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows);
  * sa_prompt_attention, rounded alike; a row that sees nothing gets out = 0,
  * lse = -inf; what a row does not see cannot change it.  Pages that several
  * neighbouring rows see are read once for all of them.
- * A page table with more than 1638400 columns gives SA_ERR_UNSUPPORTED. */
+ * A page table with more than 819200 columns gives SA_ERR_UNSUPPORTED. */
 int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
                             const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,
                             const int32_t* row_offsets, const int32_t* sel_idx, const int32_t* sel_cnt, void* out,

@@ -59,10 +59,10 @@ __device__ __forceinline__ RowSeq shared_rows(const int* row_offsets, const int*
 
 // ---------------------------------------------------------------- attention
 
-// One KV head of a sequence with up to a query tile of its rows, and the
-// tiles of eight pages each that they see some of.
+// One KV head of a sequence with up to two query tiles of its rows, and how
+// many pages they see some of.
 struct __align__(16) SparseItem {
-  int b, kvh, i, tiles;
+  int b, kvh, i, pages;
   int row0, tokens, pos0, end;      // first packed row, rows, position of the first, first position that none sees
 };
 // What work weighs: a tile, and an item's query load, first tile and epilogue.
@@ -98,8 +98,10 @@ struct RowsAttnArgs {
   SparseItem* items;                // [n_items]
   long long* before;                // [n_items + 1] weight of the items before
   uint32_t* pages;                  // [n_items][words] a bit for each page that some row of the item sees
+  int* ranks;                       // [n_rows][Hq][rank_stride] a row's blocks as places in that list
+  int* ticket;                      // the next item to take (of those behind one a block), items there are
   int n_items, words;               // at most that many; ceil(mpp / 32)
-  int kcap, S, W;
+  int kcap, rank_stride, S, W;      // rank_stride: kcap up to a multiple of four
   unsigned char bs_shift[SA_MAX_HK];
 };
 

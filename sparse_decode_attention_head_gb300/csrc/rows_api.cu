@@ -32,7 +32,7 @@ int make_params(const sa_problem* prob, Params* p) {
 }
 
 constexpr long long kMaxItems = 1 << 30;     // indices of items are 32-bit
-constexpr int kMaxSparsePages = 200 * 1024 * 8;   // an item's bitmap of pages lies in shared memory: 26 M tokens
+constexpr int kMaxSparsePages = 100 * 1024 * 8;   // an item's bitmap of pages lies in shared memory: 13 M tokens
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
@@ -76,26 +76,31 @@ SharedLayout shared_layout(const Params& p, int n_rows) {
 
 // Items of the calls with selected blocks, `rows` rows and heads each.
 long long max_items(const Params& p, int n_rows, int rows) {
-  const int T = rows / p.G;
+  const int T = rows == 256 ? 2 * (128 / p.G) : rows / p.G;
   return ((long long)n_rows / T + std::min(p.B, n_rows)) * p.Hk;
 }
 
 // The sparse attention's items behind the partials.
 struct SparseLayout {
-  size_t items, before, pages, total;
-  int words;
+  size_t items, before, ticket, pages, ranks, total;
+  int words, rank_stride;
 };
 SparseLayout sparse_layout(const Params& p, int n_rows) {
-  const size_t n = (size_t)max_items(p, n_rows, 128);
+  const size_t n = (size_t)max_items(p, n_rows, 256);
   SparseLayout l;
   l.words = (p.mpp + 31) / 32;
+  l.rank_stride = (p.kcap + 3) & ~3;
   size_t off = attn_layout().total;
   l.items = off;
   off = up(off + n * sizeof(sa::SparseItem));
   l.before = off;
   off = up(off + (n + 1) * sizeof(long long));
+  l.ticket = off;
+  off = up(off + 2 * sizeof(int));
   l.pages = off;
   off = up(off + n * l.words * sizeof(uint32_t));
+  l.ranks = off;
+  off = up(off + (size_t)n_rows * p.Hq * l.rank_stride * sizeof(int));
   l.total = off;
   return l;
 }
@@ -451,9 +456,12 @@ int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* 
   A.sel_cnt = sel_cnt;
   A.items = at<sa::SparseItem>(ws, l.items);
   A.before = at<long long>(ws, l.before);
+  A.ticket = at<int>(ws, l.ticket);
   A.pages = at<uint32_t>(ws, l.pages);
-  A.n_items = (int)max_items(p, n_rows, 128);
+  A.n_items = (int)max_items(p, n_rows, 256);
   A.words = l.words;
+  A.ranks = at<int>(ws, l.ranks);
+  A.rank_stride = l.rank_stride;
   A.kcap = p.kcap;
   A.S = std::min(p.S, 1 << 30);
   A.W = std::min(p.W, 1 << 30);

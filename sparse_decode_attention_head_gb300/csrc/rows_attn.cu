@@ -99,10 +99,6 @@ enum Kind {
   kShared,    // the same, with the prefix of a group of sequences as an item of its own
   kSparse,    // causal rows over sinks, window and the blocks of their lists
 };
-// Query tiles of an item; with selected blocks one, whose rows see more alike.
-template <int KIND>
-constexpr int kQTiles = KIND == kSparse ? 1 : 2;
-
 // A piece of a block's run: KV tiles [k0, k1) of one item.  The loading warp
 // walks the run and hands the pieces to the other roles through a ring.
 struct Piece {
@@ -114,8 +110,9 @@ struct Piece {
   int a;              // tokens of the sequence ahead of its rows
   int first;          // the item's first row in the sequence
   int to;             // Part: where the result goes
+  int u;              // kSparse: the item,
+  int out;            // and how many halves of pages, ahead of its window's, are not in its list
   long long pt;       // entry of the page table with the item's position 0
-  int u;              // kSparse: the item
   bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
 };
 
@@ -139,20 +136,16 @@ struct alignas(16) Ctl {
   float2 ml[kRows];          // (maximum, sum) of the second softmax group
 };
 
-// kSparse: what the rows see of a tile, a ring.  The loading warp names the
-// tile's pages, two warps look each row up in its list and leave 16 bits a
-// row, a bit for 8 tokens.
-constexpr int kMaskDepth = 8;            // K and V slots let the loads run at most four tiles ahead of the softmax
-struct alignas(16) MaskCtl {
-  uint64_t page_full[kMaskDepth], mask_full[kMaskDepth];
-  int page[kMaskDepth][8];               // ascending; -1 behind the item's last
-  int cut[kMaskDepth];                   // some row's view begins or ends inside 8 of its tokens
-  uint16_t mask[kMaskDepth][kRows];
+// kSparse: the pages of the last tiles loaded, ascending, -1 behind an item's
+// last.  K and V slots let the loads run at most four tiles ahead of the softmax.
+constexpr int kPageDepth = 8;
+struct alignas(16) PageRing {
+  int page[kPageDepth][8];
 };
 template <int KIND>
-constexpr size_t kSmemBytes = 1024 + (kQTiles<KIND> + kSlots) * kTileBytes + sizeof(Ctl) +
-                              (KIND == kSparse ? sizeof(MaskCtl) : 0);
-static_assert(kSmemBytes<kPlain> <= 227 * 1024 && kSmemBytes<kSparse> <= 227 * 1024, "shared memory");
+constexpr size_t kSmemBytes = 1024 + (2 + kSlots) * kTileBytes + sizeof(Ctl) + (KIND == kSparse ? sizeof(PageRing) : 0);
+static_assert(kSmemBytes<kSparse> <= 227 * 1024, "shared memory");
+constexpr uint32_t kCut = 256;           // beside a tile's bad pages: some row's view begins or ends inside 8 tokens
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -247,7 +240,7 @@ template <int KIND>
 __device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int v, int* status) {
   const int b = KIND == kShared ? v >> 1 : v;
   Seq s;
-  s.T = kQTiles<KIND> * A.tpt;
+  s.T = 2 * A.tpt;
   s.to = kAll;
   s.pt = (long long)b * A.mpp;
   if (KIND == kShared && (v & 1) == 0) {
@@ -477,19 +470,39 @@ struct Walk {
   }
 };
 
-// With selected blocks: the items lie one behind the other with the weight of
-// those before them.
+// With selected blocks: the items lie one behind the other.  Where they are
+// many, a block takes whole ones, the next when it is done with the last: the
+// items under way at a time are neighbours, whose pages L2 holds.  Else each
+// block has its share of their weight, and cuts items.
+constexpr int kWholeItems = 8;       // a block, from which they are taken whole (5.7 a block: 426 us cut, 443 whole)
+__device__ __forceinline__ bool whole_items(const RowsAttnArgs& A) {
+  return __ldg(A.ticket + 1) >= kWholeItems * (int)gridDim.x;
+}
 template <>
 struct Walk<kSparse> {
   const RowsAttnArgs& A;
-  int u, kt;
+  int u, kt, ahead;
   int4 end;
   SparseItem it;
+  bool whole;
   __device__ Walk(const RowsAttnArgs& a, const Ctl* c) : A(a) {
-    u = c->range[0].x;
-    kt = c->range[0].y;
-    end = c->range[1];
+    whole = whole_items(A);
+    if (whole) {
+      u = blockIdx.x;
+      kt = 0;
+      end = make_int4(__ldg(A.ticket + 1), 0, 0, 0);
+      ahead = take();
+    } else {
+      u = c->range[0].x;
+      kt = c->range[0].y;
+      end = c->range[1];
+    }
     load();
+  }
+  __device__ int take() {      // a whole warp
+    int x = 0;
+    if ((threadIdx.x & 31) == 0) x = (int)gridDim.x + atomicAdd(A.ticket, 1);
+    return __shfl_sync(0xffffffffu, x, 0);
   }
   __device__ void load() {
     if (u < A.n_items) {
@@ -502,25 +515,27 @@ struct Walk<kSparse> {
     while (u < end.x || (u == end.x && kt < end.y)) {
       const bool at_end = u == end.x;
       p.b = it.b; p.kvh = it.kvh; p.i = it.i;
-      p.nt = it.tiles;
+      p.nt = (it.pages + 7) / 8;
       p.k0 = kt;
-      p.k1 = at_end ? end.y : it.tiles;
+      p.k1 = at_end ? end.y : p.nt;
       p.row0 = it.row0;
       p.tokens = it.tokens;
       p.end = it.end;
-      p.edge = (it.tiles - 1) * kRows + 1;       // the last tile alone holds positions that no row sees
+      p.edge = (p.nt - 1) * kRows + 1;           // the last tile alone holds positions that no row sees
       p.a = it.pos0;
       p.first = 0;
       p.to = kAll;
       p.pt = (long long)it.b * A.mpp;
       p.u = u;
-      p.dual = true;
+      p.out = 2 * ((it.end + kP - 1) / kP - it.pages);
+      p.dual = it.tokens <= A.tpt;
       const bool some = p.k0 < p.k1 || (p.nt == 0 && p.tokens > 0 && !at_end);
       kt = 0;
       if (at_end) {
         end.y = 0;
       } else {
-        ++u;
+        u = whole ? ahead : u + 1;
+        if (whole && u < end.x) ahead = take();
         load();
       }
       if (some) return true;
@@ -541,7 +556,7 @@ __device__ __forceinline__ int4 locate_item(const RowsAttnArgs& A, long long w) 
     lo += step * n;
   }
   const long long w0 = __ldg(A.before + lo), w1 = __ldg(A.before + lo + 1);
-  return make_int4(lo, (int)((w - w0) * A.items[lo].tiles / (w1 - w0)), 0, 0);
+  return make_int4(lo, (int)((w - w0) * ((A.items[lo].pages + 7) / 8) / (w1 - w0)), 0, 0);
 }
 
 // ---------------------------------------------------------------- what a row sees of selected blocks
@@ -595,34 +610,60 @@ struct PageWalk<kSparse> {
   }
 };
 
-// A row's list, walked along ascending blocks.
-struct ListWalk {
-  const int* list;
-  int n, at;            // entries, the next to load
-  int cur, nxt;
-  __device__ __forceinline__ int get(int j) const { return j < n ? __ldg(list + j) : 0x7fffffff; }
-  __device__ __forceinline__ void start(const int* l, int count, int from) {   // from: the first block asked for
-    list = l;
-    n = count;
-    int lo = 0, hi = n;
-    if (from > 0) {
+// A row's blocks as places in the item's list of pages, in halves of pages,
+// ascending (sparse_items_kernel writes them), along ascending tiles of 16
+// halves.  Four at a time, the next four on their way.
+struct RankWalk {
+  const int4* list;
+  int groups, at;          // of four; the next to load
+  int4 now, next;
+  int used;                // of `now`
+  uint32_t acc;            // halves from the last tile's first on
+  __device__ __forceinline__ int4 get(int j) const {
+    constexpr int kNone = 0x7fffffff;
+    return j < groups ? __ldg(list + j) : make_int4(kNone, kNone, kNone, kNone);
+  }
+  // blocks of `len` halves, those ahead of tile t0 passed over
+  __device__ __forceinline__ void start(const int* l, int n_groups, int len, int t0) {
+    list = reinterpret_cast<const int4*>(l);
+    groups = n_groups;
+    int lo = 0, hi = groups;          // the first group whose last block reaches into the tile
+    if (t0 > 0) {
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(l + mid) < from) lo = mid + 1; else hi = mid;
+        if (__ldg(l + 4 * mid + 3) <= 16 * t0 - len) lo = mid + 1; else hi = mid;
       }
     }
-    cur = get(lo);
-    nxt = get(lo + 1);
+    now = get(lo);
+    next = get(lo + 1);
     at = lo + 2;
+    used = 0;
+    acc = 0;
   }
-  __device__ __forceinline__ bool has(int e) {
-    while (cur < e) {
-      cur = nxt;
-      nxt = get(at++);
+  // A bit for each half of tile t that the row's blocks hold; `by` tiles on from the last one asked for.
+  __device__ __forceinline__ uint32_t mask(int t, int by, int len) {
+    acc = by == 1 ? acc >> 16 : 0;    // a block is at most 8 halves: it reaches into one more tile
+    while (now.x < 16 * t + 16) {
+      const int sh = now.x - 16 * t;
+      const uint32_t ones = (1u << len) - 1u;
+      if (sh > -8) acc |= sh >= 0 ? ones << sh : ones >> -sh;
+      now.x = now.y;
+      now.y = now.z;
+      now.z = now.w;
+      if (++used == 4) {
+        now = next;
+        next = get(at++);
+        used = 0;
+      }
     }
-    return cur == e;
+    return acc & 0xffffu;
   }
 };
+// Bits [a, b) of 16, from `base` on.
+__device__ __forceinline__ uint32_t bits16(int a, int b, int base) {
+  const uint32_t lo = (1u << min(max(a - base, 0), 16)) - 1u, hi = (1u << min(max(b - base, 0), 16)) - 1u;
+  return hi & ~lo;
+}
 
 // The sums of one row over one piece from its definition, by a whole warp:
 // dims 4 lane on.  Taken where the product of a tile with V is not finite: a
@@ -746,18 +787,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;                                  // two tiles: [half of the dims][128 rows][64]
-  uint8_t* s_kv = smem + kQTiles<KIND> * kTileBytes;    // kSlots tiles: [16 groups of 8 tokens][half][8][64]
+  uint8_t* s_kv = smem + 2 * kTileBytes;                // kSlots tiles: [16 groups of 8 tokens][half][8][64]
   Ctl* c = reinterpret_cast<Ctl*>(s_kv + kSlots * kTileBytes);
-  MaskCtl* mc = reinterpret_cast<MaskCtl*>(c + 1);      // kSparse
+  PageRing* ring = reinterpret_cast<PageRing*>(c + 1);  // kSparse
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    if constexpr (KIND == kSparse) {
-      for (int i = 0; i < kMaskDepth; ++i) {
-        mbar_init(&mc->page_full[i], 1);
-        mbar_init(&mc->mask_full[i], 2);
-      }
-    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&c->full[i], 1);
       mbar_init(&c->empty[i], 1);
@@ -792,7 +827,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
   pdl_wait();
   pdl_trigger();
   if constexpr (KIND == kSparse) {
-    if (warp < 2) {
+    if (warp < 2 && !whole_items(A)) {
       const int4 r = locate_item(A, __ldg(A.before + A.n_items) * (blockIdx.x + warp) / gridDim.x);
       if (lane == 0) c->range[warp] = r;
     }
@@ -849,16 +884,23 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       }
       const float lag = valid ? kLag : INFINITY;   // a lane without a row never grows
       float m = -INFINITY, l = 0.f;
+      RankWalk walk;
+      int sink = 0, win0 = 0, win1 = 0, len = 0;     // kSparse: whole halves of sinks and window, of a block
+      if constexpr (KIND == kSparse) {
+        len = (1 << A.bs_shift[p.kvh]) / 8;
+        const size_t row = (size_t)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
+        walk.start(A.ranks + (valid ? row * A.rank_stride : 0), valid && lim > 0 ? A.rank_stride / 4 : 0, len, k0);
+        sink = min(A.S, min(lim, p.end)) >> 3;
+        win0 = ((max(lim - A.W, 0) + 7) >> 3) - p.out;
+        win1 = (min(lim, p.end) >> 3) - p.out;
+      }
       for (int s = h; s < N; s += 2) {
         const int t = dual ? s : s >> 1;
         const int kt = k0 + t;
         uint32_t mask = 0;
-        bool cut = false;
-        const int place = (int)((tiles + t) % kMaskDepth);
-        if constexpr (KIND == kSparse) {
-          if (!(ok = wait_warp(&mc->mask_full[place], ((tiles + t) / kMaskDepth) & 1, c, A.status))) break;
-          mask = mc->mask[place][r];
-          cut = mc->cut[place] != 0;
+        if constexpr (KIND == kSparse) {     // while the product is under way
+          mask = walk.mask(kt, dual ? 2 : 1, len) | bits16(0, sink, 16 * kt) | bits16(win0, win1, 16 * kt);
+          if (lim <= 0) mask = 0;
         }
         if (!(ok = wait_warp(&c->s_full[h], steps_done & 1, c, A.status))) break;
         ++steps_done;
@@ -868,13 +910,13 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
         tmem_ld64_finish<0>(v);
         if constexpr (KIND == kSparse) {
-          if (cut || bad != 0) {
+          if (bad != 0) {
 #pragma unroll 1
             for (int w = 0; w < 4; ++w) {
               uint32_t see = 0;            // bit j: column 32 w + j
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int page = mc->page[place][2 * w + (e >> 1)], t0 = page * kP + 8 * (e & 1);
+                const int page = ring->page[(tiles + t) % kPageDepth][2 * w + (e >> 1)], t0 = page * kP + 8 * (e & 1);
                 auto below = [t0](int x) { return (1u << min(max(x - t0, 0), 8)) - 1u; };   // of 8 tokens, those before x
                 uint32_t x = (mask >> (4 * w + e)) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
                 x &= page < 0 || ((bad >> (2 * w + (e >> 1))) & 1u) ? 0u : below(lim);
@@ -1306,14 +1348,18 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         const int* pt = A.page_table + p.pt;
         PageWalk<KIND> pages(A, p, 8 * p.k0);
         bool next_there = false;
+        uint32_t next_cut = 0;
         auto page_of = [&](int t) {
           int page;
           if constexpr (KIND == kSparse) {
             if (t == ntp) return -1;
-            const int place = (int)((tile + t) % kMaskDepth);
-            pages.next(mc->page[place]);
-            if (lane == 0) mbar_arrive(&mc->page_full[place]);
-            page = lane < kRows / kP ? mc->page[place][lane] : -1;
+            int* place = ring->page[(tile + t) % kPageDepth];
+            pages.next(place);
+            page = lane < kRows / kP ? place[lane] : -1;
+            // views begin or end inside 8 tokens where the sinks do, and where rows' windows and the rows themselves are
+            const int t0 = page * kP, w0 = p.a + 1 - A.W, w1 = w0 + p.tokens - 1;
+            const bool in = ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) || t0 + kP > p.a;
+            next_cut = __any_sync(0xffffffffu, page >= 0 && in) ? kCut : 0;
             next_there = page >= 0;
           } else {
             page = (p.k0 + t) * (kRows / kP) + lane;
@@ -1324,6 +1370,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         int next_phys = page_of(0);
         for (int t = 0; t < ntp; ++t) {
           const bool there = next_there;
+          const uint32_t cut = next_cut;
           const int phys = next_phys;
           next_phys = page_of(t + 1);
           const bool good = phys >= 0 && phys < A.num_pages;
@@ -1334,7 +1381,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
             if (idx >= kSlots && !(ok = wait_warp(&c->empty[slot], (idx / kSlots - 1) & 1, c, A.status))) break;
             uint8_t* dst = s_kv + slot * kTileBytes;
             if (kv == 0) {
-              if (lane == 0) *(volatile uint32_t*)&c->bad[(tile + t) & 15] = bads;
+              if (lane == 0) *(volatile uint32_t*)&c->bad[(tile + t) & 15] = bads | cut;
             } else if (bads != 0) {   // V of a page that is not there: zeros
               for (int x = lane; x < kTileBytes / 16; x += 32)
                 if ((bads >> (x >> 8)) & 1u) reinterpret_cast<uint4*>(dst)[x] = make_uint4(0, 0, 0, 0);
@@ -1367,69 +1414,13 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       // slot, so the parity of its full barrier alone would not tell which one
       uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
       bool ok = true;
-      const int bit = w * 32 + lane;         // kSparse: rows bit and 64 + bit
       for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
         const Piece p = c->piece[piece % kPieces];
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
         if (p.k0 < 0) break;
         const int ntp = p.k1 - p.k0;
-        ListWalk walk[2];
-        int pos[2];
-        if constexpr (KIND == kSparse) {
-          if (ntp > 0) {
-            if (!(ok = wait_warp(&mc->page_full[tile % kMaskDepth], (tile / kMaskDepth) & 1, c, A.status))) break;
-            const int from = p.k0 > 0 ? mc->page[tile % kMaskDepth][0] * kP >> A.bs_shift[p.kvh] : 0;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int r = bit + 64 * x, tok = r / A.G;
-              pos[x] = tok < A.tpt && tok < p.tokens ? p.a + tok : -1;
-              const size_t row = (size_t)(p.row0 + tok) * A.Hq + p.kvh * A.G + (r - tok * A.G);
-              if (pos[x] >= 0)
-                walk[x].start(A.sel_idx + row * A.kcap, min(max(__ldg(A.sel_cnt + row), 0), A.kcap), from);
-            }
-          }
-        }
-        for (int t = KIND == kSparse ? 0 : max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
-          if constexpr (KIND == kSparse) {
-            const int place = (int)((tile + t) % kMaskDepth);
-            if (!(ok = wait_warp(&mc->page_full[place], ((tile + t) / kMaskDepth) & 1, c, A.status))) break;
-            const int shift = A.bs_shift[p.kvh];
-            // views that begin or end inside 8 tokens: in the page with the sinks' end, and where rows' windows and
-            // the rows themselves begin
-            const int w0 = p.a + 1 - A.W, w1 = w0 + p.tokens - 1;
-            int page[8];
-            *reinterpret_cast<int4*>(page) = *reinterpret_cast<const int4*>(mc->page[place]);
-            *reinterpret_cast<int4*>(page + 4) = *reinterpret_cast<const int4*>(mc->page[place] + 4);
-            uint32_t seen[2] = {0, 0};
-            bool cut = false;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (page[j] < 0) continue;
-              const int t0 = page[j] * kP;
-              cut |= ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) || t0 + kP > p.a;
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                if (pos[x] < 0) continue;
-                uint32_t two;
-                if (shift == 3) {
-                  two = walk[x].has(2 * page[j]) ? 1u : 0u;
-                  two |= walk[x].has(2 * page[j] + 1) ? 2u : 0u;
-                } else {
-                  two = walk[x].has(t0 >> shift) ? 3u : 0u;
-                }
-                if (t0 + 8 <= A.S || (t0 > pos[x] - A.W && t0 + 7 <= pos[x])) two |= 1u;
-                if (t0 + 16 <= A.S || (t0 + 8 > pos[x] - A.W && t0 + 15 <= pos[x])) two |= 2u;
-                seen[x] |= two << (2 * j);
-              }
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) mc->mask[place][bit + 64 * x] = (uint16_t)seen[x];
-            if (bit == 0) mc->cut[place] = cut;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mc->mask_full[place]);
-            if (p.k0 + t + 1 < p.nt) continue;
-          }
+        for (int t = max(0, (p.edge >> 7) - p.k0); t < ntp; ++t) {
           const uint32_t idx = 2 * (tile + t) + 1, slot = idx % kSlots;
           if (!(ok = wait_warp(&c->edge_go[slot], (gone >> slot) & 1, c, A.status))) break;
           gone ^= 1u << slot;
@@ -1438,7 +1429,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           // 16-byte chunk x: token group x / 128, row (x / 8) % 8
           uint4* sv = reinterpret_cast<uint4*>(s_kv + slot * kTileBytes);
           if constexpr (KIND == kSparse) {
-            const int* page = mc->page[(tile + t) % kMaskDepth];
+            const int* page = ring->page[(tile + t) % kPageDepth];
             for (int x = w * 32 + lane; x < kTileBytes / 16; x += 64) {
               const int at = page[x >> 8];
               if (at < 0 || at * kP + ((x >> 7) & 1) * 8 + ((x >> 3) & 7) >= p.end) sv[x] = make_uint4(0, 0, 0, 0);

@@ -35,8 +35,8 @@ def test_attention_refusals(lib, kw):  # noqa: F811
 def test_attention_limits(lib):  # noqa: F811
     assert _attend(lib, _prob(D=64)) == BAD
     assert _attend(lib, _prob(page_size=32)) == UNSUP
-    assert _attend(lib, _prob(B=1, max_pages_per_seq=1638401), n=0) == UNSUP
-    assert _attend(lib, _prob(B=1, max_pages_per_seq=1638400), n=0) == sa.SA_OK
+    assert _attend(lib, _prob(B=1, max_pages_per_seq=819201), n=0) == UNSUP
+    assert _attend(lib, _prob(B=1, max_pages_per_seq=819200), n=0) == sa.SA_OK
     assert _attend(lib, _prob(B=1 << 20, max_pages_per_seq=1 << 10)) == UNSUP
     assert _attend(lib, _prob(), n=0, q=None, out=None) == sa.SA_OK
 
