@@ -581,8 +581,8 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
  * were; sel_cnt: [n_rows][Hq] int32.  Rows of nobody are left as they were; a
  * row without a position (more rows than tokens) has count 0.
  * max_rows rows need a workspace of
- * sa_sparse_workspace_size; more than about 2^30 / Hk rows give
- * SA_ERR_UNSUPPORTED. */
+ * sa_sparse_workspace_size; more than about 2^30 / Hk rows, or more
+ * than 65536 block slots, give SA_ERR_UNSUPPORTED. */
 int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const void* summaries,
                    const int32_t* seq_lens, const int32_t* row_offsets, int32_t* sel_idx, int32_t* sel_cnt, void* ws,
                    void* stream);

@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libsa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["summarize.cu", "select.cu", "decode.cu", "merge.cu", "sa_api.cu", "noalloc.cu", "tables.cu", "step.cu",
            "tokens.cu", "bypass.cu", "rows_attn.cu", "rotate.cu", "pages.cu", "prefixes.cu",
-           "rows_items.cu", "rows_select.cu", "rows_api.cu"]
+           "rows_items.cu", "rows_select.cu", "rows_select_tc.cu", "rows_api.cu"]
 
 
 def nvcc() -> str:

@@ -169,7 +169,8 @@ struct SelectArgs {
   const int *row_offsets, *seq_lens;
   int* sel_idx;                     // [n_rows][Hq][kcap]
   int* sel_cnt;                     // [n_rows][Hq]
-  float* scores;                    // [block][rows][slots]
+  float* scores;                    // scratch
+  int* norms;                       // [B][Hk] the bits of the largest squared norm of a summary
   int* status;
   int n_rows, n_items, B, Hq, Hk, G, mpp, slots, kcap, S, W;
   bool minmax, group;
@@ -177,9 +178,14 @@ struct SelectArgs {
   int k[SA_MAX_HQ];
 };
 
-int launch_select_rows(const SelectArgs& A, int num_sms, cudaStream_t stream);
-int select_rows_blocks(int num_sms);     // of the scratch
-int select_rows_scratch_rows();          // rows of scores a block has
+// rows_select.cu: any number of rows, up to 65536 candidates
+int launch_score_rows(const SelectArgs& A, int max_candidates, cudaStream_t stream);
+size_t score_rows_scratch(int slots, long long n_items);
+// rows_select_tc.cu: many rows
+constexpr int kTcMaxSlots = 2048;
+int launch_select_tc(const SelectArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmS, int num_sms,
+                     cudaStream_t stream);
+size_t select_tc_scratch(int slots);
 
 // ---------------------------------------------------------------- rotation
 

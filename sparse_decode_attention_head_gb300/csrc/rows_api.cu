@@ -105,9 +105,28 @@ SparseLayout sparse_layout(const Params& p, int n_rows) {
   return l;
 }
 
-size_t select_rows_bytes(const Params& p) {
-  return up(sizeof(sa::WsHeader)) + (size_t)sa::select_rows_blocks(sa::kRowsMaxCtas) * sa::select_rows_scratch_rows() *
-                                        p.slots * sizeof(float);
+// The selection's scratch behind the norms.
+constexpr int kSelectMaxSlots = 1024 * 64;      // candidates that a block's top-k holds
+bool select_by_tensor(const Params& p, int n_rows) {
+  // many rows a sequence: the tensor cores' scores; few: the summaries' bytes
+  // bound both, and scores that are canonical need no second look
+  return p.slots <= sa::kTcMaxSlots && (long long)p.B * p.Hk * p.slots < (1ll << 31) && n_rows >= 64ll * p.B;
+}
+struct SelectLayout {
+  size_t norms, scores, total;
+};
+SelectLayout select_layout(const Params& p, int n_rows) {
+  SelectLayout l;
+  size_t off = up(sizeof(sa::WsHeader));
+  l.norms = off;
+  off = up(off + (size_t)p.B * p.Hk * sizeof(int));
+  l.scores = off;
+  // a workspace for n_rows serves fewer too, in either form
+  size_t scores = sa::score_rows_scratch(p.slots, max_items(p, n_rows, 32));
+  if (select_by_tensor(p, n_rows)) scores = std::max(scores, sa::select_tc_scratch(p.slots));
+  off = up(off + scores);
+  l.total = off;
+  return l;
 }
 
 struct PageLayout {
@@ -129,15 +148,31 @@ PageLayout page_layout(const Params& p) {
   return l;
 }
 
-// q [n_rows][Hq][D] as boxes of 64 dims x G heads x 128 / G tokens.
-int make_q_map(CUtensorMap* m, const void* q, int n_rows, const Params& p, int tpt) {
+// q [n_rows][Hq][D] as boxes of 64 dims x some heads x some tokens.
+int make_q_map(CUtensorMap* m, const void* q, int n_rows, const Params& p, int tokens, int heads) {
   auto fn = sa_host::encode_fn();
   if (fn == nullptr) return SA_ERR_CUDA;
   cuuint64_t dims[3] = {SA_HEAD_DIM, (cuuint64_t)p.Hq, (cuuint64_t)n_rows};
   cuuint64_t strides[2] = {SA_HEAD_DIM * 2, (cuuint64_t)p.Hq * SA_HEAD_DIM * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tpt};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
+}
+
+// Summaries [B][Hk][slots] as boxes of 64 dims of the minimum, the maximum or
+// the mean of 64 blocks.
+int make_summary_map(CUtensorMap* m, const void* summaries, const Params& p) {
+  auto fn = sa_host::encode_fn();
+  if (fn == nullptr) return SA_ERR_CUDA;
+  const cuuint64_t kinds = p.mode == SA_SUMMARY_MINMAX ? 2 : 1;
+  cuuint64_t dims[3] = {SA_HEAD_DIM, kinds, (cuuint64_t)p.B * p.Hk * p.slots};
+  cuuint64_t strides[2] = {SA_HEAD_DIM * 2, kinds * SA_HEAD_DIM * 2};
+  cuuint32_t box[3] = {64, 1, 64};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(summaries), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SA_OK : SA_ERR_CUDA;
@@ -189,7 +224,7 @@ int attention_args(const sa_problem* prob, int32_t n_rows, const void* q, const 
   sa::RowsAttnArgs& A = c->A;
   A = sa::RowsAttnArgs{};
   A.tpt = 128 / p.G;
-  if ((rc = make_q_map(&c->tmQ, q, n_rows, p, A.tpt)) != SA_OK) return rc;
+  if ((rc = make_q_map(&c->tmQ, q, n_rows, p, A.tpt, p.G)) != SA_OK) return rc;
   if ((rc = make_tile_map(&c->tmK, k_pool, p)) != SA_OK) return rc;
   if ((rc = make_tile_map(&c->tmV, v_pool, p)) != SA_OK) return rc;
   const AttnLayout l = attn_layout();
@@ -394,7 +429,8 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
 size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows) {
   Params p;
   if (make_params(prob, &p) != SA_OK || max_rows < 0 || max_items(p, max_rows, 32) > kMaxItems) return 0;
-  return std::max({sa_rows_workspace_size(prob), sparse_layout(p, max_rows).total, select_rows_bytes(p)});
+  return std::max({sa_rows_workspace_size(prob), sparse_layout(p, max_rows).total,
+                   p.slots <= kSelectMaxSlots ? select_layout(p, max_rows).total : 0});
 }
 
 int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const void* summaries,
@@ -404,7 +440,7 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   const int rc = make_params(prob, &p);
   if (rc != SA_OK) return rc;
   if (n_rows < 0 || !summaries || !seq_lens || !row_offsets || !ws) return SA_ERR_INVALID_ARG;
-  if (max_items(p, n_rows, 32) > kMaxItems) return SA_ERR_UNSUPPORTED;
+  if (max_items(p, n_rows, 32) > kMaxItems || p.slots > kSelectMaxSlots) return SA_ERR_UNSUPPORTED;
   if (n_rows == 0) return SA_OK;
   if (!q || !sel_idx || !sel_cnt) return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(summaries) || !aligned16(ws)) return SA_ERR_INVALID_ARG;
@@ -417,10 +453,11 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   A.seq_lens = seq_lens;
   A.sel_idx = sel_idx;
   A.sel_cnt = sel_cnt;
-  A.scores = at<float>(ws, up(sizeof(sa::WsHeader)));
+  const SelectLayout l = select_layout(p, n_rows);
+  A.scores = at<float>(ws, l.scores);
+  A.norms = at<int>(ws, l.norms);
   A.status = at<int>(ws, 0);
   A.n_rows = n_rows;
-  A.n_items = (int)max_items(p, n_rows, 32);
   A.B = p.B;
   A.Hq = p.Hq;
   A.Hk = p.Hk;
@@ -434,7 +471,16 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   A.group = p.sel_mode == SA_SELECT_GROUP;
   std::copy(p.bs, p.bs + p.Hk, A.bs);
   std::copy(p.k, p.k + p.Hq, A.k);
-  return sa::launch_select_rows(A, std::min(nsm, sa::kRowsMaxCtas), as_stream(stream));
+  if (!select_by_tensor(p, n_rows)) {
+    A.n_items = (int)max_items(p, n_rows, 32);
+    return sa::launch_score_rows(A, p.slots, as_stream(stream));
+  }
+  const int T = A.group ? 128 : 128 / p.G;
+  A.n_items = (int)(((long long)n_rows / T + std::min(p.B, n_rows)) * p.Hk);
+  CUtensorMap tmQ, tmS;
+  int e = make_q_map(&tmQ, q, n_rows, p, T, A.group ? 1 : p.G);
+  if (e == SA_OK) e = make_summary_map(&tmS, summaries, p);
+  return e == SA_OK ? sa::launch_select_tc(A, tmQ, tmS, std::min(nsm, sa::kRowsMaxCtas), as_stream(stream)) : e;
 }
 
 int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,

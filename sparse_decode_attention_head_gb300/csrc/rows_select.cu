@@ -5,26 +5,21 @@
 // upwards, lanes joined 4, 2 and 1 apart), so a row's list is the one that a
 // decode step of its length writes, bit for bit.
 //
-// A block takes an item, one KV head with 32 / G neighbouring rows of a
-// sequence (up to 32 rows and heads), scores 64 candidate blocks at a time
-// from shared memory, four rows by two blocks a thread, and leaves the scores
-// in a scratch of its own; then a warp a row finds the k-th score by halving
-// the range of keys and writes the list in order.
-#include "rows.cuh"
-#include "topk.cuh"
+// This form scores on the CUDA cores: drafts and single tokens, whose few rows
+// under a KV head leave the summaries' bytes as the bound, and caches with more
+// candidates than rows_select_tc.cu takes.  A block scores 32 rows and heads
+// (an item) against a stretch of blocks, 64 at a time from shared memory, four
+// rows by two blocks a thread; a second kernel has a block a list for the top-k.
+// Scores go through a scratch; items are taken in runs that fit it.
+#include "rows_select.cuh"
 
 namespace sa {
 namespace {
 
-constexpr int kSelThreads = 256, kSelRows = 32, kSelBlocks = 64;
+constexpr int kSelThreads = 256, kSelRows = 32, kSelBlocks = 64, kSelStretch = 256;
 constexpr int kPad = 16;                              // bytes behind a row in shared memory: no bank is hit twice
 constexpr int kRowStride = kD * 2 + kPad;
-
-// Candidate blocks [j0, j1) of a row at position pos.
-__device__ __forceinline__ void row_candidates(const SelectArgs& A, int pos, int size, int& j0, int& j1) {
-  candidate_range(pos + 1, A.S, A.W, size, j0, j1);
-  j1 = min(j1, (A.mpp * kP + size - 1) / size);
-}
+constexpr size_t kScratchBytes = 256u << 20;          // at least one item
 
 // The sum of 128 products in the canonical order.
 template <bool MINMAX>
@@ -88,7 +83,7 @@ __device__ __forceinline__ void score_tile(const uint8_t* s_q, const uint8_t* s_
 }
 
 template <bool MINMAX>
-__global__ void __launch_bounds__(kSelThreads) select_rows_kernel(SelectArgs A) {
+__global__ void __launch_bounds__(kSelThreads) score_rows_kernel(SelectArgs A, int u0) {
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* s_q = smem;
   uint8_t* s_hi = smem + kSelRows * kRowStride;
@@ -97,122 +92,110 @@ __global__ void __launch_bounds__(kSelThreads) select_rows_kernel(SelectArgs A) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
+  SelectItem it;
+  if (!select_item<kSelThreads>(A, kSelRows / A.G, u0 + blockIdx.x, &s_place, it)) return;
+  int j0, j1;
+  if (item_candidates(A, it.kvh, it.pos0 + it.tokens - 1, j0, j1)) return;
+  const int from = j0 + blockIdx.y * kSelStretch, to = min(j1, from + kSelStretch);
+  if (from >= to) return;
+  const int h0 = it.kvh * A.G;
+  for (int x = tid; x < kSelRows * (kD / 8); x += kSelThreads) {
+    const int r = x / (kD / 8), d = x % (kD / 8);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < it.tokens * A.G)
+      v = reinterpret_cast<const uint4*>(A.q + ((size_t)(it.row0 + r / A.G) * A.Hq + h0 + r % A.G) * kD)[d];
+    *reinterpret_cast<uint4*>(s_q + r * kRowStride + d * 16) = v;
+  }
+  constexpr int kVecs = (MINMAX ? 2 : 1) * (kD / 8);     // 16-byte pieces of a block's summary
+  const uint4* summ = reinterpret_cast<const uint4*>(A.summaries) + ((size_t)it.b * A.Hk + it.kvh) * A.slots * kVecs;
   float* scratch = A.scores + (size_t)blockIdx.x * kSelRows * A.slots;
-  const int T = kSelRows / A.G;
-  for (int u = blockIdx.x; u < A.n_items; u += gridDim.x) {
-    find_item<kSelThreads>(A.row_offsets, A.seq_lens, A.B, A.n_rows, A.mpp, A.Hk, T, u, A.status, &s_place);
-    const ItemPlace at = s_place;
-    if (at.b < 0) return;
-    const RowSeq s = row_seq(A.row_offsets, A.seq_lens, at.b, A.n_rows, A.mpp, nullptr);
-    const int tokens = min(T, s.n - at.i * T), row0 = s.row0 + at.i * T, pos0 = s.a + at.i * T, rows = tokens * A.G;
-    const int size = A.bs[at.kvh], h0 = at.kvh * A.G;
-    int j0, j1, first0, first1;
-    row_candidates(A, pos0 + tokens - 1, size, j0, j1);       // the last row has the most, and the first ones
-    row_candidates(A, pos0, size, first0, first1);
-    if (first1 > first0) j0 = min(j0, first0);
-    bool all = true;                                          // every head keeps every candidate
-    for (int g = 0; g < A.G; ++g) all &= A.k[h0 + g] >= j1 - j0;
-    if (!all) {
-      for (int x = tid; x < kSelRows * (kD / 8); x += kSelThreads) {
-        const int r = x / (kD / 8), d = x % (kD / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          v = reinterpret_cast<const uint4*>(A.q + ((size_t)(row0 + r / A.G) * A.Hq + h0 + r % A.G) * kD)[d];
-        *reinterpret_cast<uint4*>(s_q + r * kRowStride + d * 16) = v;
-      }
-      const uint4* summ = reinterpret_cast<const uint4*>(A.summaries) +
-                          ((size_t)at.b * A.Hk + at.kvh) * A.slots * (MINMAX ? 2 : 1) * (kD / 8);
-      for (int c0 = j0; c0 < j1; c0 += kSelBlocks) {
-        __syncthreads();
-        for (int x = tid; x < kSelBlocks * (MINMAX ? 2 : 1) * (kD / 8); x += kSelThreads) {
-          const int d = x % (kD / 8), y = x / (kD / 8), c = MINMAX ? y >> 1 : y;
-          const bool low = MINMAX && (y & 1) == 0;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (c0 + c < j1) v = __ldg(summ + ((size_t)(c0 + c) * (MINMAX ? 2 : 1) + (MINMAX ? y & 1 : 0)) * (kD / 8) + d);
-          *reinterpret_cast<uint4*>((low ? s_lo : s_hi) + c * kRowStride + d * 16) = v;
-        }
-        __syncthreads();
-        float z[4][2];
-        score_tile<MINMAX>(s_q, s_lo, s_hi, 4 * warp, lane, z);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (c0 + lane + 32 * c < j1) scratch[(size_t)(4 * warp + r) * A.slots + c0 + lane + 32 * c] = z[r][c];
-        }
-      }
-      __syncthreads();
-    }
-    // a warp a row and head (of a group that selects together: a row)
-    const int lists = A.group ? tokens : rows;
-    for (int x = warp; x < lists; x += kSelThreads / 32) {
-      const int tok = A.group ? x : x / A.G, g = A.group ? 0 : x % A.G;
-      int c0, c1;
-      row_candidates(A, pos0 + tok, size, c0, c1);
-      const int n = c1 - c0, k = min(A.k[h0 + g], n), copies = A.group ? A.G : 1;
-      const size_t row = (size_t)(row0 + tok) * A.Hq + h0 + g;
-      int* list = A.sel_idx + row * A.kcap;
-      if (lane < copies) A.sel_cnt[row + lane] = k;
-      if (k == 0) continue;
-      if (k == n) {
-        for (int j = lane; j < n; j += 32)
-          for (int y = 0; y < copies; ++y) list[(size_t)y * A.kcap + j] = c0 + j;
-        continue;
-      }
-      const float* z = scratch + (size_t)(tok * A.G + g) * A.slots + c0;
-      auto key = [&](int j) -> uint32_t {
-        float v = z[j];
-        for (int y = 1; y < copies; ++y) v = __fadd_rn(v, z[(size_t)y * A.slots + j]);
-        return order_key(v);
-      };
-      // the largest key that at least k candidates reach
-      uint32_t top = 0;
-      int reach = n;
-      for (int bit = 31; bit >= 0 && reach != k; --bit) {
-        const uint32_t t = top | 1u << bit;
-        int m = 0;
-        for (int j = lane; j < n; j += 32) m += key(j) >= t;
-        m = __reduce_add_sync(0xffffffffu, m);
-        if (m >= k) {
-          top = t;
-          reach = m;
-        }
-      }
-      // those above it, and as many equal to it as there is room for (reach == k: all of them)
-      int above = 0;
-      if (reach != k) {
-        for (int j = lane; j < n; j += 32) above += key(j) > top;
-        above = __reduce_add_sync(0xffffffffu, above);
-      }
-      int ties = reach == k ? n : k - above, out = 0;
-      for (int j = lane; j - lane < n; j += 32) {
-        const uint32_t v = j < n ? key(j) : 0;
-        const bool more = j < n && v > top, even = j < n && v == top;
-        const unsigned tie = __ballot_sync(0xffffffffu, even), below = (1u << lane) - 1u;
-        const bool take = more || (even && __popc(tie & below) < ties);
-        ties -= min(ties, __popc(tie));
-        const unsigned m = __ballot_sync(0xffffffffu, take);
-        if (take)
-          for (int y = 0; y < copies; ++y) list[(size_t)y * A.kcap + out + __popc(m & below)] = c0 + j;
-        out += __popc(m);
-      }
+  for (int c0 = from; c0 < to; c0 += kSelBlocks) {
+    __syncthreads();
+#pragma unroll 4
+    for (int x = tid; x < kSelBlocks * kVecs; x += kSelThreads) {
+      const int d = x % (kD / 8), y = x / (kD / 8), c = MINMAX ? y >> 1 : y;
+      const bool low = MINMAX && (y & 1) == 0;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (c0 + c < to) v = __ldg(summ + (size_t)c0 * kVecs + x);
+      *reinterpret_cast<uint4*>((low ? s_lo : s_hi) + c * kRowStride + d * 16) = v;
     }
     __syncthreads();
+    float z[4][2];
+    score_tile<MINMAX>(s_q, s_lo, s_hi, 4 * warp, lane, z);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (c0 + lane + 32 * c < to) scratch[(size_t)(4 * warp + r) * A.slots + c0 + lane + 32 * c] = z[r][c];
+    }
   }
+}
+
+// A block a row and head (of a group that selects together: a row).
+template <int THREADS, int KEYS>
+__global__ void __launch_bounds__(THREADS) topk_rows_kernel(SelectArgs A, int u0) {
+  __shared__ TopkScratch S;
+  __shared__ ItemPlace s_place;
+  pdl_wait();
+  pdl_trigger();
+  SelectItem it;
+  if (!select_item<THREADS>(A, kSelRows / A.G, u0 + blockIdx.x, &s_place, it)) return;
+  const int tok = A.group ? blockIdx.y : blockIdx.y / A.G, g = A.group ? 0 : blockIdx.y % A.G;
+  if (tok >= it.tokens) return;
+  int c0, c1;
+  row_candidates(A, it.pos0 + tok, A.bs[it.kvh], c0, c1);
+  const int h = it.kvh * A.G + g;
+  const size_t row = (size_t)(it.row0 + tok) * A.Hq + h;
+  const float* z = A.scores + ((size_t)blockIdx.x * kSelRows + tok * A.G + g) * A.slots + c0;
+  int *list = A.sel_idx + row * A.kcap, *cnt = A.sel_cnt + row;
+  if (!A.group) {
+    group_topk<THREADS, KEYS>(z, c1 - c0, A.k[h], c0, list, cnt, 0, S);
+    return;
+  }
+  group_topk<THREADS, KEYS, true>(z, c1 - c0, A.k[h], c0, list, cnt, 0, S, A.G, (size_t)A.slots);
+  __syncthreads();
+  const int n = *cnt;
+  for (int y = 1; y < A.G; ++y) {
+    for (int i = threadIdx.x; i < n; i += THREADS) list[(size_t)y * A.kcap + i] = list[i];
+    if (threadIdx.x == 0) cnt[y] = n;
+  }
+}
+
+long long items_at_a_time(int slots, int n_items) {
+  const long long fit = (long long)(kScratchBytes / ((size_t)kSelRows * slots * sizeof(float)));
+  return std::max(1ll, std::min({fit, (long long)n_items, 65535ll}));
 }
 
 }  // namespace
 
-int select_rows_blocks(int num_sms) { return 2 * num_sms; }
-int select_rows_scratch_rows() { return kSelRows; }
+size_t score_rows_scratch(int slots, long long n_items) {
+  return (size_t)items_at_a_time(slots, (int)std::min(n_items, 1ll << 30)) * kSelRows * slots * sizeof(float);
+}
 
-int launch_select_rows(const SelectArgs& A, int num_sms, cudaStream_t stream) {
+int launch_score_rows(const SelectArgs& A, int max_candidates, cudaStream_t stream) {
   const int smem = (kSelRows + (A.minmax ? 2 : 1) * kSelBlocks) * kRowStride;
-  auto* kernel = A.minmax ? select_rows_kernel<true> : select_rows_kernel<false>;
-  if (smem_limit_at_least(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return SA_ERR_CUDA;
-  const int grid = A.n_items < select_rows_blocks(num_sms) ? A.n_items : select_rows_blocks(num_sms);
-  const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kSelThreads), (size_t)smem, stream, A);
-  return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+  auto* score = A.minmax ? score_rows_kernel<true> : score_rows_kernel<false>;
+  if (smem_limit_at_least(reinterpret_cast<const void*>(score), smem) != cudaSuccess) return SA_ERR_CUDA;
+  const int at_a_time = (int)items_at_a_time(A.slots, A.n_items), T = kSelRows / A.G;
+  const int stretches = std::max(1, (max_candidates + kSelStretch - 1) / kSelStretch);
+  for (int u0 = 0; u0 < A.n_items; u0 += at_a_time) {
+    const int n = std::min(at_a_time, A.n_items - u0);
+    cudaError_t e =
+        launch_pdl(score, dim3(n, stretches), dim3(kSelThreads), (size_t)smem, stream, A, u0);
+    if (e != cudaSuccess) return SA_ERR_CUDA;
+    const dim3 lists(n, A.group ? T : T * A.G);
+    // the smallest block that holds every candidate
+    if (max_candidates <= 128 * 8)
+      e = launch_pdl(topk_rows_kernel<128, 8>, lists, dim3(128), 0, stream, A, u0);
+    else if (max_candidates <= 256 * 16)
+      e = launch_pdl(topk_rows_kernel<256, 16>, lists, dim3(256), 0, stream, A, u0);
+    else if (max_candidates <= 1024 * 16)
+      e = launch_pdl(topk_rows_kernel<1024, 16>, lists, dim3(1024), 0, stream, A, u0);
+    else
+      e = launch_pdl(topk_rows_kernel<1024, 64>, lists, dim3(1024), 0, stream, A, u0);
+    if (e != cudaSuccess) return SA_ERR_CUDA;
+  }
+  return SA_OK;
 }
 
 }  // namespace sa

@@ -164,9 +164,87 @@ def test_behind_the_table():
     _check(r, prob, _summaries(prob, 12), status=sa.SA_ERR_CAPACITY)
 
 
+# many rows a sequence: scores of the tensor cores first, canonical ones where they are close
+
+@pytest.mark.parametrize("mode", [sa.SUMMARY_MINMAX, sa.SUMMARY_MEAN])
+@pytest.mark.parametrize("group", [False, True])
+@pytest.mark.parametrize("Hq,Hk", HEADS)
+def test_many_rows(Hq, Hk, mode, group):
+    r = _rows([260, 1, 0, 140], [900, 3000, 20, 5000], Hq, Hk, seed=Hq + 50)
+    bs = [(16, 8, 64, 32)[h % 4] for h in range(Hk)]
+    k = [5] * Hq if group else [(h * 3) % 23 for h in range(Hq)]
+    prob = Z.problem(r, bs, k, 4, 64, mode=mode, selection=sa.SELECT_GROUP if group else sa.SELECT_PER_HEAD)
+    _check(r, prob, _summaries(prob, Hq + 1))
+
+
+@pytest.mark.parametrize("kind", ["coarse", "equal"])
+@pytest.mark.parametrize("mode", [sa.SUMMARY_MINMAX, sa.SUMMARY_MEAN])
+@pytest.mark.parametrize("group", [False, True])
+def test_many_rows_with_ties(kind, mode, group):
+    r = _rows([100], [3000], 8, 2, seed=33)
+    if kind == "coarse":
+        r.q.sign_()
+    prob = Z.problem(r, [8, 16], 37, 4, 64, mode=mode, selection=sa.SELECT_GROUP if group else sa.SELECT_PER_HEAD)
+    _check(r, prob, _summaries(prob, 3, kind))
+
+
+@pytest.mark.parametrize("k", [0, 1, 2, 31, 63, 100, 118, 119, 1000])
+def test_many_rows_budgets(k):
+    r = _rows([90], [1950], 4, 2, seed=k + 1)
+    prob = Z.problem(r, 16, k, 4, 64)
+    _check(r, prob, _summaries(prob, 5))
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -7, 2.0 ** -8, 0.0])
+def test_many_rows_with_close_scores(eps):
+    # neighbouring blocks differ by at most one step of bf16 in one dim, or not at all
+    r = _rows([130], [4000], 8, 2, seed=38)
+    prob = Z.problem(r, 16, 20, 4, 64, mode=sa.SUMMARY_MEAN)
+    summ = _summaries(prob, 8)
+    summ[:, :, 1::2] = summ[:, :, :-1:2] if summ.shape[2] % 2 == 0 else summ[:, :, :-1:2][:, :, :summ[:, :, 1::2].shape[2]]
+    g = torch.Generator().manual_seed(1)
+    for j in range(1, summ.shape[2], 2):
+        summ[:, :, j, int(torch.randint(0, 128, (1,), generator=g))] *= 1 + eps
+    _check(r, prob, summ)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1e12, 1e30])
+def test_many_rows_of_other_sizes(size):
+    r = _rows([70], [2500], 8, 2, seed=39)
+    prob = Z.problem(r, [8, 16], 13, 4, 64)
+    summ = _summaries(prob, 9)
+    r.q *= size
+    _check(r, prob, summ)
+
+
+def test_many_rows_with_infinities():
+    # no bound for a KV head with an infinite summary, or for a row with an infinite query: these are scored as a whole
+    r = _rows([70], [2500], 8, 2, seed=40)
+    prob = Z.problem(r, [8, 16], 13, 4, 64)
+    summ = _summaries(prob, 10)
+    r.q.abs_().clamp_(min=0.125)
+    summ[0, 1, 77, 1, 5] = float("inf")
+    r.q[9, 2, 3] = float("inf")
+    summ[0, 0, :, 1, 3] = summ[0, 0, :, 1, 3].abs().clamp(min=0.125)      # infinity times it is infinity: all are equal
+    _check(r, prob, summ)
+
+
+def test_many_candidates():
+    r = _rows([70, 64], [30000, 12000], 8, 2, seed=41)
+    prob = Z.problem(r, [16, 32], 100, 4, 512)
+    _check(r, prob, _summaries(prob, 11))
+    r = _rows([64], [16500], 8, 1, seed=42)
+    prob = Z.problem(r, [8], 300, 0, 64, mode=sa.SUMMARY_MEAN)
+    _check(r, prob, _summaries(prob, 12))
+
+
 def test_many_sequences_and_replay():
-    rows = [(i * 5) % 4 for i in range(300)]
-    r = _rows(rows, [200 + (i * 37) % 900 for i in range(300)], 4, 2, seed=13)
+    _many([(i * 5) % 4 for i in range(300)])
+    _many([(i * 5) % 4 + (80 if i < 3 else 0) for i in range(5)])
+
+
+def _many(rows):
+    r = _rows(rows, [200 + (i * 37) % 900 for i in range(len(rows))], 4, 2, seed=13)
     prob = Z.problem(r, [16, 32], 6, 4, 64)
     summ = _summaries(prob, 13)
     idx, cnt = _check(r, prob, summ)
