@@ -3,31 +3,34 @@
 //
 // The canonical fp32 order of a score is no order that a matrix instruction
 // has, so what the tensor cores give is taken as a value a with
-//   |a - s| <= E = 2^-14 |q| max_j |k_j|      (norms of q and of max(|min|, |max|))
-// of the canonical s.  A matrix product of 256 terms in steps of 16 adds, a
-// step, 17 numbers cut to 24 bits of the largest (2^-23 of it each at most);
-// none is above sum |q k| <= |q| |k|, so 16 steps are off by at most
-// 16 * 17 * 2^-23 |q| |k| < 2^-14.9 |q| |k|, and the canonical sum by less than
-// 2^-19.  A candidate that is more than 2 E above the best one left out is
+//   |a - s| <= E = 2^-15 |q| max_j |k_j|      (norms of q and of max(|min|, |max|))
+// of the canonical s.  A matrix instruction adds 16 products and the sum so far,
+// each cut to 24 bits of the largest of them (off by 2^-23 of it at most, the
+// products of zeros not at all); none is above sum |q k| <= |q| |k|.  128
+// products and at most 16 sums are off by 144 * 2^-23 |q| |k| < 2^-15.8 |q| |k|,
+// the canonical sum by less than 2^-19.  A candidate that is more than 2 E above the best one left out is
 // selected whatever the order; one that is more than 2 E below the worst one
-// taken is not; those between (in one row out of six or so) are scored again in
+// taken is not; those between (in one row out of seven or so) are scored again in
 // the canonical order, and the best of them, lowest index first among equals,
 // fill the list.  So lists are the canonical ones, entry for entry.  A row with
 // more close ones than kClose, or without a bound (infinities), is scored
 // again as a whole.
 //
 // q . min/max summary: sum over d of q+_d kmax_d + q-_d kmin_d with q+ and q-
-// the positive and negative part, a product of twice the length.
+// the positive and negative part, a product of twice the length, half of it zeros.
 // Heads that select together: a row is a token and the product runs over the
 // group's heads too; E is G times that of the sum of their norms.
 //
 // A block (four warps, two blocks an SM) takes an item: one KV head with 128
 // rows (tokens and heads; tokens, for heads that select together) of a sequence, a thread a row.  Scores stay in
 // TMEM (up to 256 candidates; more go through a scratch, [candidate][row]).
-// The k-th score is found by counting against a threshold that starts where a
-// normal distribution has it and follows its density (three to five passes).
-// Bound by the passes' instructions: about 20 a candidate and row.
-#include <cfloat>
+// A threshold that starts where a normal distribution has it and follows its
+// density until a few more than k reach it (two to four passes that count)
+// leaves a short list of each row, in the shared memory of the operands; the
+// k-th is found there by a sorting network.
+#include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "rows_select.cuh"
 #include "tcgen.cuh"
@@ -38,9 +41,13 @@ namespace {
 constexpr int kThreads = 128, kRows = 128, kCols = 256, kTile = 64;
 constexpr int kHalfTile = kRows * 64 * 2, kSummHalf = kTile * 64 * 2;     // 64 dims of q's rows, of a tile of summaries
 constexpr int kClose = 8;                                                   // of a row, scored again one by one
+// A row's short list: the candidates above a threshold, at least k of them and
+// kShort at most, where k is at most kShortK; it lies where the operands were.
+constexpr int kShort = 64, kShortRoom = kShort + 32, kShortK = 40;
+constexpr size_t kShortBytes = (size_t)kRows * kShortRoom * sizeof(float2);     // (score, candidate)
 
 template <bool MINMAX>
-constexpr size_t kOperands = (MINMAX ? 2 : 1) * (2 * kHalfTile + 2 * kSummHalf);
+constexpr size_t kOperands = std::max<size_t>((MINMAX ? 2 : 1) * (2 * kHalfTile + 2 * kSummHalf), kShortBytes);
 
 struct Warp {
   uint16_t close[32][kClose];
@@ -97,17 +104,6 @@ __global__ void __launch_bounds__(256) summary_norms_kernel(SelectArgs A) {
   if (lane == 0) atomicMax(A.norms + unit, __float_as_int(most));     // not negative: ordered like its bits
 }
 
-// 32 scores of a row from column 32 c on.
-template <bool MEMORY>
-__device__ __forceinline__ void load32(uint32_t tmem, const float* scratch, int c, float (&v)[32]) {
-  if (MEMORY) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = scratch[(size_t)(32 * c + i) * kRows];
-  } else {
-    tmem_ld32(tmem + 32 * c, v);
-  }
-}
-
 // A row's list.  Everything is converged by warp; lanes without work pass along.
 struct RowTask {
   bool valid;            // has candidates to choose from: 0 < k < n
@@ -127,67 +123,220 @@ __device__ __forceinline__ float row_score(const SelectArgs& A, const __nv_bfloa
   return v;
 }
 
-template <bool MINMAX, bool MEMORY>
-__device__ void select_list(const SelectArgs& A, const RowTask& t, uint32_t tmem, const float* scratch, float* keys,
-                            Warp* w) {
+// Where a normal distribution has the share p of its values above.  (Hastings'
+// approximation of the quantile: Abramowitz and Stegun 26.2.22.)
+__device__ __forceinline__ float upper_quantile(float p) {
+  const float tail = sqrtf(-2.f * logf(fminf(p, 1.f - p)));
+  const float z = tail - (2.30753f + 0.27061f * tail) / (1.f + tail * (0.99229f + 0.04481f * tail));
+  return p < 0.5f ? z : -z;
+}
+
+// The close candidates of a warp's rows, n_close of each in w->close, scored in
+// the canonical order; a bit for each of the `need` best of the lane's row.
+template <bool MINMAX>
+__device__ __forceinline__ unsigned choose_close(const SelectArgs& A, const RowTask& t, int n_close, int need, Warp* w) {
   constexpr int kSummary = (MINMAX ? 2 : 1) * kD;
+  const int lane = threadIdx.x & 31, part = lane & 7;
+  const int upto = warp_incl_scan(n_close), total = __shfl_sync(0xffffffffu, upto, 31), first = upto - n_close;
+  for (int i = 0; i < n_close; ++i) w->task[first + i] = (uint16_t)(lane * kClose + i);
+  __syncwarp();
+  for (int x0 = 0; x0 < total; x0 += 4) {
+    const int x = min(x0 + (lane >> 3), total - 1), task = w->task[x], who = task / kClose;
+    const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)t.q, who);
+    const size_t summ = __shfl_sync(0xffffffffu, (unsigned long long)t.summ, who);
+    const float z = row_score<MINMAX>(A, reinterpret_cast<const __nv_bfloat16*>(row),
+                                      reinterpret_cast<const __nv_bfloat16*>(summ) +
+                                          (size_t)w->close[who][task % kClose] * kSummary, part);
+    if (part == 0) w->score[x] = z;
+  }
+  __syncwarp();
+  unsigned chosen = 0;
+  for (int i = 0; i < n_close; ++i) {
+    const float z = w->score[first + i];
+    int rank = 0;
+    for (int j = 0; j < n_close; ++j) {
+      const float o = w->score[first + j];
+      rank += o > z || (o == z && j < i);
+    }
+    if (rank < need) chosen |= 1u << i;
+  }
+  __syncwarp();
+  return chosen;
+}
+
+// Rows (a bit a lane) that are scored again as a whole, a warp a row.
+template <bool MINMAX>
+__device__ __noinline__ void select_whole(const SelectArgs& A, const RowTask& t, unsigned rows, float* keys) {
+  constexpr int kSummary = (MINMAX ? 2 : 1) * kD;
+  const int lane = threadIdx.x & 31, part = lane & 7;
+  for (; rows != 0; rows &= rows - 1) {
+    const int src = __ffs(rows) - 1, n = __shfl_sync(0xffffffffu, t.n, src), k = __shfl_sync(0xffffffffu, t.k, src);
+    const auto* q = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, (unsigned long long)t.q, src));
+    const auto* s = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, (unsigned long long)t.summ, src));
+    const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)t.row, src);
+    const int base = __shfl_sync(0xffffffffu, t.base, src);
+    for (int j0 = 0; j0 < n; j0 += 4) {
+      const int j = min(j0 + (lane >> 3), n - 1);
+      const float z = row_score<MINMAX>(A, q, s + (size_t)j * kSummary, part);
+      if (part == 0) keys[j] = z;
+    }
+    __syncwarp();
+    warp_topk([&](int j) { return order_key(keys[j]); }, n, k, base, A.sel_idx + row * A.kcap, A.group ? A.G : 1, A.kcap);
+    __syncwarp();
+  }
+}
+
+// A row's candidates' approximate scores, kStep at a time; those behind the
+// row's last are -infinity.
+constexpr int kStep = 32;
+template <bool MEMORY>
+struct Scores {
+  uint32_t tmem;
+  const float* scratch;
+  int n;
+  __device__ __forceinline__ void load(int c, float (&v)[kStep]) const {
+    if (MEMORY) {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) v[i] = scratch[(size_t)(kStep * c + i) * kRows];
+    } else {
+      tmem_ld32(tmem + kStep * c, v);
+    }
+    if (__any_sync(0xffffffffu, kStep * c + kStep > n)) {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) v[i] = kStep * c + i < n ? v[i] : -INFINITY;
+    }
+  }
+  // f(first column, kStep scores) for every chunk, in order
+  template <typename F>
+  __device__ __forceinline__ void each(int chunks, F f) const {
+    for (int c = 0; c < chunks; ++c) {
+      float v[kStep];
+      load(c, v);
+      f(kStep * c, v);
+    }
+  }
+  __device__ __forceinline__ int count(int chunks, float at) const {
+    int a = 0, b = 0;
+    for (int c = 0; c < chunks; ++c) {
+      float v[kStep];
+      load(c, v);
+#pragma unroll
+      for (int i = 0; i < kStep; i += 2) {
+        a += v[i] >= at;
+        b += v[i + 1] >= at;
+      }
+    }
+    return a + b;
+  }
+};
+
+// How many of a row's scores reach a threshold.  In TMEM a look at all of them
+// is a load's round trip every 32 columns (200 cycles for 16 scores), so up to
+// 256 are kept in registers, as pairs of fp16 in units of their spread about
+// their mean: counts that are off by what lies within 2^-9 of the threshold
+// change the length of a list, not what is selected.
+template <bool MEMORY>
+struct Counter {
+  const Scores<MEMORY>& S;
+  int chunks;
+  float mean, sigma;
+  __device__ __forceinline__ Counter(const Scores<MEMORY>& s, int c, float m, float d) : S(s), chunks(c), mean(m), sigma(d) {}
+  __device__ __forceinline__ int count(float at) const { return S.count(chunks, at); }
+};
+template <>
+struct Counter<false> {
+  __half2 h[kCols / 2];
+  float mean, inv;
+  __device__ __forceinline__ Counter(const Scores<false>& S, int chunks, float m, float sigma)
+      : mean(m), inv(fminf(1.f / sigma, 1e30f)) {
+#pragma unroll
+    for (int c = 0; c < kCols / kStep; ++c) {
+      if (c < chunks) {
+        float v[kStep];
+        S.load(c, v);
+#pragma unroll
+        for (int i = 0; i < kStep / 2; ++i)
+          h[c * (kStep / 2) + i] = __floats2half2_rn((v[2 * i] - mean) * inv, (v[2 * i + 1] - mean) * inv);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kStep / 2; ++i) h[c * (kStep / 2) + i] = __floats2half2_rn(-INFINITY, -INFINITY);
+      }
+    }
+  }
+  __device__ __forceinline__ int count(float at) const {
+    const __half2 t = __float2half2_rn((at - mean) * inv);
+    __half2 sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = __float2half2_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) sum[i & 3] = __hadd2(sum[i & 3], __hge2(h[i], t));
+    const __half2 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+    return (int)(__low2float(all) + __high2float(all));
+  }
+};
+
+// N values in descending order (Batcher's odd-even merge sort): no branches, and
+// comparators that do not wait for one another.  A step compares values K apart
+// inside runs of 2 P.
+template <int N, int P, int K>
+__device__ __forceinline__ void sort_steps(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N - K; ++i) {
+    if (i >= K % P && (i - K % P) % (2 * K) < K && i / (2 * P) == (i + K) / (2 * P)) {
+      const float a = v[i], b = v[i + K];
+      v[i] = fmaxf(a, b);
+      v[i + K] = fminf(a, b);
+    }
+  }
+  if constexpr (K > 1) sort_steps<N, P, K / 2>(v);
+  else if constexpr (2 * P < N) sort_steps<N, 2 * P, 2 * P>(v);
+}
+
+// The k-th and the next largest of a short list of at most N (-infinity where it has no such).
+template <int N>
+__device__ __forceinline__ void kth_of_list(const float2* list, int len, int k, float& kth, float& next) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = i < len ? list[i * kRows].x : -INFINITY;
+  sort_steps<N, 1, 1>(v);
+  kth = next = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i == k - 1) kth = v[i];
+    if (i == k) next = v[i];
+  }
+}
+
+// The next threshold of a search for `want` values at or above it, where there
+// are cnt at or above `at`: along the normal distribution's density, or the
+// middle of what is left.
+__device__ __forceinline__ float next_threshold(float at, int cnt, int want, int n, float mean, float sigma, float lo,
+                                                float hi, bool halve) {
+  const float z = (at - mean) / sigma, density = n * 0.3989f * __expf(-0.5f * z * z) / sigma;
+  const float next = at + (cnt - want) / fmaxf(density, 1e-6f / sigma);
+  return halve || !(next > lo && next < hi) ? 0.5f * (lo + hi) : next;
+}
+
+// Rows with many to keep: the k-th is looked for among all candidates.
+template <bool MINMAX, bool MEMORY>
+__device__ __noinline__ unsigned select_long(const SelectArgs& A, const RowTask& t, const Scores<MEMORY>& S, int chunks,
+                                             bool active, float mean, float sigma, float bound, Warp* w) {
   const int lane = threadIdx.x & 31;
-  int most = t.valid ? t.n : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (most == 0) return;
-  const int chunks = (most + 31) / 32, n = t.valid ? t.n : 0;
-  float v[32];
-  auto load = [&](int c) {      // columns behind the row's last are -infinity
-    load32<MEMORY>(tmem, scratch, c, v);
-    if (__any_sync(0xffffffffu, 32 * c + 32 > n)) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 32 * c + i < n ? v[i] : -INFINITY;
-    }
-  };
-  // range, mean and spread
-  float lo = INFINITY, hi = -INFINITY, sum = 0.f, sq = 0.f;
-  for (int c = 0; c < chunks; ++c) {
-    load(c);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float x = v[i] == -INFINITY ? 0.f : v[i];
-      sum += x;
-      sq = fmaf(x, x, sq);
-      hi = fmaxf(hi, v[i]);
-      lo = fminf(lo, v[i] == -INFINITY ? INFINITY : v[i]);
-    }
-  }
-  bool whole = t.valid && !(t.E < 1e30f && hi < 1e30f && lo > -1e30f);   // no bound: scored again as a whole
-  bool active = t.valid && !whole;
-  const float mean = sum / n, sigma = sqrtf(fmaxf(sq / n - mean * mean, 1e-30f));
-  hi += fmaxf(t.E, fabsf(hi) * 1e-6f) + 1e-30f;       // none reaches it
-  // where a normal distribution has the k-th (Hastings' approximation of its quantile)
-  float at;
-  {
-    const float p = (float)t.k / n, tail = sqrtf(-2.f * logf(fminf(p, 1.f - p)));
-    const float z = tail - (2.30753f + 0.27061f * tail) / (1.f + tail * (0.99229f + 0.04481f * tail));
-    at = mean + sigma * (p < 0.5f ? z : -z);
-    if (!(at > lo && at < hi)) at = 0.5f * (lo + hi);
-  }
+  float lo = -bound, hi = bound;
+  bool whole = false;
+  float at = mean + sigma * upper_quantile((float)t.k / t.n);
+  if (!(at > lo && at < hi)) at = 0.f;
   // count(>= lo) >= k > count(>= hi)
   bool found = false, search = active;
-  for (int step = 0; step < 40 && __any_sync(0xffffffffu, search); ++step) {
-    int cnt = 0;
-    for (int c = 0; c < chunks; ++c) {
-      load(c);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) cnt += v[i] >= at;
-    }
+  for (int step = 0; step < 60 && __any_sync(0xffffffffu, search); ++step) {
+    const int cnt = S.count(chunks, at);
     if (search) {
       if (cnt == t.k) {
         found = true;
         search = false;
       } else {
         if (cnt > t.k) lo = at; else hi = at;
-        const float z = (at - mean) / sigma, density = n * 0.3989f * __expf(-0.5f * z * z) / sigma;
-        float next = at + (cnt - t.k) / fmaxf(density, 1e-6f / sigma);
-        if (step % 3 == 2 || !(next > lo && next < hi)) next = 0.5f * (lo + hi);
+        const float next = next_threshold(at, cnt, t.k, t.n, mean, sigma, lo, hi, step % 3 == 2);
         search = hi - lo > t.E && next > lo && next < hi;
         at = next;
       }
@@ -197,15 +346,14 @@ __device__ void select_list(const SelectArgs& A, const RowTask& t, uint32_t tmem
   float sure = hi + 2.f * t.E, close_lo = lo - 2.f * t.E;
   if (__any_sync(0xffffffffu, found)) {
     float least = INFINITY, best = -INFINITY;          // of those taken, of those left
-    for (int c = 0; c < chunks; ++c) {
-      load(c);
+    S.each(chunks, [&](int, const float (&v)[kStep]) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kStep; ++i) {
         const bool in = v[i] >= at;
         least = fminf(least, in ? v[i] : INFINITY);
         best = fmaxf(best, in ? -INFINITY : v[i]);
       }
-    }
+    });
     if (found) {
       const bool apart = least - best > 2.f * t.E;
       sure = apart ? best : best + 2.f * t.E;
@@ -216,45 +364,21 @@ __device__ void select_list(const SelectArgs& A, const RowTask& t, uint32_t tmem
   bool some = active && close_lo < INFINITY;
   if (__any_sync(0xffffffffu, some)) {
     int taken = 0, n_close = 0;
-    for (int c = 0; c < chunks; ++c) {
-      load(c);
+    S.each(chunks, [&](int first, const float (&v)[kStep]) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kStep; ++i) {
         taken += v[i] > sure;
         if (some && v[i] <= sure && v[i] >= close_lo) {
-          if (n_close < kClose) w->close[lane][n_close] = (uint16_t)(32 * c + i);
+          if (n_close < kClose) w->close[lane][n_close] = (uint16_t)(first + i);
           ++n_close;
         }
       }
-    }
+    });
     if (some && n_close > kClose) {
       whole = true;
       some = active = false;
     }
-    if (!some) n_close = 0;
-    const int upto = warp_incl_scan(n_close), total = __shfl_sync(0xffffffffu, upto, 31), first = upto - n_close;
-    for (int i = 0; i < n_close; ++i) w->task[first + i] = (uint16_t)(lane * kClose + i);
-    __syncwarp();
-    const int part = lane & 7;
-    for (int x0 = 0; x0 < total; x0 += 4) {
-      const int x = min(x0 + (lane >> 3), total - 1), task = w->task[x], who = task / kClose;
-      const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)t.q, who);
-      const size_t summ = __shfl_sync(0xffffffffu, (unsigned long long)t.summ, who);
-      const float z = row_score<MINMAX>(A, reinterpret_cast<const __nv_bfloat16*>(row),
-                                        reinterpret_cast<const __nv_bfloat16*>(summ) +
-                                            (size_t)w->close[who][task % kClose] * kSummary, part);
-      if (part == 0) w->score[x] = z;
-    }
-    __syncwarp();
-    for (int i = 0; i < n_close; ++i) {
-      const float z = w->score[first + i];
-      int rank = 0;
-      for (int j = 0; j < n_close; ++j) {
-        const float o = w->score[first + j];
-        rank += o > z || (o == z && j < i);
-      }
-      if (rank < t.k - taken) chosen |= 1u << i;
-    }
+    chosen = choose_close<MINMAX>(A, t, some ? n_close : 0, t.k - taken, w);
   }
   // the list, ascending
   const int copies = A.group ? A.G : 1;
@@ -262,38 +386,177 @@ __device__ void select_list(const SelectArgs& A, const RowTask& t, uint32_t tmem
     int* list = A.sel_idx + t.row * A.kcap;
     int out = 0;
     unsigned left = chosen;
-    for (int c = 0; c < chunks; ++c) {
-      load(c);
+    S.each(chunks, [&](int first, const float (&v)[kStep]) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kStep; ++i) {
         bool take = active && v[i] > sure;
         if (active && v[i] <= sure && v[i] >= close_lo) {
           take = left & 1u;
           left >>= 1;
         }
         if (take && out < t.k) {
-          for (int y = 0; y < copies; ++y) list[(size_t)y * A.kcap + out] = t.base + 32 * c + i;
+          for (int y = 0; y < copies; ++y) list[(size_t)y * A.kcap + out] = t.base + first + i;
           ++out;
+        }
+      }
+    });
+  }
+  return __ballot_sync(0xffffffffu, whole);
+}
+
+// A row's list, a thread a row.  mine: the lane's own column of the short lists.
+template <bool MINMAX, bool MEMORY>
+__device__ __forceinline__ void select_list(const SelectArgs& A, const RowTask& t, const Scores<MEMORY>& S, float* keys,
+                                            Warp* w, float2* mine) {
+  const int lane = threadIdx.x & 31;
+  const int most = __reduce_max_sync(0xffffffffu, t.valid ? t.n : 0);
+  if (most == 0) return;
+  const int chunks = (most + kStep - 1) / kStep;
+  bool whole = t.valid && !(t.E < 1e30f);        // no bound
+  bool active = t.valid && !whole;
+  const float bound = t.E * 33000.f;             // |score| < |q| |k| + E
+  // mean and spread of at most 128 of them
+  float mean, sigma;
+  {
+    const int full = max(1, __reduce_min_sync(0xffffffffu, t.valid ? t.n : most) / kStep), step = (full + 3) / 4;
+    float sum = 0.f, sq = 0.f;
+    int cnt = 0;
+    for (int c = 0; c < full; c += step) {
+      float v[kStep];
+      S.load(c, v);
+      const int here = min(kStep, t.n - kStep * c);    // fewer where the row has no more
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const float x = i < here ? v[i] : 0.f;
+        sum += x;
+        sq = fmaf(x, x, sq);
+      }
+      cnt += here;
+    }
+    mean = active ? sum / cnt : 0.f;
+    sigma = active ? sqrtf(fmaxf(sq / cnt - mean * mean, 1e-30f)) : 1.f;
+  }
+  if (__any_sync(0xffffffffu, active && t.k > kShortK)) {
+    unsigned again = select_long<MINMAX, MEMORY>(A, t, S, chunks, active, mean, sigma, bound, w);
+    again |= __ballot_sync(0xffffffffu, whole);
+    if (again != 0) select_whole<MINMAX>(A, t, again, keys);
+    return;
+  }
+  // a threshold that a few more than k reach: enough to be sure, as a rule, that
+  // all that are close to the k-th are among them
+  float lo = -bound, hi = bound;
+  const int few = min(t.k + 2, t.n), many = t.k + 16;
+  float at = t.n <= many ? lo : mean + sigma * upper_quantile((t.k + 8.f) / t.n);
+  if (!(at >= lo && at < hi)) at = lo;
+  int tries = 0;
+  bool search = active && t.n > many;
+  if (__any_sync(0xffffffffu, search)) {
+  const Counter<MEMORY> C(S, chunks, mean, sigma);
+  while (__any_sync(0xffffffffu, search)) {
+    const int cnt = C.count(at);
+    if (search) {
+      if (cnt >= few && cnt <= many) {
+        search = false;
+      } else {
+        if (cnt > many) lo = at; else hi = at;
+        const float next = next_threshold(at, cnt, t.k + 8, t.n, mean, sigma, lo, hi, tries % 3 == 2);
+        if (++tries < 30 && next > lo && next < hi) {
+          at = next;
+        } else {           // many equal or close ones: all of them, if the list holds them
+          at = lo;
+          search = false;
         }
       }
     }
   }
-  // rows that are scored again as a whole, a warp a row
-  for (unsigned m = __ballot_sync(0xffffffffu, whole); m != 0; m &= m - 1) {
-    const int src = __ffs(m) - 1, nn = __shfl_sync(0xffffffffu, t.n, src), kk = __shfl_sync(0xffffffffu, t.k, src);
-    const auto* q = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, (unsigned long long)t.q, src));
-    const auto* s = reinterpret_cast<const __nv_bfloat16*>(__shfl_sync(0xffffffffu, (unsigned long long)t.summ, src));
-    const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)t.row, src);
-    const int base = __shfl_sync(0xffffffffu, t.base, src), part = lane & 7;
-    for (int j0 = 0; j0 < nn; j0 += 4) {
-      const int j = min(j0 + (lane >> 3), nn - 1);
-      const float z = row_score<MINMAX>(A, q, s + (size_t)j * kSummary, part);
-      if (part == 0) keys[j] = z;
+  }
+  // the short list: everything at or above it
+  int len = 0;
+  float sure = INFINITY, close_lo = INFINITY;    // taken above; close from close_lo to sure
+  search = active;
+  for (int round = 0; __any_sync(0xffffffffu, search); ++round) {
+    __syncwarp();
+    const float from = search ? at : INFINITY;
+    int got = 0;
+    S.each(chunks, [&](int first, const float (&v)[kStep]) {
+      // one that is too long already is only counted
+      const uint32_t begin = smem_u32(mine + min(got, kShort) * kRows);
+      uint32_t place = begin;
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %2;\n\t"
+            "@p st.shared.v2.b32 [%0], {%3, %4};\n\t@p add.u32 %0, %0, %5;\n\t}"
+            : "+r"(place)
+            : "f"(v[i]), "f"(from), "r"(__float_as_int(v[i])), "r"(first + i), "n"(kRows * 8)
+            : "memory");
+      got += (place - begin) / (kRows * 8);
+    });
+    if (search) len = got;
+    if (search && got > kShort) {
+      whole = true;
+      search = false;
+    }
+    const int longest = __reduce_max_sync(0xffffffffu, search ? got : 0);
+    float least, best;                           // of those taken; of those left
+    if (longest <= 32) kth_of_list<32>(mine, search ? len : 0, t.k, least, best);
+    else kth_of_list<64>(mine, search ? len : 0, t.k, least, best);
+    if (search) {
+      if (len < t.n) best = fmaxf(best, at);     // not above: what the list does not hold
+      const bool apart = least - best > 2.f * t.E;
+      sure = apart ? best : best + 2.f * t.E;
+      close_lo = apart ? INFINITY : least - 2.f * t.E;
+      search = close_lo < at && len < t.n;       // some that are close may be missing: once more, from there
+      whole = search && round > 0;
+      search = search && round == 0;
+      at = close_lo;
+    }
+  }
+  active = active && !whole;
+  bool some = active && close_lo < INFINITY;
+  if (__any_sync(0xffffffffu, some)) {
+    int taken = 0, n_close = 0;
+    uint64_t at_place = 0;      // of the close ones, eight bits each
+    if (some) {
+      for (int i = 0; i < len; ++i) {
+        const float2 x = mine[i * kRows];
+        taken += x.x > sure;
+        if (x.x <= sure && x.x >= close_lo) {
+          if (n_close < kClose) {
+            w->close[lane][n_close] = (uint16_t)__float_as_int(x.y);
+            at_place |= (uint64_t)i << (8 * n_close);
+          }
+          ++n_close;
+        }
+      }
+      if (n_close > kClose) {
+        whole = true;
+        some = active = false;
+        n_close = 0;
+      }
     }
     __syncwarp();
-    warp_topk([&](int j) { return order_key(keys[j]); }, nn, kk, base, A.sel_idx + row * A.kcap, copies, A.kcap);
-    __syncwarp();
+    const unsigned chosen = choose_close<MINMAX>(A, t, n_close, t.k - taken, w);
+    for (int i = 0; i < n_close; ++i)
+      mine[((at_place >> (8 * i)) & 255) * kRows].x = (chosen >> i) & 1u ? INFINITY : -INFINITY;
   }
+  if (active) {       // the list, ascending
+    const int copies = A.group ? A.G : 1;
+    int* list = A.sel_idx + t.row * A.kcap;
+    int out = 0;
+#pragma unroll 4
+    for (int i = 0; i < len; ++i) {
+      const float2 x = mine[i * kRows];
+      if (x.x > sure && out < t.k) {
+        const int j = t.base + __float_as_int(x.y);
+        list[out] = j;
+        for (int y = 1; y < copies; ++y) list[(size_t)y * A.kcap + out] = j;
+        ++out;
+      }
+    }
+  }
+  const unsigned rows = __ballot_sync(0xffffffffu, whole);
+  if (rows != 0) select_whole<MINMAX>(A, t, rows, keys);
 }
 
 template <bool MINMAX>
@@ -428,11 +691,11 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
       if (!ok) break;
       tc_fence_after();
       if (memory) {
-        for (int x = 0; x < cols; x += 32) {
-          float v[32];
+        for (int x = 0; x < cols; x += kStep) {
+          float v[kStep];
           tmem_ld32(mine + x, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < kStep; ++i)
             if (w0 + x + i < n_item) scratch[(size_t)(w0 + x + i) * kRows + tid] = v[i];
         }
         tc_fence_before();
@@ -442,9 +705,12 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
     }
     if (!ok) break;
     const float k2 = __int_as_float(__ldg(A.norms + it.b * A.Hk + it.kvh));
-    t.E = 6.103515625e-5f * heads * norm * sqrtf(k2) * 1.001f + 1e-35f;
-    if (memory) select_list<MINMAX, true>(A, t, mine, scratch + tid, keys, &c->warp[warp]);
-    else select_list<MINMAX, false>(A, t, mine, scratch + tid, keys, &c->warp[warp]);
+    t.E = 3.0517578125e-5f * heads * norm * sqrtf(k2) * 1.001f + 1e-35f;
+    float2* list = reinterpret_cast<float2*>(smem) + tid;      // the operands are done with
+    const int n = t.valid ? t.n : 0;
+    if (memory) select_list<MINMAX, true>(A, t, Scores<true>{mine, scratch + tid, n}, keys, &c->warp[warp], list);
+    else select_list<MINMAX, false>(A, t, Scores<false>{mine, scratch + tid, n}, keys, &c->warp[warp], list);
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
