@@ -182,10 +182,10 @@ struct SelectArgs {
 int launch_score_rows(const SelectArgs& A, int max_candidates, cudaStream_t stream);
 size_t score_rows_scratch(int slots, long long n_items);
 // rows_select_tc.cu: many rows
-constexpr int kTcMaxSlots = 2048;
+constexpr int kTcMaxSlots = 4096;
 int launch_select_tc(const SelectArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmS, int num_sms,
                      cudaStream_t stream);
-size_t select_tc_scratch(int slots);
+size_t select_tc_scratch(int slots, long long n_items);
 
 // ---------------------------------------------------------------- rotation
 

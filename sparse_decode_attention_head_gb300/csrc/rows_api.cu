@@ -107,10 +107,20 @@ SparseLayout sparse_layout(const Params& p, int n_rows) {
 
 // The selection's scratch behind the norms.
 constexpr int kSelectMaxSlots = 1024 * 64;      // candidates that a block's top-k holds
-bool select_by_tensor(const Params& p, int n_rows) {
-  // many rows a sequence: the tensor cores' scores; few: the summaries' bytes
-  // bound both, and scores that are canonical need no second look
-  return p.slots <= sa::kTcMaxSlots && (long long)p.B * p.Hk * p.slots < (1ll << 31) && n_rows >= 64ll * p.B;
+// Which form takes less, from what each measured (32 heads over 8): the tensor
+// cores' one a round of two items an SM, 15 us and 0.16 us a candidate block
+// (seven times that where lists are long: their k-th is looked for among all);
+// the canonical one 15 us and 1 us for 60000 scores.  8 x 64 rows of 8K, blocks
+// of 64: 29 us against 85; 8 x 8 rows of 32K, blocks of 16: 330 against 80.
+// Both are bounded by the table's width, not by lengths, which the host does not see.
+bool select_by_tensor(const Params& p, int n_rows, bool at_most) {
+  if (p.slots > sa::kTcMaxSlots || (long long)p.B * p.Hk * p.slots >= (1ll << 31)) return false;
+  const int T = p.sel_mode == SA_SELECT_GROUP ? 128 : 128 / p.G;
+  const int k = *std::max_element(p.k, p.k + p.Hq);
+  const long long items = ((long long)n_rows / T + std::min(p.B, n_rows)) * p.Hk;
+  const long long rounds = at_most ? 1 : (items + 303) / 304;    // at_most: for any number of rows up to these
+  const double tensor = rounds * (15.0 + 0.16 * p.slots) * (k > 40 ? 7.0 : 1.0);
+  return tensor < 15.0 + (double)n_rows * p.Hq * p.slots / 60e3;
 }
 struct SelectLayout {
   size_t norms, scores, total;
@@ -123,7 +133,8 @@ SelectLayout select_layout(const Params& p, int n_rows) {
   l.scores = off;
   // a workspace for n_rows serves fewer too, in either form
   size_t scores = sa::score_rows_scratch(p.slots, max_items(p, n_rows, 32));
-  if (select_by_tensor(p, n_rows)) scores = std::max(scores, sa::select_tc_scratch(p.slots));
+  if (select_by_tensor(p, n_rows, true))
+    scores = std::max(scores, sa::select_tc_scratch(p.slots, max_items(p, n_rows, 128)));
   off = up(off + scores);
   l.total = off;
   return l;
@@ -471,7 +482,7 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   A.group = p.sel_mode == SA_SELECT_GROUP;
   std::copy(p.bs, p.bs + p.Hk, A.bs);
   std::copy(p.k, p.k + p.Hq, A.k);
-  if (!select_by_tensor(p, n_rows)) {
+  if (!select_by_tensor(p, n_rows, false)) {
     A.n_items = (int)max_items(p, n_rows, 32);
     return sa::launch_score_rows(A, p.slots, as_stream(stream));
   }

@@ -21,60 +21,64 @@ constexpr int kPad = 16;                              // bytes behind a row in s
 constexpr int kRowStride = kD * 2 + kPad;
 constexpr size_t kScratchBytes = 256u << 20;          // at least one item
 
-// The sum of 128 products in the canonical order.
+// Byte selectors of two dims for max where q >= 0 and min elsewhere, as __byte_perm(max, min, .) takes them.
+__device__ __forceinline__ uint32_t selectors(uint32_t q) {
+  return (bf16_lo(q) >= 0.f ? 0x10u : 0x54u) | (bf16_hi(q) >= 0.f ? 0x3200u : 0x7600u);
+}
+
+// Four rows against two blocks, the sums of 128 products in the canonical
+// order.  The loop over lanes is kept a loop: all of it at once is 48 KB of
+// instructions.
 template <bool MINMAX>
-__device__ __forceinline__ void score_tile(const uint8_t* s_q, const uint8_t* s_lo, const uint8_t* s_hi, int r0, int c0,
-                                           float (&out)[4][2]) {
-  float quad[4][2], pair[4][2];
-#pragma unroll
-  for (int step = 0; step < 8; ++step) {
-    // lanes 0 4 2 6 1 5 3 7: (0 + 4) + (2 + 6), then (1 + 5) + (3 + 7)
-    constexpr int kOrder[8] = {0, 4, 2, 6, 1, 5, 3, 7};
-    const int part = kOrder[step];
-    float acc[4][2];
+__device__ __forceinline__ void score_tile(const uint8_t* s_q, const uint8_t* s_sel, const uint8_t* s_lo,
+                                           const uint8_t* s_hi, int r0, int c0, float (&out)[4][2]) {
+  auto lane_sum = [&](int part, float (&acc)[4][2]) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint4 q[4], lo[2], hi[2];
+      const int at = part * 32 + half * 16;
+      uint4 q[4], sel[4], lo[2], hi[2];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        q[r] = *reinterpret_cast<const uint4*>(s_q + (r0 + r) * kRowStride + part * 32 + half * 16);
+      for (int r = 0; r < 4; ++r) {
+        q[r] = *reinterpret_cast<const uint4*>(s_q + (r0 + r) * kRowStride + at);
+        if (MINMAX) sel[r] = *reinterpret_cast<const uint4*>(s_sel + (r0 + r) * kRowStride + at);
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        hi[c] = *reinterpret_cast<const uint4*>(s_hi + (c0 + 32 * c) * kRowStride + part * 32 + half * 16);
-        if (MINMAX) lo[c] = *reinterpret_cast<const uint4*>(s_lo + (c0 + 32 * c) * kRowStride + part * 32 + half * 16);
+        hi[c] = *reinterpret_cast<const uint4*>(s_hi + (c0 + 32 * c) * kRowStride + at);
+        if (MINMAX) lo[c] = *reinterpret_cast<const uint4*>(s_lo + (c0 + 32 * c) * kRowStride + at);
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint32_t x = reinterpret_cast<const uint32_t*>(&q[r])[w];
-          uint32_t sel = 0;
-          if (MINMAX)
-            sel = (bf16_lo(x) >= 0.f ? 0x10u : 0x54u) | (bf16_hi(x) >= 0.f ? 0x3200u : 0x7600u);
+          const uint32_t x = (&q[r].x)[w];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t y = reinterpret_cast<const uint32_t*>(&hi[c])[w];
-            if (MINMAX) y = __byte_perm(y, reinterpret_cast<const uint32_t*>(&lo[c])[w], sel);
-            float a = half == 0 && w == 0 ? -0.0f : acc[r][c];
-            a = fma_bf16_lo(x, y, a);
+            const uint32_t y = MINMAX ? __byte_perm((&hi[c].x)[w], (&lo[c].x)[w], (&sel[r].x)[w]) : (&hi[c].x)[w];
+            const float a = fma_bf16_lo(x, y, half == 0 && w == 0 ? -0.0f : acc[r][c]);
             acc[r][c] = fma_bf16_hi(x, y, a);
           }
         }
       }
     }
+  };
+  float first[4][2], quad[4][2];
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {        // lanes 0 and 4, 2 and 6; 1 and 5, 3 and 7
+    const int part = (i & 1) * 2 + (i >> 1);
+    float a[4][2], b[4][2];
+    lane_sum(part, a);
+    lane_sum(part + 4, b);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float a = acc[r][c];
-        if (step == 0 || step == 2 || step == 4 || step == 6) {
-          if (step == 0 || step == 4) pair[r][c] = a;
-          else out[r][c] = a;
-        } else if (step == 1 || step == 5) {
-          pair[r][c] = __fadd_rn(pair[r][c], a);
+        const float x = __fadd_rn(a[r][c], b[r][c]);
+        if ((i & 1) == 0) {
+          first[r][c] = x;
         } else {
-          const float four = __fadd_rn(pair[r][c], __fadd_rn(out[r][c], a));
-          if (step == 3) quad[r][c] = four;
+          const float four = __fadd_rn(first[r][c], x);
+          if (i == 1) quad[r][c] = four;
           else out[r][c] = __fadd_rn(__fadd_rn(quad[r][c], four), 0.0f);
         }
       }
@@ -83,10 +87,11 @@ __device__ __forceinline__ void score_tile(const uint8_t* s_q, const uint8_t* s_
 }
 
 template <bool MINMAX>
-__global__ void __launch_bounds__(kSelThreads) score_rows_kernel(SelectArgs A, int u0) {
+__global__ void __launch_bounds__(kSelThreads, 2) score_rows_kernel(SelectArgs A, int u0) {
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* s_q = smem;
-  uint8_t* s_hi = smem + kSelRows * kRowStride;
+  uint8_t* s_sel = s_q + kSelRows * kRowStride;
+  uint8_t* s_hi = s_sel + (MINMAX ? kSelRows * kRowStride : 0);
   uint8_t* s_lo = s_hi + kSelBlocks * kRowStride;
   __shared__ ItemPlace s_place;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -105,23 +110,35 @@ __global__ void __launch_bounds__(kSelThreads) score_rows_kernel(SelectArgs A, i
     if (r < it.tokens * A.G)
       v = reinterpret_cast<const uint4*>(A.q + ((size_t)(it.row0 + r / A.G) * A.Hq + h0 + r % A.G) * kD)[d];
     *reinterpret_cast<uint4*>(s_q + r * kRowStride + d * 16) = v;
+    if (MINMAX)
+      *reinterpret_cast<uint4*>(s_sel + r * kRowStride + d * 16) =
+          make_uint4(selectors(v.x), selectors(v.y), selectors(v.z), selectors(v.w));
   }
   constexpr int kVecs = (MINMAX ? 2 : 1) * (kD / 8);     // 16-byte pieces of a block's summary
   const uint4* summ = reinterpret_cast<const uint4*>(A.summaries) + ((size_t)it.b * A.Hk + it.kvh) * A.slots * kVecs;
   float* scratch = A.scores + (size_t)blockIdx.x * kSelRows * A.slots;
+  // a tile's summaries while the one before is scored
+  constexpr int kEach = kSelBlocks * kVecs / kSelThreads;
+  uint4 next[kEach];
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int x = e * kSelThreads + tid;
+      next[e] = c0 + x / kVecs < to ? __ldg(summ + (size_t)c0 * kVecs + x) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch(from);
   for (int c0 = from; c0 < to; c0 += kSelBlocks) {
     __syncthreads();
-#pragma unroll 4
-    for (int x = tid; x < kSelBlocks * kVecs; x += kSelThreads) {
-      const int d = x % (kD / 8), y = x / (kD / 8), c = MINMAX ? y >> 1 : y;
-      const bool low = MINMAX && (y & 1) == 0;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c0 + c < to) v = __ldg(summ + (size_t)c0 * kVecs + x);
-      *reinterpret_cast<uint4*>((low ? s_lo : s_hi) + c * kRowStride + d * 16) = v;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int x = e * kSelThreads + tid, d = x % (kD / 8), y = x / (kD / 8), c = MINMAX ? y >> 1 : y;
+      *reinterpret_cast<uint4*>((MINMAX && (y & 1) == 0 ? s_lo : s_hi) + c * kRowStride + d * 16) = next[e];
     }
     __syncthreads();
+    if (c0 + kSelBlocks < to) fetch(c0 + kSelBlocks);
     float z[4][2];
-    score_tile<MINMAX>(s_q, s_lo, s_hi, 4 * warp, lane, z);
+    score_tile<MINMAX>(s_q, s_sel, s_lo, s_hi, 4 * warp, lane, z);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
 #pragma unroll
@@ -173,7 +190,7 @@ size_t score_rows_scratch(int slots, long long n_items) {
 }
 
 int launch_score_rows(const SelectArgs& A, int max_candidates, cudaStream_t stream) {
-  const int smem = (kSelRows + (A.minmax ? 2 : 1) * kSelBlocks) * kRowStride;
+  const int smem = (A.minmax ? 2 : 1) * (kSelRows + kSelBlocks) * kRowStride;
   auto* score = A.minmax ? score_rows_kernel<true> : score_rows_kernel<false>;
   if (smem_limit_at_least(reinterpret_cast<const void*>(score), smem) != cudaSuccess) return SA_ERR_CUDA;
   const int at_a_time = (int)items_at_a_time(A.slots, A.n_items), T = kSelRows / A.G;
@@ -187,6 +204,8 @@ int launch_score_rows(const SelectArgs& A, int max_candidates, cudaStream_t stre
     // the smallest block that holds every candidate
     if (max_candidates <= 128 * 8)
       e = launch_pdl(topk_rows_kernel<128, 8>, lists, dim3(128), 0, stream, A, u0);
+    else if (max_candidates <= 256 * 8)
+      e = launch_pdl(topk_rows_kernel<256, 8>, lists, dim3(256), 0, stream, A, u0);
     else if (max_candidates <= 256 * 16)
       e = launch_pdl(topk_rows_kernel<256, 16>, lists, dim3(256), 0, stream, A, u0);
     else if (max_candidates <= 1024 * 16)

@@ -18,8 +18,11 @@
 //
 // q . min/max summary: sum over d of q+_d kmax_d + q-_d kmin_d with q+ and q-
 // the positive and negative part, a product of twice the length, half of it zeros.
-// Heads that select together: a row is a token and the product runs over the
-// group's heads too; E is G times that of the sum of their norms.
+// Heads that select together: a row is a token, and what the product takes is
+// the sum of the group's queries (of their positive and of their negative
+// parts), as two bf16 that hold 2^-17 of it, one product behind the other:
+// twice the steps, so E = 2^-14 |sum over heads of |q|| max_j |k_j|, which has
+// room for the heads' canonical sums and the rounding of the operand.
 //
 // A block (four warps, two blocks an SM) takes an item: one KV head with 128
 // rows (tokens and heads; tokens, for heads that select together) of a sequence, a thread a row.  Scores stay in
@@ -46,8 +49,12 @@ constexpr int kClose = 8;                                                   // o
 constexpr int kShort = 64, kShortRoom = kShort + 32, kShortK = 40;
 constexpr size_t kShortBytes = (size_t)kRows * kShortRoom * sizeof(float2);     // (score, candidate)
 
+// Tiles of summaries under way: what 96 KB, two blocks an SM, leave beside two
+// tiles of q (its parts, or the two bf16 of a group's sum).
 template <bool MINMAX>
-constexpr size_t kOperands = std::max<size_t>((MINMAX ? 2 : 1) * (2 * kHalfTile + 2 * kSummHalf), kShortBytes);
+constexpr int kStages = MINMAX ? 1 : 2;
+template <bool MINMAX>
+constexpr size_t kOperands = std::max<size_t>(4 * kHalfTile + kStages<MINMAX> * (MINMAX ? 4 : 2) * kSummHalf, kShortBytes);
 
 struct Warp {
   uint16_t close[32][kClose];
@@ -56,13 +63,17 @@ struct Warp {
 };
 struct Ctl {
   Warp warp[kThreads / 32];
-  uint64_t q_full, s_full, done;
+  uint64_t q_full, s_full[4], free[4], done;
+  float norm[kRows];
   uint32_t tmem;
   ItemPlace place;
 };
 template <bool MINMAX>
 constexpr size_t kSmem = 1024 + kOperands<MINMAX> + sizeof(Ctl);
 static_assert(2 * (kSmem<true> + 1024) <= 228 * 1024, "two blocks an SM");
+
+// Of a block's scratch: whole steps of candidates.
+__host__ __device__ constexpr size_t scratch_columns(int slots) { return (size_t)(slots + 31) / 32 * 32; }
 
 // The largest norm of max(|min|, |max|) (of the mean) among a KV head's summaries, as the bits of its square.
 template <bool MINMAX>
@@ -140,14 +151,20 @@ __device__ __forceinline__ unsigned choose_close(const SelectArgs& A, const RowT
   const int upto = warp_incl_scan(n_close), total = __shfl_sync(0xffffffffu, upto, 31), first = upto - n_close;
   for (int i = 0; i < n_close; ++i) w->task[first + i] = (uint16_t)(lane * kClose + i);
   __syncwarp();
-  for (int x0 = 0; x0 < total; x0 += 4) {
-    const int x = min(x0 + (lane >> 3), total - 1), task = w->task[x], who = task / kClose;
-    const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)t.q, who);
-    const size_t summ = __shfl_sync(0xffffffffu, (unsigned long long)t.summ, who);
-    const float z = row_score<MINMAX>(A, reinterpret_cast<const __nv_bfloat16*>(row),
-                                      reinterpret_cast<const __nv_bfloat16*>(summ) +
-                                          (size_t)w->close[who][task % kClose] * kSummary, part);
-    if (part == 0) w->score[x] = z;
+  for (int x0 = 0; x0 < total; x0 += 8) {      // two each eight lanes, their loads together
+    float z[2];
+    int x[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      x[y] = min(x0 + 4 * y + (lane >> 3), total - 1);
+      const int task = w->task[x[y]], who = task / kClose;
+      const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)t.q, who);
+      const size_t summ = __shfl_sync(0xffffffffu, (unsigned long long)t.summ, who);
+      z[y] = row_score<MINMAX>(A, reinterpret_cast<const __nv_bfloat16*>(row),
+                               reinterpret_cast<const __nv_bfloat16*>(summ) +
+                                   (size_t)w->close[who][task % kClose] * kSummary, part);
+    }
+    if (part < 2) w->score[part == 0 ? x[0] : x[1]] = part == 0 ? z[0] : z[1];
   }
   __syncwarp();
   unsigned chosen = 0;
@@ -247,8 +264,9 @@ template <>
 struct Counter<false> {
   __half2 h[kCols / 2];
   float mean, inv;
+  int used;      // chunks
   __device__ __forceinline__ Counter(const Scores<false>& S, int chunks, float m, float sigma)
-      : mean(m), inv(fminf(1.f / sigma, 1e30f)) {
+      : mean(m), inv(fminf(1.f / sigma, 1e30f)), used(chunks) {
 #pragma unroll
     for (int c = 0; c < kCols / kStep; ++c) {
       if (c < chunks) {
@@ -257,9 +275,6 @@ struct Counter<false> {
 #pragma unroll
         for (int i = 0; i < kStep / 2; ++i)
           h[c * (kStep / 2) + i] = __floats2half2_rn((v[2 * i] - mean) * inv, (v[2 * i + 1] - mean) * inv);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kStep / 2; ++i) h[c * (kStep / 2) + i] = __floats2half2_rn(-INFINITY, -INFINITY);
       }
     }
   }
@@ -269,7 +284,12 @@ struct Counter<false> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum[i] = __float2half2_rn(0.f);
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) sum[i & 3] = __hadd2(sum[i & 3], __hge2(h[i], t));
+    for (int c = 0; c < kCols / kStep; ++c) {
+      if (c < used) {
+#pragma unroll
+        for (int i = 0; i < kStep / 2; ++i) sum[i & 3] = __hadd2(sum[i & 3], __hge2(h[c * (kStep / 2) + i], t));
+      }
+    }
     const __half2 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
     return (int)(__low2float(all) + __high2float(all));
   }
@@ -540,18 +560,32 @@ __device__ __forceinline__ void select_list(const SelectArgs& A, const RowTask& 
     for (int i = 0; i < n_close; ++i)
       mine[((at_place >> (8 * i)) & 255) * kRows].x = (chosen >> i) & 1u ? INFINITY : -INFINITY;
   }
-  if (active) {       // the list, ascending
-    const int copies = A.group ? A.G : 1;
-    int* list = A.sel_idx + t.row * A.kcap;
-    int out = 0;
-#pragma unroll 4
-    for (int i = 0; i < len; ++i) {
-      const float2 x = mine[i * kRows];
-      if (x.x > sure && out < t.k) {
-        const int j = t.base + __float_as_int(x.y);
-        list[out] = j;
-        for (int y = 1; y < copies; ++y) list[(size_t)y * A.kcap + out] = j;
+  // the list, ascending
+  const int copies = A.group ? A.G : 1, longest = __reduce_max_sync(0xffffffffu, active ? len : 0);
+  int* list = A.sel_idx + t.row * A.kcap;
+  int out = 0;
+  for (int i0 = 0; i0 < longest; i0 += 8) {
+    float2 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = mine[(i0 + i) * kRows];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (active && i0 + i < len && x[i].x > sure && out < t.k) {
+        const int e = t.base + __float_as_int(x[i].y);
+        list[out] = e;
+        mine[out * kRows].y = __int_as_float(e);     // for the copies; its place has been read
         ++out;
+      }
+    }
+  }
+  if (copies > 1) {            // the group's other heads: a row at a time, its entries in turn by the lanes
+    __syncwarp();
+    for (unsigned m = __ballot_sync(0xffffffffu, active); m != 0; m &= m - 1) {
+      const int src = __ffs(m) - 1, k = __shfl_sync(0xffffffffu, t.k, src);
+      int* to = reinterpret_cast<int*>(__shfl_sync(0xffffffffu, (unsigned long long)list, src));
+      for (int j = lane; j < k; j += 32) {
+        const int e = __float_as_int(mine[src - lane + j * kRows].y);
+        for (int y = 1; y < copies; ++y) to[(size_t)y * A.kcap + j] = e;
       }
     }
   }
@@ -559,18 +593,108 @@ __device__ __forceinline__ void select_list(const SelectArgs& A, const RowTask& 
   if (rows != 0) select_whole<MINMAX>(A, t, rows, keys);
 }
 
+// A row of q in shared memory (128-byte swizzle) becomes q+, and q- a tile
+// further on; its squared norm.
+template <bool MINMAX>
+__device__ __forceinline__ float split_row(uint8_t* s_q, int row) {
+  float sq = 0.f;
+#pragma unroll 4
+  for (int x = 0; x < 16; ++x) {
+    uint4* p = reinterpret_cast<uint4*>(s_q + (x >> 3) * kHalfTile + row * 128 + (((x & 7) ^ (row & 7)) << 4));
+    uint4 y = *p, neg = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t& a = (&y.x)[e];
+      const float lo = bf16_lo(a), hi = bf16_hi(a);
+      sq = fmaf(lo, lo, sq);
+      sq = fmaf(hi, hi, sq);
+      if (MINMAX) {
+        const uint32_t minus = (a & 0x8000u ? 0xffffu : 0u) | (a & 0x80000000u ? 0xffff0000u : 0u);
+        (&neg.x)[e] = a & minus;
+        a &= ~minus;
+      }
+    }
+    if (MINMAX) {
+      *p = y;
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + 2 * kHalfTile) = neg;
+    }
+  }
+  return sq;
+}
+
+// The sums of a group's queries as the operand, rounded to bf16, and what that
+// leaves, rounded too: of all at once in two tiles, or of the positive and of
+// the negative parts in two tiles, the rounded ones in part 0 and the rest in
+// part 1.  16 threads a row.  Answers the norm of the thread's row's sum of |q|.
+template <bool MINMAX>
+__device__ __forceinline__ float sum_of_heads(const SelectArgs& A, const SelectItem& it, uint8_t* s_q, int part,
+                                              float* s_norm) {
+  const int tid = threadIdx.x, x = tid & 15;
+#pragma unroll 2
+  for (int row = tid >> 4; row < kRows; row += kThreads / 16) {
+    const uint4* q = reinterpret_cast<const uint4*>(
+        A.q + ((size_t)min(it.row0 + row, A.n_rows - 1) * A.Hq + it.kvh * A.G) * kD) + x;
+    uint4 y[kMaxG];
+#pragma unroll
+    for (int g = 0; g < kMaxG; ++g) y[g] = g < A.G ? __ldg(q + g * (kD / 8)) : make_uint4(0, 0, 0, 0);
+    float plus[8], minus[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      plus[e] = minus[e] = 0.f;
+#pragma unroll
+      for (int g = 0; g < kMaxG; ++g) {
+        const uint32_t w = (&y[g].x)[e >> 1];
+        const float v = e & 1 ? bf16_hi(w) : bf16_lo(w);
+        plus[e] += v > 0.f ? v : 0.f;
+        minus[e] += v > 0.f ? 0.f : v;            // NaN goes here
+      }
+    }
+    float sq = 0.f;
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float both = plus[e] - minus[e];
+      sq = fmaf(both, both, sq);
+      if (!MINMAX) plus[e] += minus[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      auto rest = [](float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); };
+      const float p0 = plus[2 * e], p1 = plus[2 * e + 1], m0 = minus[2 * e], m1 = minus[2 * e + 1];
+      if (MINMAX) {
+        a[e] = part == 0 ? pack_bf16(p0, p1) : pack_bf16(rest(p0), rest(p1));
+        b[e] = part == 0 ? pack_bf16(m0, m1) : pack_bf16(rest(m0), rest(m1));
+      } else {
+        a[e] = pack_bf16(p0, p1);
+        b[e] = pack_bf16(rest(p0), rest(p1));
+      }
+    }
+    uint8_t* p = s_q + (x >> 3) * kHalfTile + row * 128 + (((x & 7) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(p) = make_uint4(a[0], a[1], a[2], a[3]);
+    *reinterpret_cast<uint4*>(p + 2 * kHalfTile) = make_uint4(b[0], b[1], b[2], b[3]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (x == 0) s_norm[row] = sqrtf(sq);
+  }
+  __syncthreads();
+  return s_norm[tid];
+}
+
 template <bool MINMAX>
 __global__ void __launch_bounds__(kThreads, 2)
 select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmS) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_q = smem;                                             // [q or q+, q-][half of the dims][128 rows][64]
-  uint8_t* s_k = smem + (MINMAX ? 2 : 1) * 2 * kHalfTile;          // [max, min][half][64 blocks][64]
+  uint8_t* s_q = smem;                         // [q+, q- or a sum's two bf16][half of the dims][128 rows][64]
+  uint8_t* s_k = smem + 4 * kHalfTile;         // [stage][max, min][half][64 blocks][64]
   Ctl* c = reinterpret_cast<Ctl*>(smem + kOperands<MINMAX>);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     mbar_init(&c->q_full, 1);
-    mbar_init(&c->s_full, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&c->s_full[i], 1);
+      mbar_init(&c->free[i], 1);
+    }
     mbar_init(&c->done, 1);
     fence_mbar_init();
   }
@@ -583,10 +707,11 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
   const uint32_t tmem = c->tmem, mine = tmem + ((uint32_t)warp << 21);
   const uint64_t dQ = smem_desc(smem_u32(s_q), 16, 1024), dK = smem_desc(smem_u32(s_k), 16, 1024);
   constexpr uint32_t id = bf16_idesc(kRows, kTile, false);
-  float* scratch = A.scores + (size_t)blockIdx.x * A.slots * (kRows + kThreads / 32);
-  float* keys = scratch + (size_t)A.slots * kRows + (size_t)warp * A.slots;
-  const int T = A.group ? kRows : kRows / A.G, heads = A.group ? A.G : 1;
-  uint32_t q_phase = 0, s_phase = 0, d_phase = 0;
+  const size_t columns = scratch_columns(A.slots);
+  float* scratch = A.scores + blockIdx.x * columns * (kRows + kThreads / 32);
+  float* keys = scratch + columns * (kRows + warp);
+  const int T = A.group ? kRows : kRows / A.G, parts = MINMAX && A.group ? 2 : 1;
+  uint32_t q_phase = 0, tile = 0, d_phase = 0;
   bool ok = true;
   for (int u = blockIdx.x; u < A.n_items; u += gridDim.x) {
     SelectItem it;
@@ -626,67 +751,61 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
     const bool memory = n_item > kCols;
     for (int w0 = 0; w0 < n_item && ok; w0 += kCols) {
       const int cols = min(kCols, n_item - w0);
-      for (int head = 0; head < heads && ok; ++head) {
-        if (w0 == 0 || heads > 1) {       // else q is there
-          if (tid == 0) {
-            const int rows = A.group ? kRows : T * A.G;
-            mbar_arrive_expect_tx(&c->q_full, rows * kD * 2);
+      for (int part = 0; part < parts && ok; ++part) {
+        constexpr int kPieces = MINMAX ? 4 : 2, kStageBytes = kPieces * kSummHalf, kS = kStages<MINMAX>;
+        const int tiles = (cols + kTile - 1) / kTile, slot0 = (it.b * A.Hk + it.kvh) * A.slots + j0 + w0;
+        auto load = [&](int i) {     // summaries behind the item's last come along; no row looks at them
+          uint64_t* bar = &c->s_full[(tile + i) % kS];
+          mbar_arrive_expect_tx(bar, kStageBytes);
+          for (int y = 0; y < kPieces; ++y)
+            tma_load_3d(s_k + (tile + i) % kS * kStageBytes + y * kSummHalf, &tmS, (y & 1) * 64, MINMAX ? 1 - (y >> 1) : 0,
+                        slot0 + i * kTile, bar);
+        };
+        if (tid == 0) {
+          if (!A.group && w0 == 0) {
+            mbar_arrive_expect_tx(&c->q_full, T * A.G * kD * 2);
             for (int half = 0; half < 2; ++half)
-              tma_load_3d(s_q + half * kHalfTile, &tmQ, half * 64, h0 + head, it.row0, &c->q_full);
+              tma_load_3d(s_q + half * kHalfTile, &tmQ, half * 64, h0, it.row0, &c->q_full);
           }
-          ok = mbar_wait_bounded(&c->q_full, q_phase & 1, A.status);
-          ++q_phase;
-          // q+ and q- of the thread's row, and its norm
-          float sq = 0.f;
-          if (ok) {
-#pragma unroll 4
-            for (int x = 0; x < 16; ++x) {
-              uint4* p = reinterpret_cast<uint4*>(s_q + (x >> 3) * kHalfTile + tid * 128 + (((x & 7) ^ (tid & 7)) << 4));
-              uint4 y = *p, neg = make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < min(tiles, kS); ++i) load(i);
+        }
+        __syncwarp();
+        if (!A.group) {
+          if (w0 == 0) {
+            ok = mbar_wait_bounded(&c->q_full, q_phase & 1, A.status);
+            ++q_phase;
+            if (ok) norm = sqrtf(split_row<MINMAX>(s_q, tid));
+          }
+        } else if (MINMAX || w0 == 0) {      // else both are there
+          norm = sum_of_heads<MINMAX>(A, it, s_q, part, c->norm);
+        }
+        fence_proxy_async_smem();
+        ok = !__syncthreads_or(!ok);
+        if (ok && tid == 0) {
+          const int steps = MINMAX || A.group ? 16 : 8;
+          for (int i = 0; i < tiles; ++i) {
+            const uint32_t stage = (tile + i) % kS, parity = ((tile + i) / kS) & 1;
+            if (!(ok = mbar_wait_bounded(&c->s_full[stage], parity, A.status))) break;
+            tc_fence_after();
+            const uint64_t k = dK + stage * (kStageBytes / 16);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t& a = (&y.x)[e];
-                const float lo = bf16_lo(a), hi = bf16_hi(a);
-                sq = fmaf(lo, lo, sq);
-                sq = fmaf(hi, hi, sq);
-                if (MINMAX) {
-                  const uint32_t minus = (a & 0x8000u ? 0xffffu : 0u) | (a & 0x80000000u ? 0xffff0000u : 0u);
-                  (&neg.x)[e] = a & minus;
-                  a &= ~minus;
-                }
-              }
-              if (MINMAX) {
-                *p = y;
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + 2 * kHalfTile) = neg;
-              }
+            for (int y = 0; y < 16; ++y)
+              if (y < steps)
+                tc_mma_ss(tmem + i * kTile, dQ + (y >> 2) * (kHalfTile / 16) + (y & 3) * 2,
+                          k + (y >> 2) % kPieces * (kSummHalf / 16) + (y & 3) * 2, id, y != 0 || part != 0);
+            tc_commit(&c->free[stage]);
+            if (i + kS < tiles) {
+              if (!(ok = mbar_wait_bounded(&c->free[stage], parity, A.status))) break;
+              load(i + kS);
             }
           }
-          if (w0 == 0) norm += sqrtf(sq);
-          fence_proxy_async_smem();
-          ok = !__syncthreads_or(!ok);
+          tc_commit(&c->done);
         }
-        for (int x = 0; x < cols && ok; x += kTile) {
-          if (tid == 0) {
-            // summaries behind the item's last come along; no row looks at them
-            const int slot = ((it.b * A.Hk + it.kvh) * A.slots) + j0 + w0 + x;
-            mbar_arrive_expect_tx(&c->s_full, (MINMAX ? 4 : 2) * kSummHalf);
-            for (int y = 0; y < (MINMAX ? 4 : 2); ++y)
-              tma_load_3d(s_k + y * kSummHalf, &tmS, (y & 1) * 64, MINMAX ? 1 - (y >> 1) : 0, slot, &c->s_full);
-            ok = mbar_wait_bounded(&c->s_full, s_phase & 1, A.status);
-            if (ok) {
-              tc_fence_after();
-#pragma unroll
-              for (int y = 0; y < (MINMAX ? 16 : 8); ++y)
-                tc_mma_ss(tmem + x, dQ + (y >> 2) * (kHalfTile / 16) + (y & 3) * 2,
-                          dK + (y >> 2) * (kSummHalf / 16) + (y & 3) * 2, id, y != 0 || head != 0);
-              tc_commit(&c->done);
-            }
-          }
-          ++s_phase;
-          if (ok) ok = mbar_wait_bounded(&c->done, d_phase & 1, A.status);
-          ++d_phase;
-          ok = !__syncthreads_or(!ok);
-        }
+        __syncwarp();        // lanes that wait for `done` already would hold up the one that issues
+        tile += tiles;
+        if (ok) ok = mbar_wait_bounded(&c->done, d_phase & 1, A.status);
+        ++d_phase;
+        ok = !__syncthreads_or(!ok);
       }
       if (!ok) break;
       tc_fence_after();
@@ -705,7 +824,7 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
     }
     if (!ok) break;
     const float k2 = __int_as_float(__ldg(A.norms + it.b * A.Hk + it.kvh));
-    t.E = 3.0517578125e-5f * heads * norm * sqrtf(k2) * 1.001f + 1e-35f;
+    t.E = (A.group ? 6.103515625e-5f : 3.0517578125e-5f) * norm * sqrtf(k2) * 1.001f + 1e-35f;
     float2* list = reinterpret_cast<float2*>(smem) + tid;      // the operands are done with
     const int n = t.valid ? t.n : 0;
     if (memory) select_list<MINMAX, true>(A, t, Scores<true>{mine, scratch + tid, n}, keys, &c->warp[warp], list);
@@ -723,8 +842,9 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
 
 }  // namespace
 
-size_t select_tc_scratch(int slots) {
-  return (size_t)2 * kRowsMaxCtas * slots * (kRows + kThreads / 32) * sizeof(float);
+size_t select_tc_scratch(int slots, long long n_items) {
+  const size_t blocks = (size_t)std::min<long long>(2 * kRowsMaxCtas, n_items);
+  return blocks * scratch_columns(slots) * (kRows + kThreads / 32) * sizeof(float);
 }
 
 template <bool MINMAX>
