@@ -100,6 +100,7 @@ struct RowsAttnArgs {
   uint32_t* pages;                  // [n_items][words] a bit for each page that some row of the item sees
   int* ranks;                       // [n_rows][Hq][rank_stride] a row's blocks as places in that list
   int* ticket;                      // the next item to take (of those behind one a block), items there are
+  int* arrived;                     // in the workspace's header: blocks that are done, zero between calls
   int n_items, words;               // at most that many; ceil(mpp / 32)
   int kcap, rank_stride, S, W;      // rank_stride: kcap up to a multiple of four
   unsigned char bs_shift[SA_MAX_HK];

@@ -514,6 +514,7 @@ int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* 
   A.items = at<sa::SparseItem>(ws, l.items);
   A.before = at<long long>(ws, l.before);
   A.ticket = at<int>(ws, l.ticket);
+  A.arrived = at<sa::WsHeader>(ws, 0)->pad;
   A.pages = at<uint32_t>(ws, l.pages);
   A.n_items = (int)max_items(p, n_rows, 256);
   A.words = l.words;

@@ -570,43 +570,62 @@ template <>
 struct PageWalk<kSparse> {
   const uint32_t* bits;
   int words, base;       // base: the first of the 32 words that the lanes hold
-  uint32_t mine;         // pages not given yet
+  uint32_t mine;
+  int upto, total;       // pages up to and with the lane's word, of all 32
+  int given;             // of these
   __device__ __forceinline__ void load() {
     const int w = base + (threadIdx.x & 31);
     mine = w < words ? __ldg(bits + w) : 0u;
+    upto = warp_incl_scan(__popc(mine));
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    given = 0;
   }
   // ahead: pages to pass over
   __device__ __forceinline__ PageWalk(const RowsAttnArgs& A, const Piece& p, int ahead)
       : bits(A.pages + (size_t)p.u * A.words), words((p.end + 32 * kP - 1) / (32 * kP)), base(0) {
     load();
-    while (true) {
-      const int n = __popc(mine), upto = warp_incl_scan(n), total = __shfl_sync(0xffffffffu, upto, 31);
-      if (ahead < total || base + 32 >= words) {
-        for (int d = min(ahead - (upto - n), n); d > 0; --d) mine &= mine - 1;
-        return;
-      }
+    while (ahead >= total && base + 32 < words) {
       ahead -= total;
       base += 32;
       load();
     }
+    given = min(ahead, total);
   }
-  __device__ __forceinline__ void next(int* page) {
+  // Lane j < 8: the j-th of the next eight, -1 where there are no more.
+  __device__ __forceinline__ int next() {
     const int lane = threadIdx.x & 31;
-    if (lane < 8) page[lane] = -1;
-    __syncwarp();
-    int got = 0;
+    int page = -1, got = 0;
     while (true) {
-      const int n = __popc(mine), upto = warp_incl_scan(n), total = __shfl_sync(0xffffffffu, upto, 31);
-      for (int at = got + upto - n; mine != 0 && at < 8; ++at) {
-        page[at] = (base + lane) * 32 + __ffs(mine) - 1;
-        mine &= mine - 1;
+      // the word with page `want`: behind all that hold fewer
+      const int want = given + lane - got;
+      int owner = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = __popc(__ballot_sync(0xffffffffu, upto <= given + j - got));
+        if (lane == j) owner = n;
       }
-      got += total;
-      if (got >= 8 || base + 32 >= words) break;
+      owner = min(owner, 31);
+      uint32_t x = __shfl_sync(0xffffffffu, mine, owner);
+      int k = want - (__shfl_sync(0xffffffffu, upto, owner) - __popc(x));     // of the word's
+      if (lane >= got && lane < 8 && want < total) {
+        page = (base + owner) * 32;
+#pragma unroll
+        for (int half = 16; half > 0; half >>= 1) {
+          const int n = __popc(x & ((1u << half) - 1u));
+          if (k >= n) {
+            k -= n;
+            x >>= half;
+            page += half;
+          }
+        }
+      }
+      const int take = min(8 - got, total - given);
+      got += take;
+      given += take;
+      if (got == 8 || base + 32 >= words) return page;
       base += 32;
       load();
     }
-    __syncwarp();
   }
 };
 
@@ -909,34 +928,25 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         tmem_ld64_start<0>(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
         tmem_ld64_finish<0>(v);
+        uint32_t see[4] = {0, 0, 0, 0};      // kSparse: a bit for each column
         if constexpr (KIND == kSparse) {
           if (bad != 0) {
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {
-              uint32_t see = 0;            // bit j: column 32 w + j
+            const int* page = ring->page[(tiles + t) % kPageDepth];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int page = ring->page[(tiles + t) % kPageDepth][2 * w + (e >> 1)], t0 = page * kP + 8 * (e & 1);
-                auto below = [t0](int x) { return (1u << min(max(x - t0, 0), 8)) - 1u; };   // of 8 tokens, those before x
-                uint32_t x = (mask >> (4 * w + e)) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
-                x &= page < 0 || ((bad >> (2 * w + (e >> 1))) & 1u) ? 0u : below(lim);
-                see |= x << (8 * e);
-              }
-              float x[32];
-              uint32_t y[32];
-              tmem_ld32(tS + 32 * w, x);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) y[j] = (see >> j) & 1u ? __float_as_uint(x[j]) : 0xff800000u;
-              tmem_st32(tS + 32 * w, y);
+            for (int e = 0; e < 16; ++e) {
+              const int t0 = page[e >> 1] * kP + 8 * (e & 1);
+              auto below = [t0](int x) { return (1u << min(max(x - t0, 0), 8)) - 1u; };   // of 8 tokens, those before x
+              uint32_t x = (mask >> e) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
+              x &= t0 < 0 || ((bad >> (e >> 1)) & 1u) ? 0u : below(lim);
+              see[e >> 2] |= x << (8 * (e & 3));
             }
-            tmem_wait_st();
-            tmem_ld64_start<0>(tS, v);
-            tmem_ld64_finish<0>(v);
-            mask = 0xffffu;
+          } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) see[w] = ((((mask >> (4 * w)) & 15u) * 0x00204081u) & 0x01010101u) * 255u;
           }
 #pragma unroll
           for (int j = 0; j < 64; ++j)
-            if (!((mask >> (j >> 3)) & 1u)) v[j] = -INFINITY;
+            if (!((see[j >> 5] >> (j & 31)) & 1u)) v[j] = -INFINITY;
         } else if ((kt + 1) * kRows > edge || bad != 0) {
           // masked in TMEM, 32 columns at a time: once or twice an item, and
           // a long piece of straight code would cost its instruction fetches
@@ -975,7 +985,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         if constexpr (KIND == kSparse) {
 #pragma unroll
           for (int j = 64; j < 128; ++j)
-            if (!((mask >> (j >> 3)) & 1u)) v[j] = -INFINITY;
+            if (!((see[j >> 5] >> (j & 31)) & 1u)) v[j] = -INFINITY;
         }
 #pragma unroll
         for (int j = 64; j < 128; j += 8) {
@@ -1354,8 +1364,8 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
           if constexpr (KIND == kSparse) {
             if (t == ntp) return -1;
             int* place = ring->page[(tile + t) % kPageDepth];
-            pages.next(place);
-            page = lane < kRows / kP ? place[lane] : -1;
+            page = pages.next();
+            if (lane < kRows / kP) place[lane] = page;
             // views begin or end inside 8 tokens where the sinks do, and where rows' windows and the rows themselves are
             const int t0 = page * kP, w0 = p.a + 1 - A.W, w1 = w0 + p.tokens - 1;
             const bool in = ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) || t0 + kP > p.a;

@@ -9,136 +9,31 @@
 // instructions an entry (looking every page of a tile up in the list took the
 // attention three times as long).
 //
-// A block an item: bits are set in shared memory, so lists of any length and
-// order give the same bitmap.  Bound by the latency of its reads (offsets,
-// counts, lists) and the lists' bytes.  A second kernel sums the items' weights
-// up for the attention's blocks.
+// A block an item: bits are set in shared memory, so lists of any length give
+// the same bitmap whatever the order of the threads.  Bound by the latency of
+// its reads (offsets, then counts and entries, four rows' at once) and the
+// lists' bytes: a row a warp at a time, counts first, took 375 us of a 32K
+// prompt's 3.7 ms.  The last block to finish sums the items' weights up for the
+// attention's blocks.
 #include "rows.cuh"
 
 namespace sa {
 namespace {
 
-constexpr int kItemThreads = 128, kScanThreads = 1024, kScanEach = 4;
+constexpr int kItemThreads = 256, kAtOnce = 4, kScanEach = 4;
+constexpr int kNone = 0x7fffffff;
 
-__global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs A) {
-  extern __shared__ uint32_t s_bits[];
-  __shared__ ItemPlace s_place;
-  __shared__ int s_sum[kItemThreads / 32];
+// before[u + 1]: item u's weight becomes the sum up to and with it.  A whole block.
+__device__ void sum_weights(const RowsAttnArgs& A, long long* s_sum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int u = blockIdx.x, T = 2 * A.tpt;
-  pdl_wait();
-  pdl_trigger();
-  find_item<kItemThreads>(A.row_offsets, A.seq_lens, A.B, A.n_rows, A.mpp, A.Hk, T, u, A.status, &s_place);
-  const int b = s_place.b;
-  SparseItem it{};
-  if (b < 0) {
-    if (tid == 0) {
-      A.items[u] = it;
-      A.before[u + 1] = 0;
-    }
-    return;
-  }
-  const RowSeq s = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, nullptr);
-  it.b = b;
-  it.kvh = s_place.kvh;
-  it.i = (s.n + T - 1) / T - 1 - s_place.i;      // those that see most first: the last ones taken are short
-  it.tokens = min(T, s.n - it.i * T);
-  it.row0 = s.row0 + it.i * T;
-  it.pos0 = s.a + it.i * T;
-  it.end = max(0, min(s.L, it.pos0 + it.tokens));
-  const int n_pages = (it.end + kP - 1) / kP, words = (n_pages + 31) / 32;
-  for (int w = tid; w < words; w += kItemThreads) s_bits[w] = 0;
-  __syncthreads();
-  auto set = [&](int page) {
-    const uint32_t bit = 1u << (page & 31);
-    if (!(*(volatile uint32_t*)&s_bits[page >> 5] & bit)) atomicOr(&s_bits[page >> 5], bit);
-  };
-  if (it.end > 0) {
-    const int sinks = (min(A.S, it.end) + kP - 1) / kP;
-    for (int page = tid; page < sinks; page += kItemThreads) set(page);
-    const int first = max(it.pos0, 0);                    // the first row that sees anything
-    const int window = first + 1 > A.W ? first + 1 - A.W : 0;
-    for (int page = window / kP + tid; page < n_pages; page += kItemThreads) set(page);
-    const int shift = A.bs_shift[it.kvh];
-    for (int r = warp; r < it.tokens * A.G; r += kItemThreads / 32) {
-      const int tok = r / A.G, pos = min(it.pos0 + tok, it.end - 1);   // rows behind the table see what lies in it
-      if (it.pos0 + tok < 0) continue;
-      const size_t row = (size_t)(it.row0 + tok) * A.Hq + it.kvh * A.G + (r - tok * A.G);
-      const int n = min(max(__ldg(A.sel_cnt + row), 0), A.kcap);
-      const int* list = A.sel_idx + row * A.kcap;
-      for (int j = lane; j < n; j += 32) {
-        const int e = __ldg(list + j);
-        if (e < 0 || e > pos >> shift) continue;
-        const int t0 = e << shift, last = min(t0 + (1 << shift) - 1, pos) / kP;
-        for (int page = t0 / kP; page <= last; ++page) set(page);
-      }
-    }
-  }
-  __syncthreads();
-  // pages ahead of each word
-  int* s_ahead = reinterpret_cast<int*>(s_bits + A.words);
-  int carry = 0;
-  for (int w0 = 0; w0 < words; w0 += kItemThreads) {
-    const int w = w0 + tid;
-    const uint32_t x = w < words ? s_bits[w] : 0u;
-    if (w < words) A.pages[(size_t)u * A.words + w] = x;
-    const int n = __popc(x), incl = warp_incl_scan(n);
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    int at = carry + incl - n, total = 0;
-#pragma unroll
-    for (int y = 0; y < kItemThreads / 32; ++y) {
-      if (y < warp) at += s_sum[y];
-      total += s_sum[y];
-    }
-    if (w < words) s_ahead[w] = at;
-    __syncthreads();
-    carry += total;
-  }
-  // the lists again, entries that count alone: the place of a block's first half page
-  const int shift = A.bs_shift[it.kvh];
-  for (int r = warp; r < it.tokens * A.G; r += kItemThreads / 32) {
-    const int tok = r / A.G, pos = min(it.pos0 + tok, it.end - 1);
-    if (it.pos0 + tok < 0) continue;
-    const size_t row = (size_t)(it.row0 + tok) * A.Hq + it.kvh * A.G + (r - tok * A.G);
-    const int n = min(max(__ldg(A.sel_cnt + row), 0), A.kcap);
-    const int* list = A.sel_idx + row * A.kcap;
-    int* ranks = A.ranks + row * A.rank_stride;
-    int m = 0;
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      const int e = j0 + lane < n ? __ldg(list + j0 + lane) : -1;
-      const bool on = e >= 0 && pos >= 0 && e <= pos >> shift;
-      const unsigned all = __ballot_sync(0xffffffffu, on);
-      if (on) {
-        const int page = (e << shift) / kP, w = page >> 5;
-        const int rank = s_ahead[w] + __popc(s_bits[w] & ((1u << (page & 31)) - 1u));
-        ranks[m + __popc(all & ((1u << lane) - 1u))] = 2 * rank + (shift == 3 ? e & 1 : 0);
-      }
-      m += __popc(all);
-    }
-    for (int j = m + lane; j < A.rank_stride; j += 32) ranks[j] = 0x7fffffff;
-  }
-  if (tid == 0) {
-    it.pages = carry;
-    A.items[u] = it;
-    A.before[u + 1] = (long long)((carry + 7) / 8) * kSparseTileCost + kSparseItemCost;
-  }
-}
-
-// before[u + 1]: item u's weight becomes the sum up to and with it.
-__global__ void __launch_bounds__(kScanThreads) sparse_scan_kernel(RowsAttnArgs A) {
-  __shared__ long long s_sum[kScanThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_trigger();
   long long carry = 0;
   int real = 0;
-  for (int u0 = 0; u0 < A.n_items; u0 += kScanThreads * kScanEach) {
+  for (int u0 = 0; u0 < A.n_items; u0 += kItemThreads * kScanEach) {
     long long x[kScanEach], sum = 0;
 #pragma unroll
     for (int e = 0; e < kScanEach; ++e) {
       const int u = u0 + tid * kScanEach + e;
-      x[e] = u < A.n_items ? A.before[u + 1] : 0;
+      x[e] = u < A.n_items ? *(volatile long long*)(A.before + u + 1) : 0;
       sum += x[e];
       real += x[e] > 0;
     }
@@ -152,7 +47,7 @@ __global__ void __launch_bounds__(kScanThreads) sparse_scan_kernel(RowsAttnArgs 
     __syncthreads();
     long long at = carry + incl - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w < kScanThreads / 32; ++w) {
+    for (int w = 0; w < kItemThreads / 32; ++w) {
       if (w < warp) at += s_sum[w];
       total += s_sum[w];
     }
@@ -174,13 +69,138 @@ __global__ void __launch_bounds__(kScanThreads) sparse_scan_kernel(RowsAttnArgs 
   if (lane == 0 && real > 0) atomicAdd(A.ticket + 1, real);
 }
 
+// f(row, entry's index j, entry) for all places j < rank_stride of the lists of
+// an item's rows; entries behind a row's count are kNone.
+template <typename F>
+__device__ __forceinline__ void each_entry(const RowsAttnArgs& A, const SparseItem& it, F f) {
+  int per = 4;                                       // lanes a row: a power of two
+  while (per < A.rank_stride && per < 32) per *= 2;
+  const int tid = threadIdx.x, sub = tid % per, groups = kItemThreads / per, blocks = (A.rank_stride + per - 1) / per;
+  const int units = it.tokens * A.G * blocks;        // of `per` places of a row's list
+  for (int i0 = tid / per; i0 < units; i0 += groups * kAtOnce) {
+    int n[kAtOnce], e[kAtOnce], r[kAtOnce], j[kAtOnce];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const int i = i0 + x * groups;
+      r[x] = i < units ? i / blocks : -1;
+      j[x] = i < units ? (i - r[x] * blocks) * per + sub : kNone;
+      n[x] = 0;
+      e[x] = 0;
+      if (r[x] >= 0) {
+        const int tok = r[x] / A.G;
+        const size_t row = (size_t)(it.row0 + tok) * A.Hq + it.kvh * A.G + (r[x] - tok * A.G);
+        n[x] = __ldg(A.sel_cnt + row);
+        if (j[x] < A.kcap) e[x] = __ldg(A.sel_idx + row * A.kcap + j[x]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x)
+      if (j[x] < A.rank_stride) f(r[x], j[x], j[x] < min(n[x], A.kcap) ? e[x] : kNone);
+  }
+}
+
+__global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs A) {
+  extern __shared__ uint32_t s_bits[];
+  __shared__ ItemPlace s_place;
+  __shared__ long long s_sum[kItemThreads / 32];
+  __shared__ bool s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = blockIdx.x, T = 2 * A.tpt;
+  pdl_wait();
+  pdl_trigger();
+  find_item<kItemThreads>(A.row_offsets, A.seq_lens, A.B, A.n_rows, A.mpp, A.Hk, T, u, A.status, &s_place);
+  const int b = s_place.b;
+  SparseItem it{};
+  long long weight = 0;
+  if (b >= 0) {
+    const RowSeq s = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, nullptr);
+    it.b = b;
+    it.kvh = s_place.kvh;
+    it.i = (s.n + T - 1) / T - 1 - s_place.i;      // those that see most first: the last ones taken are short
+    it.tokens = min(T, s.n - it.i * T);
+    it.row0 = s.row0 + it.i * T;
+    it.pos0 = s.a + it.i * T;
+    it.end = max(0, min(s.L, it.pos0 + it.tokens));
+    const int n_pages = (it.end + kP - 1) / kP, words = (n_pages + 31) / 32;
+    for (int w = tid; w < words; w += kItemThreads) s_bits[w] = 0;
+    __syncthreads();
+    auto set = [&](int w, uint32_t m) {
+      if ((*(volatile uint32_t*)&s_bits[w] & m) != m) atomicOr(&s_bits[w], m);
+    };
+    const int shift = A.bs_shift[it.kvh];
+    // a row's last position that is there (rows behind the table see what lies in it); negative: it sees nothing
+    auto last_pos = [&](int r) {
+      const int pos = it.pos0 + r / A.G;
+      return pos < 0 ? pos : min(pos, it.end - 1);
+    };
+    if (it.end > 0) {
+      const int sinks = (min(A.S, it.end) + kP - 1) / kP;
+      for (int page = tid; page < sinks; page += kItemThreads) set(page >> 5, 1u << (page & 31));
+      const int first = max(it.pos0, 0);                    // the first row that sees anything
+      const int window = first + 1 > A.W ? first + 1 - A.W : 0;
+      for (int page = window / kP + tid; page < n_pages; page += kItemThreads) set(page >> 5, 1u << (page & 31));
+      each_entry(A, it, [&](int r, int, int e) {
+        const int pos = last_pos(r);
+        if (pos < 0 || e < 0 || e > pos >> shift) return;
+        const int page = (e << shift) / kP, end = min(((e + 1) << shift) - 1, pos) / kP;   // in one word: aligned
+        set(page >> 5, ((2u << (end - page)) - 1u) << (page & 31));
+      });
+    }
+    __syncthreads();
+    // pages ahead of each word
+    int* s_ahead = reinterpret_cast<int*>(s_bits + A.words);
+    int* s_warp = reinterpret_cast<int*>(s_sum);
+    int carry = 0;
+    for (int w0 = 0; w0 < words; w0 += kItemThreads) {
+      const int w = w0 + tid;
+      const uint32_t x = w < words ? s_bits[w] : 0u;
+      if (w < words) A.pages[(size_t)u * A.words + w] = x;
+      const int n = __popc(x), incl = warp_incl_scan(n);
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      int at = carry + incl - n, total = 0;
+#pragma unroll
+      for (int y = 0; y < kItemThreads / 32; ++y) {
+        if (y < warp) at += s_warp[y];
+        total += s_warp[y];
+      }
+      if (w < words) s_ahead[w] = at;
+      __syncthreads();
+      carry += total;
+    }
+    // the lists again: the place of a block's first half page.  Entries below zero are ahead of all of them,
+    // those behind the row or its count are behind, so that lists stay ascending.
+    each_entry(A, it, [&](int r, int j, int e) {
+      const int pos = last_pos(r), tok = r / A.G;
+      int rank = e < 0 ? -64 : kNone;
+      if (e >= 0 && pos >= 0 && e <= pos >> shift) {
+        const int page = (e << shift) / kP, w = page >> 5;
+        rank = 2 * (s_ahead[w] + __popc(s_bits[w] & ((1u << (page & 31)) - 1u))) + (shift == 3 ? e & 1 : 0);
+      }
+      A.ranks[((size_t)(it.row0 + tok) * A.Hq + it.kvh * A.G + (r - tok * A.G)) * A.rank_stride + j] = rank;
+    });
+    it.pages = carry;
+    weight = (long long)((carry + 7) / 8) * kSparseTileCost + kSparseItemCost;
+  }
+  if (tid == 0) {
+    A.items[u] = it;
+    A.before[u + 1] = weight;
+    __threadfence();
+    s_last = atomicAdd(A.arrived, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  sum_weights(A, s_sum);
+  if (tid == 0) *A.arrived = 0;      // as the next call finds it
+}
+
 }  // namespace
 
 int launch_sparse_items(const RowsAttnArgs& A, cudaStream_t stream) {
   const int smem = 2 * A.words * (int)sizeof(uint32_t);
   if (smem_limit_at_least(reinterpret_cast<const void*>(sparse_items_kernel), smem) != cudaSuccess) return SA_ERR_CUDA;
-  cudaError_t e = launch_pdl(sparse_items_kernel, dim3(A.n_items), dim3(kItemThreads), (size_t)smem, stream, A);
-  if (e == cudaSuccess) e = launch_pdl(sparse_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, A);
+  const cudaError_t e = launch_pdl(sparse_items_kernel, dim3(A.n_items), dim3(kItemThreads), (size_t)smem, stream, A);
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
