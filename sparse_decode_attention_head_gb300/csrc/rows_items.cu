@@ -69,33 +69,40 @@ __device__ void sum_weights(const RowsAttnArgs& A, long long* s_sum) {
   if (lane == 0 && real > 0) atomicAdd(A.ticket + 1, real);
 }
 
-// f(row, entry's index j, entry) for all places j < rank_stride of the lists of
-// an item's rows; entries behind a row's count are kNone.
+// f(row's token, row and head ahead of it from the item's first, entry's index
+// j, entry) for all places j < rank_stride of the lists of an item's rows;
+// entries behind a row's count are kNone.  No divisions: they were most of the
+// kernel's instructions.
 template <typename F>
 __device__ __forceinline__ void each_entry(const RowsAttnArgs& A, const SparseItem& it, F f) {
-  int per = 4;                                       // lanes a row: a power of two
-  while (per < A.rank_stride && per < 32) per *= 2;
-  const int tid = threadIdx.x, sub = tid % per, groups = kItemThreads / per, blocks = (A.rank_stride + per - 1) / per;
-  const int units = it.tokens * A.G * blocks;        // of `per` places of a row's list
-  for (int i0 = tid / per; i0 < units; i0 += groups * kAtOnce) {
-    int n[kAtOnce], e[kAtOnce], r[kAtOnce], j[kAtOnce];
+  int log = 2;                                       // of the lanes a row
+  while ((1 << log) < A.rank_stride && log < 5) ++log;
+  const int tid = threadIdx.x, sub = tid & ((1 << log) - 1), groups = kItemThreads >> log;
+  const int rows = it.tokens * A.G;
+  const unsigned by_g = 65536u / A.G + 1;            // r / G for r < 256, G <= 8
+  const size_t first = (size_t)it.row0 * A.Hq + it.kvh * A.G;
+  const int* counts = A.sel_cnt + first;
+  const int* lists = A.sel_idx + first * A.kcap;
+  for (int j = sub; j < A.rank_stride; j += 1 << log) {
+    for (int r0 = tid >> log; r0 < rows; r0 += groups * kAtOnce) {
+      int n[kAtOnce], e[kAtOnce];
+      unsigned tok[kAtOnce], at[kAtOnce];
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x) {
-      const int i = i0 + x * groups;
-      r[x] = i < units ? i / blocks : -1;
-      j[x] = i < units ? (i - r[x] * blocks) * per + sub : kNone;
-      n[x] = 0;
-      e[x] = 0;
-      if (r[x] >= 0) {
-        const int tok = r[x] / A.G;
-        const size_t row = (size_t)(it.row0 + tok) * A.Hq + it.kvh * A.G + (r[x] - tok * A.G);
-        n[x] = __ldg(A.sel_cnt + row);
-        if (j[x] < A.kcap) e[x] = __ldg(A.sel_idx + row * A.kcap + j[x]);
+      for (int x = 0; x < kAtOnce; ++x) {
+        const unsigned r = r0 + x * groups;
+        n[x] = 0;
+        e[x] = 0;
+        if (r < rows) {
+          tok[x] = r * by_g >> 16;
+          at[x] = tok[x] * (A.Hq - A.G) + r;         // tok * Hq + head
+          n[x] = __ldg(counts + at[x]);
+          if (j < A.kcap) e[x] = __ldg(lists + (size_t)at[x] * A.kcap + j);
+        }
       }
-    }
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x)
-      if (j[x] < A.rank_stride) f(r[x], j[x], j[x] < min(n[x], A.kcap) ? e[x] : kNone);
+      for (int x = 0; x < kAtOnce; ++x)
+        if (r0 + x * groups < rows) f((int)tok[x], first + at[x], j, j < min(n[x], A.kcap) ? e[x] : kNone);
+    }
   }
 }
 
@@ -129,8 +136,8 @@ __global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs
     };
     const int shift = A.bs_shift[it.kvh];
     // a row's last position that is there (rows behind the table see what lies in it); negative: it sees nothing
-    auto last_pos = [&](int r) {
-      const int pos = it.pos0 + r / A.G;
+    auto last_pos = [&](int tok) {
+      const int pos = it.pos0 + tok;
       return pos < 0 ? pos : min(pos, it.end - 1);
     };
     if (it.end > 0) {
@@ -139,8 +146,8 @@ __global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs
       const int first = max(it.pos0, 0);                    // the first row that sees anything
       const int window = first + 1 > A.W ? first + 1 - A.W : 0;
       for (int page = window / kP + tid; page < n_pages; page += kItemThreads) set(page >> 5, 1u << (page & 31));
-      each_entry(A, it, [&](int r, int, int e) {
-        const int pos = last_pos(r);
+      each_entry(A, it, [&](int tok, size_t, int, int e) {
+        const int pos = last_pos(tok);
         if (pos < 0 || e < 0 || e > pos >> shift) return;
         const int page = (e << shift) / kP, end = min(((e + 1) << shift) - 1, pos) / kP;   // in one word: aligned
         set(page >> 5, ((2u << (end - page)) - 1u) << (page & 31));
@@ -170,14 +177,14 @@ __global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs
     }
     // the lists again: the place of a block's first half page.  Entries below zero are ahead of all of them,
     // those behind the row or its count are behind, so that lists stay ascending.
-    each_entry(A, it, [&](int r, int j, int e) {
-      const int pos = last_pos(r), tok = r / A.G;
+    each_entry(A, it, [&](int tok, size_t row, int j, int e) {
+      const int pos = last_pos(tok);
       int rank = e < 0 ? -64 : kNone;
       if (e >= 0 && pos >= 0 && e <= pos >> shift) {
         const int page = (e << shift) / kP, w = page >> 5;
         rank = 2 * (s_ahead[w] + __popc(s_bits[w] & ((1u << (page & 31)) - 1u))) + (shift == 3 ? e & 1 : 0);
       }
-      A.ranks[((size_t)(it.row0 + tok) * A.Hq + it.kvh * A.G + (r - tok * A.G)) * A.rank_stride + j] = rank;
+      A.ranks[row * A.rank_stride + j] = rank;
     });
     it.pages = carry;
     weight = (long long)((carry + 7) / 8) * kSparseTileCost + kSparseItemCost;
