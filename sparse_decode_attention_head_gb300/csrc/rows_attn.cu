@@ -85,20 +85,26 @@ constexpr int kThreads = 384;
 // measured yet).
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "registers");
-// What work weighs: a KV token of an item with one query tile (bound by the
-// loads: measured 1.45 us a tile of them) and with two (1.6 us), and an item's
-// query load, first tile and epilogue (3.4 us).
-constexpr int kOneCost = 6, kTwoCost = 7, kItemCost = 2000;
-constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
-
-enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
-
 // What the kernel attends to, an instance each.
 enum Kind {
   kPlain,     // prompts and trees, each sequence over all of its cache
   kShared,    // the same, with the prefix of a group of sequences as an item of its own
   kSparse,    // causal rows over sinks, window and the blocks of their lists
 };
+// What work weighs: a KV token of an item with one query tile (bound by the
+// loads: measured 1.45 us a tile of them) and with two (1.6 us), and an item's
+// query load, first tile and epilogue (3.4 us).
+// With shared prefixes items with one query tile run beside others with two, which leave them more of the
+// memory's rate, and most items are a sequence's few own tokens (128 sequences behind 32K: 179 us at the others' costs).
+template <int KIND>
+constexpr int kOneCost = KIND == kShared ? 5 : 6;
+template <int KIND>
+constexpr int kItemCost = KIND == kShared ? 2400 : 2000;
+constexpr int kTwoCost = 7;
+constexpr float kLag = 8.f;              // log2 of the growth of a row maximum that makes a rescale
+
+enum { kDescValid = 1, kDescFirst = 2, kDescLast = 4, kDescDual = 8 };
+
 // A piece of a block's run: KV tiles [k0, k1) of one item.  The loading warp
 // walks the run and hands the pieces to the other roles through a ring.
 struct Piece {
@@ -283,16 +289,17 @@ __device__ __forceinline__ int tiles_of(int end) { return (end + kRows - 1) / kR
 // Weight of a KV head's first k items, in closed form: KV tokens seen, times
 // what a tile of them takes with one query tile or with two, and a fixed cost
 // each.  All items but a sequence's last have two query tiles.
+template <int KIND>
 __device__ __forceinline__ long long weight_before(const RowsAttnArgs& A, const Seq& s, int k) {
   if (k == 0) return 0;
   const int full = min(k, s.items - 1);
   const bool flat = A.tree != nullptr || s.to == kPrefix;     // all rows see about the same
   const long long before = max(flat ? s.L : s.a, 0);
   long long w = (before * full + (flat ? 0 : (long long)s.T * full * (full + 1) / 2)) * kTwoCost +
-                (long long)k * kItemCost;
+                (long long)k * kItemCost<KIND>;
   if (k == s.items) {
     const int tokens = s.n - full * s.T;
-    w += (before + (flat ? 0 : s.n)) * (tokens <= A.tpt ? kOneCost : kTwoCost);
+    w += (before + (flat ? 0 : s.n)) * (tokens <= A.tpt ? kOneCost<KIND> : kTwoCost);
   }
   return w;
 }
@@ -307,7 +314,7 @@ __device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* st
   s = Seq{};
   for (int b = lane; b < sequences<KIND>(A); b += 32) {
     const Seq x = load_seq<KIND>(A, b, status);
-    const long long m = weight_before(A, x, x.items) * A.Hk;
+    const long long m = weight_before<KIND>(A, x, x.items) * A.Hk;
     w += m;
     if (b < 32) {
       s = x;
@@ -317,6 +324,22 @@ __device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* st
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
   return w;
+}
+
+// The KV head, item and KV tile at weight `rem` of a sequence, all of whose heads weigh `mine`.
+template <int KIND, typename T>
+__device__ __forceinline__ void locate_in(const RowsAttnArgs& A, T rem, const Seq& s, T mine, int4& r) {
+  const T each = mine / (T)A.Hk;
+  r.y = (int)(rem / each);
+  rem -= each * r.y;
+  int lo = 0, hi = s.items;     // the item: weight_before(lo) <= rem < weight_before(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((T)weight_before<KIND>(A, s, mid) <= rem) lo = mid; else hi = mid;
+  }
+  const T w0 = (T)weight_before<KIND>(A, s, lo), w1 = (T)weight_before<KIND>(A, s, lo + 1);
+  r.z = lo;
+  r.w = (int)((unsigned long long)(rem - w0) * tiles_of(item_end(A, s, lo)) / (w1 - w0));
 }
 
 // One warp: the item and KV tile at weight w (the end: a sequence behind the last).
@@ -330,7 +353,7 @@ __device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine
       mine = 0;
       if (b < n_seq) {
         s = load_seq<KIND>(A, b, nullptr);
-        mine = (T)weight_before(A, s, s.items) * A.Hk;
+        mine = (T)weight_before<KIND>(A, s, s.items) * A.Hk;
       }
     }
     T upto = mine;
@@ -346,20 +369,7 @@ __device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine
     }
     const int src = __ffs(hit) - 1;
     int4 r = make_int4(b, 0, 0, 0);
-    if (lane == src) {
-      T rem = w - (before + upto - mine);
-      const T each = mine / (T)A.Hk;
-      r.y = (int)(rem / each);
-      rem -= each * r.y;
-      int lo = 0, hi = s.items;     // the item: weight_before(lo) <= rem < weight_before(hi)
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((T)weight_before(A, s, mid) <= rem) lo = mid; else hi = mid;
-      }
-      const T w0 = (T)weight_before(A, s, lo), w1 = (T)weight_before(A, s, lo + 1);
-      r.z = lo;
-      r.w = (int)((unsigned long long)(rem - w0) * tiles_of(item_end(A, s, lo)) / (w1 - w0));
-    }
+    if (lane == src) locate_in<KIND, T>(A, w - (before + upto - mine), s, mine, r);
     r.x = __shfl_sync(0xffffffffu, r.x, src);
     r.y = __shfl_sync(0xffffffffu, r.y, src);
     r.z = __shfl_sync(0xffffffffu, r.z, src);
@@ -419,6 +429,56 @@ __device__ __forceinline__ bool locate_small(const RowsAttnArgs& A, int run, int
   return true;
 }
 
+// Many sequences, by the whole block: the weight ahead of each goes to `ahead`
+// [sequences + 1] in shared memory, and warps 0 and 1 look up where the block's
+// run begins and ends.  (Warp by warp, 32 sequences a round of loads: 1000
+// sequences in groups of 50 took 183 us in place of 119.)
+constexpr int kMaxAhead = kSlots * kTileBytes / (int)sizeof(long long) - 1;
+template <int KIND>
+__device__ __forceinline__ int4 locate_many(const RowsAttnArgs& A, long long* ahead, long long* s_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = sequences<KIND>(A);
+  for (int v = tid; v < n; v += kThreads) {
+    const Seq s = load_seq<KIND>(A, v, blockIdx.x == 0 ? A.status : nullptr);
+    ahead[v] = weight_before<KIND>(A, s, s.items) * A.Hk;
+  }
+  __syncthreads();
+  const int each = (n + kThreads - 1) / kThreads, v0 = min(tid * each, n), v1 = min(v0 + each, n);
+  long long sum = 0;
+  for (int v = v0; v < v1; ++v) sum += ahead[v];
+  long long upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) s_sum[warp] = upto;
+  __syncthreads();
+  long long at = upto - sum;
+  for (int w = 0; w < warp; ++w) at += s_sum[w];
+  for (int v = v0; v < v1; ++v) {
+    const long long x = ahead[v];
+    ahead[v] = at;
+    at += x;
+  }
+  if (tid == kThreads - 1) ahead[n] = at;      // the last thread's share ends at n
+  __syncthreads();
+  int4 r = make_int4(n, 0, 0, 0);
+  if (warp < 2) {
+    const long long w = ahead[n] * (blockIdx.x + warp) / gridDim.x;
+    if (w < ahead[n]) {
+      int lo = 0, hi = n;                      // ahead[lo] <= w < ahead[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ahead[mid] <= w) lo = mid; else hi = mid;
+      }
+      const Seq s = load_seq<KIND>(A, lo, nullptr);
+      r.x = lo;
+      locate_in<KIND, long long>(A, w - ahead[lo], s, ahead[lo + 1] - ahead[lo], r);
+    }
+  }
+  return r;
+}
+
 // One thread walks a block's run, piece by piece.
 template <int KIND>
 struct Walk {
@@ -433,6 +493,28 @@ struct Walk {
     end = c->range[1];
     done = b >= sequences<KIND>(A);
     if (!done) s = load_seq<KIND>(A, b, nullptr);
+  }
+  // The next sequence with items, looked for by a whole warp, 32 at once: every
+  // other one may be the prefix of a sequence that leads no group.
+  __device__ __forceinline__ void next_shared() {
+    const int lane = threadIdx.x & 31;
+    for (++b; b < sequences<KIND>(A); b += 32) {
+      Seq x{};
+      if (b + lane < sequences<KIND>(A)) x = load_seq<KIND>(A, b + lane, nullptr);
+      const unsigned hit = __ballot_sync(0xffffffffu, x.items > 0);
+      if (hit == 0) continue;
+      const int src = __ffs(hit) - 1;
+      b += src;
+      s.row0 = __shfl_sync(0xffffffffu, x.row0, src);
+      s.n = __shfl_sync(0xffffffffu, x.n, src);
+      s.L = __shfl_sync(0xffffffffu, x.L, src);
+      s.a = __shfl_sync(0xffffffffu, x.a, src);
+      s.items = __shfl_sync(0xffffffffu, x.items, src);
+      s.to = __shfl_sync(0xffffffffu, x.to, src);
+      s.pt = __shfl_sync(0xffffffffu, x.pt, src);
+      return;
+    }
+    done = true;
   }
   __device__ bool next(Piece& p) {
     while (!done) {
@@ -458,10 +540,14 @@ struct Walk {
         i = 0;
         if (++kvh == A.Hk) {
           kvh = 0;
-          do {
-            if (++b >= sequences<KIND>(A)) { done = true; break; }
-            s = load_seq<KIND>(A, b, nullptr);
-          } while (s.items == 0);
+          if (KIND == kShared) {
+            next_shared();
+          } else {
+            do {
+              if (++b >= sequences<KIND>(A)) { done = true; break; }
+              s = load_seq<KIND>(A, b, nullptr);
+            } while (s.items == 0);
+          }
         }
       }
       if (some) return true;
@@ -850,6 +936,10 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       const int4 r = locate_item(A, __ldg(A.before + A.n_items) * (blockIdx.x + warp) / gridDim.x);
       if (lane == 0) c->range[warp] = r;
     }
+  } else if (KIND == kShared && sequences<KIND>(A) > 32 && sequences<KIND>(A) <= kMaxAhead) {
+    const int4 r = locate_many<KIND>(A, reinterpret_cast<long long*>(s_kv), reinterpret_cast<long long*>(c->ml));
+    if (warp < 2 && lane == 0) c->range[warp] = r;
+    fence_proxy_async_smem();      // copies come to where the weights were
   } else if (warp < 2) {   // where this block's run begins (warp 0) and ends (warp 1)
     Seq s;
     long long mine;

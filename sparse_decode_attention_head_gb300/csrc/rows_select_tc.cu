@@ -823,8 +823,9 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
       }
     }
     if (!ok) break;
-    const float k2 = __int_as_float(__ldg(A.norms + it.b * A.Hk + it.kvh));
-    t.E = (A.group ? 6.103515625e-5f : 3.0517578125e-5f) * norm * sqrtf(k2) * 1.001f + 1e-35f;
+    // squares below the smallest fp32 are lost: together less than (5e-22)^2
+    const float k_norm = sqrtf(__int_as_float(__ldg(A.norms + it.b * A.Hk + it.kvh))) + 5e-22f;
+    t.E = (A.group ? 6.103515625e-5f : 3.0517578125e-5f) * (norm + 5e-22f) * k_norm * 1.001f + 1e-35f;
     float2* list = reinterpret_cast<float2*>(smem) + tid;      // the operands are done with
     const int n = t.valid ? t.n : 0;
     if (memory) select_list<MINMAX, true>(A, t, Scores<true>{mine, scratch + tid, n}, keys, &c->warp[warp], list);

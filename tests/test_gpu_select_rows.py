@@ -229,6 +229,57 @@ def test_many_rows_with_infinities():
     _check(r, prob, summ)
 
 
+@pytest.mark.parametrize("size", [1.0, 1e-25, 1e-36])
+@pytest.mark.parametrize("group", [False, True])
+def test_many_rows_whose_products_cancel(size, group):
+    # large products that cancel: what is left, and with it the order, is the rounding of the canonical sums
+    r = _rows([96], [3000], 8, 2, seed=43)
+    prob = Z.problem(r, 16, 12, 4, 64, mode=sa.SUMMARY_MEAN, selection=sa.SELECT_GROUP if group else sa.SELECT_PER_HEAD)
+    summ = _summaries(prob, 13)
+    big = torch.randn(64, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") * 1000
+    r.q[:] = r.q.sign() * 0 + 1
+    r.q[:, :, 64:] = -1
+    summ[:] = 0.001 * summ
+    summ += torch.cat([big, big]).to(torch.bfloat16)
+    r.q[::3] += (0.01 * torch.randn(r.q[::3].shape, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")).to(torch.bfloat16)
+    r.q *= size
+    _check(r, prob, summ)
+
+
+def test_many_rows_at_once_and_captured():
+    rs = [_rows([300, 200], [4000, 900], 8, 2, seed=44), _rows([400], [6000], 28, 4, seed=45)]
+    probs = [Z.problem(rs[0], [16, 64], 20, 4, 64), Z.problem(rs[1], [64, 32, 16, 64], 9, 4, 128, mode=sa.SUMMARY_MEAN, selection=sa.SELECT_GROUP)]
+    summs = [_summaries(p, 14 + i) for i, p in enumerate(probs)]
+    want = [_check(r, p, s) for r, p, s in zip(rs, probs, summs)]
+    wss = [sa.Workspace(p, rows=True, max_rows=r.n_rows) for r, p in zip(rs, probs)]
+    got = [[torch.full_like(x, -7) for x in w] for w in want]
+    streams = [torch.cuda.Stream() for _ in rs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for r, p, s, ws, g, st in zip(rs, probs, summs, wss, got, streams):
+            with torch.cuda.stream(st):
+                sa.select_rows(p, r.q, s, r.lens, r.offsets, *g, ws)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for r, p, s, ws, g in zip(rs, probs, summs, wss, got):
+            sa.select_rows(p, r.q, s, r.lens, r.offsets, *g, ws)
+    for g in got:
+        for x in g:
+            x.fill_(-7)
+    for r in rs:
+        r.q.neg_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for r, p, s, ws, g in zip(rs, probs, summs, wss, got):
+        again = _check(r, p, s)
+        assert torch.equal(again[0], g[0]) and torch.equal(again[1], g[1])
+        assert ws.status() == sa.SA_OK
+
+
 def test_many_candidates():
     r = _rows([70, 64], [30000, 12000], 8, 2, seed=41)
     prob = Z.problem(r, [16, 32], 100, 4, 512)
