@@ -1015,28 +1015,42 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         ++steps_done;
         tc_fence_after();
         float v[128];
-        tmem_ld64_start<0>(tS, v);
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
-        tmem_ld64_finish<0>(v);
-        uint32_t see[4] = {0, 0, 0, 0};      // kSparse: a bit for each column
-        if constexpr (KIND == kSparse) {
-          if (bad != 0) {
-            const int* page = ring->page[(tiles + t) % kPageDepth];
+        if (KIND == kSparse && bad != 0) {
+          // halves of which a row sees some tokens, where its sinks end, its window begins and the row itself is: those
+          // tokens are taken out in TMEM, and the half counts as seen.  Few columns of a tile, by a short loop.
+          for (uint32_t x = bad & 255u; x != 0; x &= x - 1) mask &= ~(3u << (2 * (__ffs(x) - 1)));
+          mask &= bits16(16 * kt, ((min(lim, p.end) + 7) >> 3) - p.out, 16 * kt);      // a block reaches behind the row
+          const int s0 = (A.S >> 3) - 16 * kt, w0 = ((lim - A.W) >> 3) - p.out - 16 * kt, c0 = (lim >> 3) - p.out - 16 * kt;
+          uint32_t cut = 0;
+          if ((A.S & 7) != 0 && A.S < lim && (unsigned)s0 < 16u) cut |= 1u << s0;
+          if (lim > A.W && lim - A.W < p.end && ((lim - A.W) & 7) != 0 && (unsigned)w0 < 16u) cut |= 1u << w0;
+          cut &= ~mask;              // a selected block's are seen in full, up to the row
+          if (lim > 0 && lim <= p.end && (lim & 7) != 0 && (unsigned)c0 < 16u) cut |= 1u << c0;
+          for (uint32_t x = bad & 255u; x != 0; x &= x - 1) cut &= ~(3u << (2 * (__ffs(x) - 1)));
+          const int* page = ring->page[(tiles + t) % kPageDepth];
+#pragma unroll 1
+          for (uint32_t x = __reduce_or_sync(0xffffffffu, cut); x != 0; x &= x - 1) {
+            const int e = __ffs(x) - 1, t0 = page[e >> 1] * kP + 8 * (e & 1);
+            auto below = [t0](int y) { return (1u << min(max(y - t0, 0), 8)) - 1u; };   // of 8 tokens, those before y
+            uint32_t see = (mask >> e) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
+            see &= below(lim);
+            if (!((cut >> e) & 1u)) see = 0xffu;     // this row's half is whole, or not seen at all
+            uint32_t y[8];
+            tmem_ld8(tS + 8 * e, y);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int t0 = page[e >> 1] * kP + 8 * (e & 1);
-              auto below = [t0](int x) { return (1u << min(max(x - t0, 0), 8)) - 1u; };   // of 8 tokens, those before x
-              uint32_t x = (mask >> e) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
-              x &= t0 < 0 || ((bad >> (e >> 1)) & 1u) ? 0u : below(lim);
-              see[e >> 2] |= x << (8 * (e & 3));
-            }
-          } else {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) see[w] = ((((mask >> (4 * w)) & 15u) * 0x00204081u) & 0x01010101u) * 255u;
+            for (int j = 0; j < 8; ++j) y[j] = (see >> j) & 1u ? y[j] : 0xff800000u;
+            tmem_st8(tS + 8 * e, y);
           }
+          mask |= cut;
+          tmem_wait_st();
+        }
+        tmem_ld64_start<0>(tS, v);
+        tmem_ld64_finish<0>(v);
+        if constexpr (KIND == kSparse) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
-            if (!((see[j >> 5] >> (j & 31)) & 1u)) v[j] = -INFINITY;
+            if (!((mask >> (j >> 3)) & 1u)) v[j] = -INFINITY;
         } else if ((kt + 1) * kRows > edge || bad != 0) {
           // masked in TMEM, 32 columns at a time: once or twice an item, and
           // a long piece of straight code would cost its instruction fetches
@@ -1075,7 +1089,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         if constexpr (KIND == kSparse) {
 #pragma unroll
           for (int j = 64; j < 128; ++j)
-            if (!((see[j >> 5] >> (j & 31)) & 1u)) v[j] = -INFINITY;
+            if (!((mask >> (j >> 3)) & 1u)) v[j] = -INFINITY;
         }
 #pragma unroll
         for (int j = 64; j < 128; j += 8) {
