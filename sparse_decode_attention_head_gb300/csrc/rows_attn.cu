@@ -647,7 +647,8 @@ __device__ __forceinline__ int4 locate_item(const RowsAttnArgs& A, long long w) 
 
 // ---------------------------------------------------------------- what a row sees of selected blocks
 
-// Eight pages of an item's bitmap at a time, by a whole warp.
+// The pages of an item's bitmap, eight at a time, by a whole warp, which looks up
+// those of four tiles at once.
 template <int KIND>
 struct PageWalk {
   __device__ __forceinline__ PageWalk(const RowsAttnArgs&, const Piece&, int) {}
@@ -659,6 +660,7 @@ struct PageWalk<kSparse> {
   uint32_t mine;
   int upto, total;       // pages up to and with the lane's word, of all 32
   int given;             // of these
+  int batch, place;      // a page a lane; the next of them
   __device__ __forceinline__ void load() {
     const int w = base + (threadIdx.x & 31);
     mine = w < words ? __ldg(bits + w) : 0u;
@@ -668,7 +670,7 @@ struct PageWalk<kSparse> {
   }
   // ahead: pages to pass over
   __device__ __forceinline__ PageWalk(const RowsAttnArgs& A, const Piece& p, int ahead)
-      : bits(A.pages + (size_t)p.u * A.words), words((p.end + 32 * kP - 1) / (32 * kP)), base(0) {
+      : bits(A.pages + (size_t)p.u * A.words), words((p.end + 32 * kP - 1) / (32 * kP)), base(0), place(32) {
     load();
     while (ahead >= total && base + 32 < words) {
       ahead -= total;
@@ -677,41 +679,45 @@ struct PageWalk<kSparse> {
     }
     given = min(ahead, total);
   }
-  // Lane j < 8: the j-th of the next eight, -1 where there are no more.
-  __device__ __forceinline__ int next() {
+  __device__ __forceinline__ void refill() {
     const int lane = threadIdx.x & 31;
-    int page = -1, got = 0;
-    while (true) {
+    batch = -1;
+    for (int got = 0;;) {
       // the word with page `want`: behind all that hold fewer
       const int want = given + lane - got;
       int owner = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int n = __popc(__ballot_sync(0xffffffffu, upto <= given + j - got));
-        if (lane == j) owner = n;
-      }
-      owner = min(owner, 31);
+      for (int step = 16; step > 0; step >>= 1)
+        if (__shfl_sync(0xffffffffu, upto, owner + step - 1) <= want) owner += step;
       uint32_t x = __shfl_sync(0xffffffffu, mine, owner);
       int k = want - (__shfl_sync(0xffffffffu, upto, owner) - __popc(x));     // of the word's
-      if (lane >= got && lane < 8 && want < total) {
-        page = (base + owner) * 32;
+      if (lane >= got && want < total) {
+        batch = (base + owner) * 32;
 #pragma unroll
         for (int half = 16; half > 0; half >>= 1) {
           const int n = __popc(x & ((1u << half) - 1u));
           if (k >= n) {
             k -= n;
             x >>= half;
-            page += half;
+            batch += half;
           }
         }
       }
-      const int take = min(8 - got, total - given);
+      const int take = min(32 - got, total - given);
       got += take;
       given += take;
-      if (got == 8 || base + 32 >= words) return page;
+      if (got == 32 || base + 32 >= words) break;
       base += 32;
       load();
     }
+    place = 0;
+  }
+  // Lane j < 8: the j-th of the next eight, -1 where there are no more.
+  __device__ __forceinline__ int next() {
+    if (place == 32) refill();
+    const int page = __shfl_sync(0xffffffffu, batch, place + (threadIdx.x & 7));
+    place += 8;
+    return (threadIdx.x & 31) < 8 ? page : -1;
   }
 };
 
