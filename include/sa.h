@@ -533,7 +533,7 @@ int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, con
  * system prompt).  Groups are neighbouring sequences: group g has those from
  * group_offsets[g] to group_offsets[g + 1] - 1 (device int32 [n_groups + 1],
  * non-decreasing; offsets that decrease or pass B are cut and record
- * SA_ERR_INVALID_ARG).
+ * SA_ERR_INVALID_ARG; n_groups is at most B).
  *
  * sa_shared_prefixes finds what each group shares: the longest run of leading
  * table entries, all in the pool, that is the same for every sequence of the

@@ -22,7 +22,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8, kThreads = 256, kStretch = 4;   // entries a thread has in flight
+constexpr int kCluster = 8, kThreads = 256, kStretch = 8;   // entries a thread has in flight
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 shared_prefixes_kernel(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,

@@ -180,6 +180,7 @@ class Problem:
         self._bs = (ctypes.c_int32 * max(1, len(self.block_sizes)))(*self.block_sizes)
         self._k = (ctypes.c_int32 * max(1, len(self.k_per_head)))(*self.k_per_head)
         self._summary_shape = None
+        self._room = {}       # workspace bytes of the row calls that need some by their rows
         self._c = _Problem(B, Hq, Hk, D, page_size, max_pages_per_seq, num_pages, sink, window, mode,
                            ctypes.cast(self._bs, ctypes.POINTER(ctypes.c_int32)),
                            ctypes.cast(self._k, ctypes.POINTER(ctypes.c_int32)), kcap, self.scale, selection)
@@ -663,9 +664,13 @@ def shared_prefixes(prob: Problem, page_table, seq_lens, row_offsets, group_offs
                                     prefix_lens.data_ptr(), ws.buf.data_ptr(), stream), "sa_shared_prefixes")
 
 
-def _check_room(prob: Problem, ws: Workspace, n: int):
-    if n > ws.max_rows:
-        raise ValueError("the workspace must be made with max_rows, for as many rows")
+def _check_room(prob: Problem, ws: Workspace, size: str, n: int):
+    """The workspace is made for n rows, and has what `size` (a size function of
+    the library) says they need for this problem; asked when their number changes."""
+    if prob._room.get(size, (-1, 0))[0] != n:
+        prob._room[size] = (n, int(getattr(lib(), size)(prob.ref, n)))
+    if n > ws.max_rows or prob._room[size][1] > ws.buf.numel():
+        raise ValueError("the workspace must be made with max_rows, for as many rows of this problem")
 
 
 def shared_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row_offsets, members, prefix_lens, out,
@@ -679,7 +684,7 @@ def shared_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens, row
     if tree_mask is not None:
         args.append((tree_mask, torch.int64, (q.shape[0],), "tree_mask"))
     stream = _check_rows_args(prob, ws, args)
-    _check_room(prob, ws, q.shape[0])
+    _check_room(prob, ws, "sa_shared_workspace_size", q.shape[0])
     _check(lib().sa_shared_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                      page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(), _p(tree_mask),
                                      members.data_ptr(), prefix_lens.data_ptr(), out.data_ptr(), _p(lse),
@@ -695,7 +700,7 @@ def select_rows(prob: Problem, q, summaries, seq_lens, row_offsets, sel_idx, sel
         (q, torch.bfloat16, (n, prob.Hq, prob.D), "q"), (summaries, torch.bfloat16, prob.summary_shape(), "summaries"),
         (seq_lens, torch.int32, (prob.B,), "seq_lens"), (row_offsets, torch.int32, (prob.B + 1,), "row_offsets"),
         (sel_idx, torch.int32, (n, prob.Hq, prob.kcap), "sel_idx"), (sel_cnt, torch.int32, (n, prob.Hq), "sel_cnt")))
-    _check_room(prob, ws, n)
+    _check_room(prob, ws, "sa_sparse_workspace_size", n)
     _check(lib().sa_select_rows(prob.ref, n, q.data_ptr(), summaries.data_ptr(), seq_lens.data_ptr(),
                                 row_offsets.data_ptr(), sel_idx.data_ptr(), sel_cnt.data_ptr(), ws.buf.data_ptr(),
                                 stream), "sa_select_rows")
@@ -711,7 +716,7 @@ def sparse_row_attention(prob: Problem, q, k_pool, v_pool, page_table, seq_lens,
     args += [(sel_idx, torch.int32, (q.shape[0], prob.Hq, prob.kcap), "sel_idx"),
              (sel_cnt, torch.int32, (q.shape[0], prob.Hq), "sel_cnt")]
     stream = _check_rows_args(prob, ws, args)
-    _check_room(prob, ws, q.shape[0])
+    _check_room(prob, ws, "sa_sparse_workspace_size", q.shape[0])
     _check(lib().sa_sparse_row_attention(prob.ref, q.shape[0], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                          page_table.data_ptr(), seq_lens.data_ptr(), row_offsets.data_ptr(),
                                          sel_idx.data_ptr(), sel_cnt.data_ptr(), out.data_ptr(), _p(lse),
