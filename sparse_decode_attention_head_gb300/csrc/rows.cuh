@@ -87,12 +87,13 @@ struct RowsAttnArgs {
   const int* prefix_lens;           // [B] tokens of the group's prefix
   float* half;                      // [2][n_rows][Hq][kD] sums over the prefix and over a sequence's own tokens
   float2* half_ml;                  // [2][n_rows][Hq] (maximum, sum), base 2
+  bool join_own;                    // few own tokens are attended where the two are joined
   int n_rows, B, Hq, Hk, G, mpp, num_pages;
   int tpt;                          // tokens of a query tile: 128 / G
   float scale_log2;                 // scale log2(e)
-  // selected blocks only
-  const __nv_bfloat16* q;           // [n_rows][Hq][kD]
+  const __nv_bfloat16* q;           // [n_rows][Hq][kD]; these two also with selected blocks
   const __nv_bfloat16* k_pool;
+  // selected blocks only
   const int* sel_idx;               // [n_rows][Hq][kcap] blocks, ascending
   const int* sel_cnt;               // [n_rows][Hq]
   SparseItem* items;                // [n_items]

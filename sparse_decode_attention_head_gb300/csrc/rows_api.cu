@@ -432,6 +432,8 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
   c.A.tree = reinterpret_cast<const unsigned long long*>(tree_mask_or_null);
   c.A.members = members;
   c.A.prefix_lens = prefix_lens;
+  c.A.q = static_cast<const __nv_bfloat16*>(q);
+  c.A.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
   c.A.half = at<float>(ws, l.half);
   c.A.half_ml = at<float2>(ws, l.ml);
   return sa::launch_shared_attention(c.A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));

@@ -165,6 +165,63 @@ def test_large_batch():
     _check(Shared(groups, [1 if i % 9 else 0 for i in range(n)], [(i * 31) % 50 for i in range(n)], 8, 2, seed=12))
 
 
+def _many_few(Hq, Hk, seed, tree):
+    """More sequences than blocks, few rows and mostly few tokens of their own: those are attended where the parts are joined."""
+    B = -(-320 // Hk)
+    rng = np.random.RandomState(seed)
+    rows = [int(rng.choice((1, 1, 1, 2, 3, 4, 5, 0))) for _ in range(B)]
+    rows[7] = 12
+    own = [int(rng.randint(0, 190)) for _ in range(B)]
+    own[:8] = [0, 156, 157, 159, 160, 161, 15, 3]
+    groups, left = [], B
+    while left:
+        m = min(left, int(rng.randint(1, 40)))
+        groups.append((m, int(rng.randint(0, 14))))
+        left -= m
+    r = Shared(groups, rows, own, Hq, Hk, seed=seed)
+    assert r.n_rows <= 4 * B
+    return r, R.tree_words(rows, seed) if tree else None
+
+
+@pytest.mark.parametrize("Hq,Hk", [(2, 2), (4, 2), (6, 2), (8, 2), (10, 2), (12, 2), (14, 2), (16, 2)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_many_sequences_of_few_tokens(Hq, Hk, tree):
+    r, words = _many_few(Hq, Hk, Hq, tree)
+    _check(r, words)
+
+
+def test_many_sequences_unseen_values_and_bad_pages():
+    r, _ = _many_few(8, 2, 3, False)
+    plan = _plan(r)
+    two = [b for b in range(r.B) if r.rows[b] >= 2 and int(plan[1][b]) > 0 and int(r.lens[b]) - int(plan[1][b]) < 100]
+    b, c, d = two[0], two[1], two[2]
+    # the newest token is seen by the sequence's last row alone
+    L = int(r.lens[b])
+    r.v_pool[int(r.table[b, (L - 1) // P]), 0, (L - 1) % P, 9] = float("inf")
+    L = int(r.lens[c])
+    r.v_pool[int(r.table[c, (L - 1) // P]), 1, (L - 1) % P] = float("nan")
+    out, lse = _check(r, plan=plan)
+    assert bool(torch.isposinf(out[int(r.offsets[b + 1]) - 1, :4, 9]).all())
+    assert bool(torch.isnan(out[int(r.offsets[c + 1]) - 1, 4:]).all())
+    r.table[d, int(plan[1][d]) // P] = -1
+    _check(r, plan=plan, status=sa.SA_ERR_BAD_PAGE)
+
+
+def test_many_sequences_bits_and_replay():
+    r, _ = _many_few(28, 4, 5, False)
+    plan = _plan(r)
+    out, lse = _run(r, plan=plan)
+    ws = sa.Workspace(r.prob, rows=True, max_rows=r.n_rows)
+    o, x = torch.zeros_like(out), torch.zeros_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.shared_attention(r.prob, r.q, r.k_pool, r.v_pool, r.table, r.lens, r.offsets, *plan, o, ws, lse=x)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(x, lse)
+
+
 def test_prefix_by_hand():
     # less than what is shared, and none for some: the result is the same attention
     r = Shared([(4, 40), (3, 25)], [1] * 7, [9, 0, 100, 31, 16, 2, 5], 8, 2, seed=13)
