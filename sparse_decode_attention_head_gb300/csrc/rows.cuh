@@ -82,16 +82,22 @@ struct RowsAttnArgs {
   float2* part_ml;                  // [cta][2][2][128] (maximum, sum), base 2
   int4* desc;                       // [cta][2] what the partials are of
   int* status;
+  int n_rows, B, Hq, Hk, G, mpp, num_pages;
+  int tpt;                          // tokens of a query tile: 128 / G
+  float scale_log2;                 // scale log2(e)
+};
+// With shared prefixes or selected blocks.  (Apart: with these fields the kernel
+// of prompts keeps its arguments elsewhere and takes 1448 us in place of 1397 for
+// 16384 rows.)
+struct RowsMoreArgs : RowsAttnArgs {
   // shared prefixes only
   const int* members;               // [B] sequences of the group that b leads, 0 elsewhere
   const int* prefix_lens;           // [B] tokens of the group's prefix
   float* half;                      // [2][n_rows][Hq][kD] sums over the prefix and over a sequence's own tokens
   float2* half_ml;                  // [2][n_rows][Hq] (maximum, sum), base 2
   bool join_own;                    // few own tokens are attended where the two are joined
-  int n_rows, B, Hq, Hk, G, mpp, num_pages;
-  int tpt;                          // tokens of a query tile: 128 / G
-  float scale_log2;                 // scale log2(e)
-  const __nv_bfloat16* q;           // [n_rows][Hq][kD]; these two also with selected blocks
+  // these two in both
+  const __nv_bfloat16* q;           // [n_rows][Hq][kD]
   const __nv_bfloat16* k_pool;
   // selected blocks only
   const int* sel_idx;               // [n_rows][Hq][kcap] blocks, ascending
@@ -109,11 +115,11 @@ struct RowsAttnArgs {
 
 int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           int num_sms, cudaStream_t stream);
-int launch_shared_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+int launch_shared_attention(const RowsMoreArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, int num_sms, cudaStream_t stream);
 
-int launch_sparse_items(const RowsAttnArgs& A, cudaStream_t stream);
-int launch_sparse_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+int launch_sparse_items(const RowsMoreArgs& A, cudaStream_t stream);
+int launch_sparse_attention(const RowsMoreArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, int num_sms, cudaStream_t stream);
 int launch_shared_prefixes(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,
                            int n_groups, int min_tokens, int* members, int* prefix_lens, int B, int mpp, int num_pages,

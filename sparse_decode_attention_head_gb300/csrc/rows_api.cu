@@ -210,7 +210,7 @@ int make_tile_map(CUtensorMap* m, const void* pool, const Params& p) {
 // there is anything to do, `rest` whether a call's other arguments are there.
 struct AttnCall {
   Params p;
-  sa::RowsAttnArgs A;
+  sa::RowsMoreArgs A;
   CUtensorMap tmQ, tmK, tmV;
   int nsm;
   bool launch;
@@ -232,8 +232,8 @@ int attention_args(const sa_problem* prob, int32_t n_rows, const void* q, const 
   if (overlap(q, row_bytes, out, row_bytes)) return SA_ERR_INVALID_ARG;
   c->nsm = sa_host::num_sms_current();
   if (c->nsm <= 0) return SA_ERR_CUDA;
-  sa::RowsAttnArgs& A = c->A;
-  A = sa::RowsAttnArgs{};
+  sa::RowsMoreArgs& A = c->A;
+  A = sa::RowsMoreArgs{};
   A.tpt = 128 / p.G;
   if ((rc = make_q_map(&c->tmQ, q, n_rows, p, A.tpt, p.G)) != SA_OK) return rc;
   if ((rc = make_tile_map(&c->tmK, k_pool, p)) != SA_OK) return rc;
@@ -508,7 +508,7 @@ int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* 
   if (max_items(p, n_rows, 32) > kMaxItems || p.mpp > kMaxSparsePages) return SA_ERR_UNSUPPORTED;
   if (!c.launch) return SA_OK;
   const SparseLayout l = sparse_layout(p, n_rows);
-  sa::RowsAttnArgs& A = c.A;
+  sa::RowsMoreArgs& A = c.A;
   A.q = static_cast<const __nv_bfloat16*>(q);
   A.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
   A.sel_idx = sel_idx;

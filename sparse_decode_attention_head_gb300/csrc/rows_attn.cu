@@ -62,11 +62,23 @@
 // behind 30K others: 0.68 ms, 1.56 PFLOP/s, and 0.72 ms, 1.48 PFLOP/s.  With one
 // query tile the cache's bytes bound it: 32 drafted tokens for each of 8
 // sequences of 32K: 177 us, 6.1 TB/s.
+//
+// Two more instances of the kernel (Kind below).  With shared prefixes the rows of
+// a group's sequences are one item's over the prefix, which is so read once, and
+// each sequence's own tokens are items of their own; the two parts are joined
+// as 32-bit sums.  128 single tokens behind 32K, 32 / 8 heads: 174 us for 616 MB
+// (3.5 TB/s): prefix tiles of 256 rows are bound by the tensor core's chain, the
+// sequences' own by HBM, and an item's start and end cost 3.4 us.  With selected
+// blocks an item's tiles are the pages that some of its rows see, and each row
+// finds its own in them: 32768 rows, 16 blocks of 64 each and a window of 512,
+// 3.1 ms; a tile of 256 rows takes 1.85 us, of which the tensor core's chain alone
+// is 1.54, and the items see five times what a row does.
 // Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
 // interleave and both finish late); one barrier for all of a tile's weights
 // in place of one for each half (2 %); two threads a row (1.90 ms: 104
 // registers do not hold what they need, and they meet once a tile).
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 #include "tcgen.cuh"
@@ -91,6 +103,8 @@ enum Kind {
   kShared,    // the same, with the prefix of a group of sequences as an item of its own
   kSparse,    // causal rows over sinks, window and the blocks of their lists
 };
+template <int KIND>
+using Args = std::conditional_t<KIND == kPlain, RowsAttnArgs, RowsMoreArgs>;
 // What work weighs: a KV token of an item with one query tile (bound by the
 // loads: measured 1.45 us a tile of them) and with two (1.6 us), and an item's
 // query load, first tile and epilogue (3.4 us).
@@ -115,18 +129,26 @@ struct Piece {
   int end, edge;      // item_end, item_edge
   int a;              // tokens of the sequence ahead of its rows
   int first;          // the item's first row in the sequence
+  bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
+};
+struct MorePiece : Piece {
   int to;             // Part: where the result goes
   int u;              // kSparse: the item,
   int out;            // and how many halves of pages, ahead of its window's, are not in its list
   long long pt;       // entry of the page table with the item's position 0
-  bool dual;          // one query tile, KV tiles taken in turn by both softmax groups
 };
+template <int KIND>
+using PieceOf = std::conditional_t<KIND == kPlain, Piece, MorePiece>;
+// The entry of the page table with an item's position 0.
+__device__ __forceinline__ long long table_at(const RowsAttnArgs& A, const Piece& p) { return (long long)p.b * A.mpp; }
+__device__ __forceinline__ long long table_at(const RowsAttnArgs&, const MorePiece& p) { return p.pt; }
 
 constexpr int kPieces = 4;
 constexpr int kPieceReaders = 11;        // warps: softmax, matrix instructions, edge
 
+template <int KIND>
 struct alignas(16) Ctl {
-  Piece piece[kPieces];
+  PieceOf<KIND> piece[kPieces];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full, q_empty;
@@ -149,7 +171,7 @@ struct alignas(16) PageRing {
   int page[kPageDepth][8];
 };
 template <int KIND>
-constexpr size_t kSmemBytes = 1024 + (2 + kSlots) * kTileBytes + sizeof(Ctl) + (KIND == kSparse ? sizeof(PageRing) : 0);
+constexpr size_t kSmemBytes = 1024 + (2 + kSlots) * kTileBytes + sizeof(Ctl<KIND>) + (KIND == kSparse ? sizeof(PageRing) : 0);
 static_assert(kSmemBytes<kSparse> <= 227 * 1024, "shared memory");
 constexpr uint32_t kCut = 256;           // beside a tile's bad pages: some row's view begins or ends inside 8 tokens
 
@@ -162,7 +184,8 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // Waits with a limit of kWaitNs; a wait that runs out, here or elsewhere in the
 // block, ends the block's work.
 constexpr unsigned long long kWaitNs = 2000000000ull;
-[[nodiscard]] __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+template <typename C>
+[[nodiscard]] __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, C* c, int* status) {
   unsigned long long t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
@@ -191,7 +214,8 @@ __device__ __forceinline__ void wait_out(uint64_t* bar, uint32_t parity, int* st
 }
 
 // wait_bar by a whole warp: all lanes see the same answer.
-[[nodiscard]] __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* c, int* status) {
+template <typename C>
+[[nodiscard]] __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, C* c, int* status) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, c, status));
 }
 
@@ -238,7 +262,7 @@ struct Seq : RowSeq {
 // rows.  Each would take an item of the attention kernel, whose start and end
 // cost more than two tiles.
 constexpr int kJoinTokens = 160, kJoinRows = 4;
-__device__ __forceinline__ bool own_in_join(const RowsAttnArgs& A, const Seq& s) {
+__device__ __forceinline__ bool own_in_join(const RowsMoreArgs& A, const Seq& s) {
   return A.join_own && s.to == kOwn && s.n <= kJoinRows && s.L <= kJoinTokens;
 }
 
@@ -251,21 +275,23 @@ __device__ __forceinline__ int sequences(const RowsAttnArgs& A) {
   return KIND == kShared ? 2 * A.B : A.B;
 }
 template <int KIND>
-__device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int v, int* status) {
+__device__ __forceinline__ Seq load_seq(const Args<KIND>& A, int v, int* status) {
   const int b = KIND == kShared ? v >> 1 : v;
   Seq s;
   s.T = 2 * A.tpt;
   s.to = kAll;
   s.pt = (long long)b * A.mpp;
-  if (KIND == kShared && (v & 1) == 0) {
-    const RowSeq g = shared_rows(A.row_offsets, A.members, A.prefix_lens, A.B, b, A.n_rows, A.mpp);
-    static_cast<RowSeq&>(s) = g;
-    s.to = kPrefix;
-    s.items = (s.n + s.T - 1) / s.T;
-    return s;
+  if constexpr (KIND == kShared) {
+    if ((v & 1) == 0) {
+      static_cast<RowSeq&>(s) = shared_rows(A.row_offsets, A.members, A.prefix_lens, A.B, b, A.n_rows, A.mpp);
+      s.to = kPrefix;
+      s.items = (s.n + s.T - 1) / s.T;
+      return s;
+    }
   }
   static_cast<RowSeq&>(s) = row_seq(A.row_offsets, A.seq_lens, b, A.n_rows, A.mpp, status);
-  if (KIND == kShared) {
+  s.items = (s.n + s.T - 1) / s.T;
+  if constexpr (KIND == kShared) {
     const int x = shared_prefix(A.prefix_lens, b, s, A.mpp, status);
     if (x > 0) {
       s.to = kOwn;
@@ -273,15 +299,14 @@ __device__ __forceinline__ Seq load_seq(const RowsAttnArgs& A, int v, int* statu
       s.a -= x;
       s.L -= x;
     }
+    if (own_in_join(A, s)) s.items = 0;
   }
-  s.items = KIND == kShared && own_in_join(A, s) ? 0 : (s.n + s.T - 1) / s.T;
   if (A.tree != nullptr && s.n > kMaxTree) {
     if (status != nullptr) set_status(status, SA_ERR_CAPACITY);
     s.items = 0;
   }
   return s;
 }
-
 // The first position that no row of item i sees.
 __device__ __forceinline__ int item_end(const RowsAttnArgs& A, const Seq& s, int i) {
   if (A.tree != nullptr) return s.L;
@@ -315,7 +340,7 @@ __device__ __forceinline__ long long weight_before(const RowsAttnArgs& A, const 
 // One warp: the total weight of all items.  `s` and `mine` are the lane's own
 // sequence, of the first 32, and its weight.
 template <int KIND>
-__device__ __forceinline__ long long total_weight(const RowsAttnArgs& A, int* status, Seq& s, long long& mine) {
+__device__ __forceinline__ long long total_weight(const Args<KIND>& A, int* status, Seq& s, long long& mine) {
   const int lane = threadIdx.x & 31;
   long long w = 0;
   mine = 0;
@@ -352,7 +377,7 @@ __device__ __forceinline__ void locate_in(const RowsAttnArgs& A, T rem, const Se
 
 // One warp: the item and KV tile at weight w (the end: a sequence behind the last).
 template <int KIND, typename T>
-__device__ __forceinline__ int4 locate(const RowsAttnArgs& A, T w, Seq s, T mine) {
+__device__ __forceinline__ int4 locate(const Args<KIND>& A, T w, Seq s, T mine) {
   const int lane = threadIdx.x & 31, n_seq = sequences<KIND>(A);
   T before = 0;
   for (int b0 = 0; b0 < n_seq; b0 += 32) {
@@ -443,7 +468,7 @@ __device__ __forceinline__ bool locate_small(const RowsAttnArgs& A, int run, int
 // sequences in groups of 50 took 183 us in place of 119.)
 constexpr int kMaxAhead = kSlots * kTileBytes / (int)sizeof(long long) - 1;
 template <int KIND>
-__device__ __forceinline__ int4 locate_many(const RowsAttnArgs& A, long long* ahead, long long* s_sum) {
+__device__ __forceinline__ int4 locate_many(const Args<KIND>& A, long long* ahead, long long* s_sum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = sequences<KIND>(A);
   for (int v = tid; v < n; v += kThreads) {
     const Seq s = load_seq<KIND>(A, v, blockIdx.x == 0 ? A.status : nullptr);
@@ -490,12 +515,12 @@ __device__ __forceinline__ int4 locate_many(const RowsAttnArgs& A, long long* ah
 // One thread walks a block's run, piece by piece.
 template <int KIND>
 struct Walk {
-  const RowsAttnArgs& A;
+  const Args<KIND>& A;
   int b, kvh, i, kt;
   int4 end;
   bool done;
   Seq s;
-  __device__ Walk(const RowsAttnArgs& a, const Ctl* c) : A(a) {
+  __device__ Walk(const Args<KIND>& a, const Ctl<KIND>* c) : A(a) {
     const int4 r = c->range[0];
     b = r.x; kvh = r.y; i = r.z; kt = r.w;
     end = c->range[1];
@@ -524,7 +549,7 @@ struct Walk {
     }
     done = true;
   }
-  __device__ bool next(Piece& p) {
+  __device__ bool next(PieceOf<KIND>& p) {
     while (!done) {
       const bool at_end = b == end.x && kvh == end.y && i == end.z;
       p.b = b; p.kvh = kvh; p.i = i;
@@ -534,8 +559,10 @@ struct Walk {
       p.k0 = kt;
       p.k1 = at_end ? end.w : p.nt;
       p.a = s.a;
-      p.to = s.to;
-      p.pt = s.pt;
+      if constexpr (KIND != kPlain) {
+        p.to = s.to;
+        p.pt = s.pt;
+      }
       p.first = i * s.T;
       p.row0 = s.row0 + i * s.T;
       p.tokens = min(s.T, s.n - i * s.T);
@@ -569,17 +596,17 @@ struct Walk {
 // items under way at a time are neighbours, whose pages L2 holds.  Else each
 // block has its share of their weight, and cuts items.
 constexpr int kWholeItems = 8;       // a block, from which they are taken whole (5.7 a block: 426 us cut, 443 whole)
-__device__ __forceinline__ bool whole_items(const RowsAttnArgs& A) {
+__device__ __forceinline__ bool whole_items(const RowsMoreArgs& A) {
   return __ldg(A.ticket + 1) >= kWholeItems * (int)gridDim.x;
 }
 template <>
 struct Walk<kSparse> {
-  const RowsAttnArgs& A;
+  const RowsMoreArgs& A;
   int u, kt, ahead;
   int4 end;
   SparseItem it;
   bool whole;
-  __device__ Walk(const RowsAttnArgs& a, const Ctl* c) : A(a) {
+  __device__ Walk(const RowsMoreArgs& a, const Ctl<kSparse>* c) : A(a) {
     whole = whole_items(A);
     if (whole) {
       u = blockIdx.x;
@@ -605,7 +632,7 @@ struct Walk<kSparse> {
       it = SparseItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     }
   }
-  __device__ bool next(Piece& p) {
+  __device__ bool next(MorePiece& p) {
     while (u < end.x || (u == end.x && kt < end.y)) {
       const bool at_end = u == end.x;
       p.b = it.b; p.kvh = it.kvh; p.i = it.i;
@@ -639,7 +666,7 @@ struct Walk<kSparse> {
 };
 
 // One warp: the item and tile at weight w of all items (w = total: behind the last).
-__device__ __forceinline__ int4 locate_item(const RowsAttnArgs& A, long long w) {
+__device__ __forceinline__ int4 locate_item(const RowsMoreArgs& A, long long w) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = A.n_items;      // before[lo] <= w < before[hi]
   if (w >= __ldg(A.before + hi)) return make_int4(hi, 0, 0, 0);
@@ -677,7 +704,7 @@ struct PageWalk<kSparse> {
     given = 0;
   }
   // ahead: pages to pass over
-  __device__ __forceinline__ PageWalk(const RowsAttnArgs& A, const Piece& p, int ahead)
+  __device__ __forceinline__ PageWalk(const RowsMoreArgs& A, const MorePiece& p, int ahead)
       : bits(A.pages + (size_t)p.u * A.words), words((p.end + 32 * kP - 1) / (32 * kP)), base(0), place(32) {
     load();
     while (ahead >= total && base + 32 < words) {
@@ -792,7 +819,7 @@ struct SeenRow {
   int kvh, pos;
   float M;
 };
-__device__ __noinline__ float4 sums_of_row(const RowsAttnArgs& A, const Piece& p, SeenRow s) {
+__device__ __noinline__ float4 sums_of_row(const RowsMoreArgs& A, const MorePiece& p, SeenRow s) {
   const int lane = threadIdx.x & 31;
   const int shift = A.bs_shift[s.kvh];
   const int n = min(max(__ldg(A.sel_cnt + s.row), 0), A.kcap);
@@ -901,13 +928,13 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
-rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+rows_attention_kernel(Args<KIND> A, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;                                  // two tiles: [half of the dims][128 rows][64]
   uint8_t* s_kv = smem + 2 * kTileBytes;                // kSlots tiles: [16 groups of 8 tokens][half][8][64]
-  Ctl* c = reinterpret_cast<Ctl*>(s_kv + kSlots * kTileBytes);
+  auto* c = reinterpret_cast<Ctl<KIND>*>(s_kv + kSlots * kTileBytes);
   PageRing* ring = reinterpret_cast<PageRing*>(c + 1);  // kSparse
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -985,7 +1012,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
     bool ok = true;
     for (int piece = 0;; ++piece) {
       if (!(ok = wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status))) break;
-      const Piece& p = c->piece[piece % kPieces];
+      const PieceOf<KIND>& p = c->piece[piece % kPieces];
       const int k0 = p.k0, ntp = p.k1 - k0, edge = p.edge;
       const bool dual = p.dual;
       if (k0 < 0) break;
@@ -1030,7 +1057,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         tc_fence_after();
         float v[128];
         const uint32_t bad = *(volatile uint32_t*)&c->bad[(tiles + t) & 15];
-        if (KIND == kSparse && bad != 0) {
+        if constexpr (KIND == kSparse) if (bad != 0) {
           // halves of which a row sees some tokens, where its sinks end, its window begins and the row itself is: those
           // tokens are taken out in TMEM, and the half counts as seen.  Few columns of a tile, by a short loop.
           for (uint32_t x = bad & 255u; x != 0; x &= x - 1) mask &= ~(3u << (2 * (__ffs(x) - 1)));
@@ -1190,14 +1217,20 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         const float w0 = l == 0.f ? 0.f : two ? ex2(m - M) : 1.f, w1 = two && l1 != 0.f ? ex2(m1 - M) : 0.f;
         const float lt = l * w0 + (two ? l1 * w1 : 0.f);
         // a whole item's rows are done; those of a part of two wait for the other, as 32-bit sums
-        const bool final_out = whole && (KIND != kShared || p.to == kAll);
+        const long long row = (long long)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
+        bool final_out = whole;
+        float* half = nullptr;
+        float2* half_ml = nullptr;
+        if constexpr (KIND == kShared) {
+          final_out = whole && p.to == kAll;
+          const long long at = (p.to == kOwn ? (long long)A.n_rows * A.Hq : 0) + row;
+          half = A.half + at * kD;
+          half_ml = A.half_ml + at;
+        }
         const float inv = final_out ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
         const int which = p.k0 > 0 ? 0 : 1;
         const size_t slot = ((size_t)blockIdx.x * 2 + which) * 2 + h;
         float* part = A.part + slot * kRows * kD + 4 * r;     // [dims / 4][row][4]
-        const long long row = (long long)(p.row0 + tok) * A.Hq + p.kvh * A.G + g;
-        const size_t half_row = KIND == kShared ? (p.to == kOwn ? (size_t)A.n_rows * A.Hq : 0) + row : 0;
-        float* half = KIND == kShared ? A.half + half_row * kD : nullptr;
         // a row's result lies in one lane: four lanes exchange theirs, so that
         // a store covers 64 bytes of each of 8 rows and not 16 of 32
         long long rows4[4];
@@ -1247,7 +1280,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 if (rows4[j] >= 0)
-                  reinterpret_cast<uint4*>(A.half + (half_row - row + rows4[j]) * kD + 32 * q4 + 16 * e)[lane & 3] =
+                  reinterpret_cast<uint4*>(half + (rows4[j] - row) * kD + 32 * q4 + 16 * e)[lane & 3] =
                       make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
             }
           } else {
@@ -1278,11 +1311,12 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         } else if (poisoned) {
           __syncwarp();     // the row was stored by its neighbours too
           if (valid)
-            add_poison(A, EdgeRow{A.page_table + p.pt, word, max(p.edge, p.k0 * kRows), min(p.end, p.k1 * kRows), lim, p.a},
+            add_poison(A, EdgeRow{A.page_table + table_at(A, p), word, max(p.edge, p.k0 * kRows),
+                                  min(p.end, p.k1 * kRows), lim, p.a},
                        p.kvh, final_out ? A.out + row * kD : nullptr, whole ? half : part, whole ? 4 : 4 * kRows);
         }
         if (KIND == kShared && whole && !final_out) {
-          if (valid) A.half_ml[half_row] = make_float2(M, lt);
+          if (valid) *half_ml = make_float2(M, lt);
         } else if (whole) {
           if (valid && A.lse != nullptr) A.lse[row] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * 0.693147180559945309f;
         } else {
@@ -1452,7 +1486,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       bool ok = true;
       Walk<KIND> walk(A, c);
       for (int piece = 0;; ++piece) {
-        Piece p;
+        PieceOf<KIND> p;
         if (!walk.next(p)) p.k0 = p.k1 = -1;
         if (piece >= kPieces &&
             !(ok = wait_warp(&c->piece_empty[piece % kPieces], (piece / kPieces - 1) & 1, c, A.status)))
@@ -1473,7 +1507,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
         }
         ++pieces;
         // a lane a page of the tile; the next tile's pages are looked up while this one's are copied
-        const int* pt = A.page_table + p.pt;
+        const int* pt = A.page_table + table_at(A, p);
         PageWalk<KIND> pages(A, p, 8 * p.k0);
         bool next_there = false;
         uint32_t next_cut = 0;
@@ -1543,7 +1577,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
       uint32_t tile = 0, gone = 0;   // gone: a parity bit a slot
       bool ok = true;
       for (int piece = 0; wait_warp(&c->piece_full[piece % kPieces], (piece / kPieces) & 1, c, A.status); ++piece) {
-        const Piece p = c->piece[piece % kPieces];
+        const PieceOf<KIND> p = c->piece[piece % kPieces];
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->piece_empty[piece % kPieces]);
         if (p.k0 < 0) break;
@@ -1610,7 +1644,7 @@ rows_attention_kernel(RowsAttnArgs A, const __grid_constant__ CUtensorMap tmQ, c
 // at all of them, and no load waits for another's value after that.
 constexpr int kMergeWarps = 4, kMergeRows = 4 * kMergeWarps, kMergeBatch = 4;
 template <int KIND>
-__global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnArgs A) {
+__global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(Args<KIND> A) {
   __shared__ int s_last;
   __shared__ unsigned s_there[kRowsMaxCtas / 32 + 1];
   __shared__ float2 s_ml[kMergeWarps][kRowsMaxCtas][4];   // (maximum, sum) of piece i, then (weight, -)
@@ -1700,7 +1734,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnAr
   if (t_row >= A.tpt || tok >= s.n) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t row = (size_t)(s.row0 + tok) * A.Hq + (size_t)d.y * A.G + g;
-  if (KIND == kShared && s.to != kAll) {
+  if constexpr (KIND == kShared) if (s.to != kAll) {
     const size_t half_row = (s.to == kOwn ? (size_t)A.n_rows * A.Hq : 0) + row;
 #pragma unroll
     for (int x = 0; x < 4; ++x) reinterpret_cast<float4*>(A.half + half_row * kD)[8 * x + part] = o[x];
@@ -1717,7 +1751,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(RowsAttnAr
 constexpr int kJoinWarps = 8;
 // Joins the two parts of rows behind a shared prefix.  A block takes a packed
 // row, a warp each of its heads in turn; rows that had no prefix are done.
-__global__ void __launch_bounds__(kJoinWarps * 32) rows_join_kernel(RowsAttnArgs A) {
+__global__ void __launch_bounds__(kJoinWarps * 32) rows_join_kernel(RowsMoreArgs A) {
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1758,7 +1792,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) rows_join_kernel(RowsAttnArgs
 // then K and V at once (a warp a row and KV head, page after page: 91 us in
 // place of 72 for 8 x 8 beams).
 template <int G>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsAttnArgs A) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsMoreArgs A) {
   __shared__ __align__(16) float4 s_o[kJoinWarps][G][32];
   __shared__ float2 s_ml[kJoinWarps][G];
   __shared__ __align__(16) uint4 s_q[G][kD / 8];
@@ -1916,7 +1950,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsA
 }
 
 template <int KIND>
-int launch(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
+int launch(const Args<KIND>& A, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, int num_sms,
            cudaStream_t stream) {
   const int ctas = std::min(num_sms, kRowsMaxCtas);
   if (smem_limit_at_least(reinterpret_cast<const void*>(rows_attention_kernel<KIND>), (int)kSmemBytes<KIND>) != cudaSuccess)
@@ -1935,9 +1969,9 @@ int launch_rows_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const C
   return launch<kPlain>(A, tmQ, tmK, tmV, num_sms, stream);
 }
 
-int launch_shared_attention(const RowsAttnArgs& args, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+int launch_shared_attention(const RowsMoreArgs& args, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, int num_sms, cudaStream_t stream) {
-  RowsAttnArgs A = args;
+  RowsMoreArgs A = args;
   // few rows a sequence, and more sequences and KV heads than twice the blocks: a block would have items of one or two
   // tiles one behind the other (1000 single tokens in groups of 50: 120 us without, 78 with; four beams: 19.5 and 21.9)
   A.join_own = (long long)A.n_rows <= (long long)kJoinRows * A.B && (long long)A.B * A.Hk >= 2ll * num_sms &&
@@ -1948,7 +1982,7 @@ int launch_shared_attention(const RowsAttnArgs& args, const CUtensorMap& tmQ, co
   if (!A.join_own) {
     e = launch_pdl(rows_join_kernel, dim3(A.n_rows), dim3(kJoinWarps * 32), 0, stream, A);
   } else {
-    void (*const join[kMaxG])(RowsAttnArgs) = {rows_own_join_kernel<1>, rows_own_join_kernel<2>, rows_own_join_kernel<3>,
+    void (*const join[kMaxG])(RowsMoreArgs) = {rows_own_join_kernel<1>, rows_own_join_kernel<2>, rows_own_join_kernel<3>,
                                                rows_own_join_kernel<4>, rows_own_join_kernel<5>, rows_own_join_kernel<6>,
                                                rows_own_join_kernel<7>, rows_own_join_kernel<8>};
     e = launch_pdl(join[A.G - 1], dim3(A.n_rows * A.Hk), dim3(kJoinWarps * 32), 0, stream, A);
@@ -1956,7 +1990,7 @@ int launch_shared_attention(const RowsAttnArgs& args, const CUtensorMap& tmQ, co
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
-int launch_sparse_attention(const RowsAttnArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+int launch_sparse_attention(const RowsMoreArgs& A, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, int num_sms, cudaStream_t stream) {
   const int rc = launch_sparse_items(A, stream);
   return rc == SA_OK ? launch<kSparse>(A, tmQ, tmK, tmV, num_sms, stream) : rc;

@@ -24,7 +24,7 @@ constexpr int kItemThreads = 256, kAtOnce = 4, kScanEach = 4;
 constexpr int kNone = 0x7fffffff;
 
 // before[u + 1]: item u's weight becomes the sum up to and with it.  A whole block.
-__device__ void sum_weights(const RowsAttnArgs& A, long long* s_sum) {
+__device__ void sum_weights(const RowsMoreArgs& A, long long* s_sum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long carry = 0;
   int real = 0;
@@ -74,7 +74,7 @@ __device__ void sum_weights(const RowsAttnArgs& A, long long* s_sum) {
 // entries behind a row's count are kNone.  No divisions: they were most of the
 // kernel's instructions.
 template <typename F>
-__device__ __forceinline__ void each_entry(const RowsAttnArgs& A, const SparseItem& it, F f) {
+__device__ __forceinline__ void each_entry(const RowsMoreArgs& A, const SparseItem& it, F f) {
   int log = 2;                                       // of the lanes a row
   while ((1 << log) < A.rank_stride && log < 5) ++log;
   const int tid = threadIdx.x, sub = tid & ((1 << log) - 1), groups = kItemThreads >> log;
@@ -106,7 +106,7 @@ __device__ __forceinline__ void each_entry(const RowsAttnArgs& A, const SparseIt
   }
 }
 
-__global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs A) {
+__global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsMoreArgs A) {
   extern __shared__ uint32_t s_bits[];
   __shared__ ItemPlace s_place;
   __shared__ long long s_sum[kItemThreads / 32];
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kItemThreads) sparse_items_kernel(RowsAttnArgs
 
 }  // namespace
 
-int launch_sparse_items(const RowsAttnArgs& A, cudaStream_t stream) {
+int launch_sparse_items(const RowsMoreArgs& A, cudaStream_t stream) {
   const int smem = 2 * A.words * (int)sizeof(uint32_t);
   if (smem_limit_at_least(reinterpret_cast<const void*>(sparse_items_kernel), smem) != cudaSuccess) return SA_ERR_CUDA;
   const cudaError_t e = launch_pdl(sparse_items_kernel, dim3(A.n_items), dim3(kItemThreads), (size_t)smem, stream, A);
