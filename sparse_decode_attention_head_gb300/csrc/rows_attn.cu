@@ -71,7 +71,7 @@
 // sequences' own by HBM, and an item's start and end cost 3.4 us.  With selected
 // blocks an item's tiles are the pages that some of its rows see, and each row
 // finds its own in them: 32768 rows, 16 blocks of 64 each and a window of 512,
-// 3.1 ms; a tile of 256 rows takes 1.85 us, of which the tensor core's chain alone
+// 3.1 ms; a tile of 256 rows takes 1.9 us, of which the tensor core's chain alone
 // is 1.54, and the items see five times what a row does.
 // Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
 // interleave and both finish late); one barrier for all of a tile's weights
