@@ -1786,15 +1786,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) rows_join_kernel(RowsMoreArgs
 }
 
 // The same, and the own tokens of rows that have few (A.join_own).  A block takes
-// a KV head of a packed row, a warp a head of its group, and to attend them a
-// warp a page: K in pairs of lanes a token, V in four dims a lane, in 32 bits
+// a KV head of a packed row, a warp every fourth head of its group, and to attend
+// them a warp a page: K in pairs of lanes a token, V in four dims a lane, in 32 bits
 // throughout.  Bound by the latency of its reads: the row's sequence, the page,
 // then K and V at once (a warp a row and KV head, page after page: 91 us in
-// place of 72 for 8 x 8 beams).
+// place of 72 for 8 x 8 beams).  Four blocks of four warps an SM: rows of few
+// pages leave eight warps idle (1000 rows of 10..60 tokens: 79 us with eight, 69
+// with four; 2000 rows of 64 heads: 631 and 505; three blocks without the spills
+// of groups of five heads and more: 524).
+constexpr int kOwnWarps = 4;
 template <int G>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsMoreArgs A) {
-  __shared__ __align__(16) float4 s_o[kJoinWarps][G][32];
-  __shared__ float2 s_ml[kJoinWarps][G];
+__global__ void __launch_bounds__(kOwnWarps * 32, 4) rows_own_join_kernel(RowsMoreArgs A) {
+  __shared__ __align__(16) float4 s_o[kOwnWarps][G][32];
+  __shared__ float2 s_ml[kOwnWarps][G];
   __shared__ __align__(16) uint4 s_q[G][kD / 8];
   pdl_wait();
   pdl_trigger();
@@ -1815,18 +1819,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsM
   if (A.tree != nullptr && s.n > kMaxTree) return;
   const size_t own = (size_t)A.n_rows * A.Hq, r = (size_t)row * A.Hq + (size_t)kvh * G;
   const bool here = own_in_join(A, s);
-  float4 a{}, o{};           // of head `warp`: the prefix's part and the sequence's own
-  float2 ma{}, mb{};
-  if (warp < G) {
-    a = reinterpret_cast<const float4*>(A.half + (r + warp) * kD)[lane];
-    ma = A.half_ml[r + warp];
+  constexpr int kHeads = (G + kOwnWarps - 1) / kOwnWarps;
+  float4 a[kHeads], o[kHeads];           // of heads warp, warp + 4: the prefix's part and the sequence's own
+  float2 ma[kHeads], mb[kHeads];
+#pragma unroll
+  for (int x = 0; x < kHeads; ++x) {
+    const int g = warp + x * kOwnWarps;
+    if (g >= G) continue;
+    a[x] = reinterpret_cast<const float4*>(A.half + (r + g) * kD)[lane];
+    ma[x] = A.half_ml[r + g];
     if (!here) {
-      o = reinterpret_cast<const float4*>(A.half + (own + r + warp) * kD)[lane];
-      mb = A.half_ml[own + r + warp];
+      o[x] = reinterpret_cast<const float4*>(A.half + (own + r + g) * kD)[lane];
+      mb[x] = A.half_ml[own + r + g];
     }
   }
   if (here) {
-    for (int x = threadIdx.x; x < G * (kD / 8); x += kJoinWarps * 32)
+    for (int x = threadIdx.x; x < G * (kD / 8); x += kOwnWarps * 32)
       (&s_q[0][0])[x] = __ldg(reinterpret_cast<const uint4*>(A.q + r * kD) + x);
     const int lim = A.tree != nullptr ? s.a : s.a + row - s.row0 + 1;   // sees positions below, and the drafts of its word
     const unsigned long long word = A.tree != nullptr ? __ldg(A.tree + row) : 0ull;
@@ -1844,7 +1852,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsM
       l[g] = 0.f;
     }
     __syncthreads();
-    for (int page = warp; page * kP < s.L; page += kJoinWarps) {
+    for (int page = warp; page * kP < s.L; page += kOwnWarps) {
       const int phys = __ldg(A.page_table + s.pt + page);
       if (phys < 0 || phys >= A.num_pages) {
         if (lane == 0) set_status(A.status, SA_ERR_BAD_PAGE);
@@ -1920,33 +1928,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) rows_own_join_kernel(RowsM
       if (lane == 0) s_ml[warp][g] = make_float2(m[g], l[g]);
     }
     __syncthreads();
-    if (warp < G) {
-      mb = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) mb.x = fmaxf(mb.x, s_ml[w][warp].x);
+    for (int x = 0; x < kHeads; ++x) {
+      const int g = warp + x * kOwnWarps;
+      if (g >= G) continue;
+      o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      mb[x] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
-        const float2 x = s_ml[w][warp];
-        if (x.y == 0.f) continue;                // no page of it, or nothing seen
-        const float f = ex2(x.x - mb.x);
-        const float4 y = s_o[w][warp][lane];
-        mb.y = fmaf(x.y, f, mb.y);
-        o.x = fmaf(y.x, f, o.x);
-        o.y = fmaf(y.y, f, o.y);
-        o.z = fmaf(y.z, f, o.z);
-        o.w = fmaf(y.w, f, o.w);
+      for (int w = 0; w < kOwnWarps; ++w) mb[x].x = fmaxf(mb[x].x, s_ml[w][g].x);
+#pragma unroll
+      for (int w = 0; w < kOwnWarps; ++w) {
+        const float2 z = s_ml[w][g];
+        if (z.y == 0.f) continue;                // no page of it, or nothing seen
+        const float f = ex2(z.x - mb[x].x);
+        const float4 y = s_o[w][g][lane];
+        mb[x].y = fmaf(z.y, f, mb[x].y);
+        o[x].x = fmaf(y.x, f, o[x].x);
+        o[x].y = fmaf(y.y, f, o[x].y);
+        o[x].z = fmaf(y.z, f, o[x].z);
+        o[x].w = fmaf(y.w, f, o[x].w);
       }
     }
   }
-  if (warp >= G) return;
-  const float M = ma.y == 0.f ? mb.x : mb.y == 0.f ? ma.x : fmaxf(ma.x, mb.x);
-  const float wa = ma.y == 0.f ? 0.f : ex2(ma.x - M), wb = mb.y == 0.f ? 0.f : ex2(mb.x - M);
-  const float sum = wa * ma.y + wb * mb.y;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum, fa = wa * inv, fb = wb * inv;
-  reinterpret_cast<uint2*>(A.out + (r + warp) * kD)[lane] =
-      make_uint2(pack_bf16(fmaf(a.x, fa, o.x * fb), fmaf(a.y, fa, o.y * fb)),
-                 pack_bf16(fmaf(a.z, fa, o.z * fb), fmaf(a.w, fa, o.w * fb)));
-  if (lane == 0 && A.lse != nullptr) A.lse[r + warp] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.693147180559945309f;
+#pragma unroll
+  for (int x = 0; x < kHeads; ++x) {
+    const int g = warp + x * kOwnWarps;
+    if (g >= G) continue;
+    const float M = ma[x].y == 0.f ? mb[x].x : mb[x].y == 0.f ? ma[x].x : fmaxf(ma[x].x, mb[x].x);
+    const float wa = ma[x].y == 0.f ? 0.f : ex2(ma[x].x - M), wb = mb[x].y == 0.f ? 0.f : ex2(mb[x].x - M);
+    const float sum = wa * ma[x].y + wb * mb[x].y;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum, fa = wa * inv, fb = wb * inv;
+    reinterpret_cast<uint2*>(A.out + (r + g) * kD)[lane] =
+        make_uint2(pack_bf16(fmaf(a[x].x, fa, o[x].x * fb), fmaf(a[x].y, fa, o[x].y * fb)),
+                   pack_bf16(fmaf(a[x].z, fa, o[x].z * fb), fmaf(a[x].w, fa, o[x].w * fb)));
+    if (lane == 0 && A.lse != nullptr) A.lse[r + g] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.693147180559945309f;
+  }
 }
 
 template <int KIND>
@@ -1985,7 +2001,7 @@ int launch_shared_attention(const RowsMoreArgs& args, const CUtensorMap& tmQ, co
     void (*const join[kMaxG])(RowsMoreArgs) = {rows_own_join_kernel<1>, rows_own_join_kernel<2>, rows_own_join_kernel<3>,
                                                rows_own_join_kernel<4>, rows_own_join_kernel<5>, rows_own_join_kernel<6>,
                                                rows_own_join_kernel<7>, rows_own_join_kernel<8>};
-    e = launch_pdl(join[A.G - 1], dim3(A.n_rows * A.Hk), dim3(kJoinWarps * 32), 0, stream, A);
+    e = launch_pdl(join[A.G - 1], dim3(A.n_rows * A.Hk), dim3(kOwnWarps * 32), 0, stream, A);
   }
   return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }

@@ -111,6 +111,18 @@ def test_long():
     _check(r, prob, _summaries(prob, 7))
 
 
+def test_more_than_the_scratch_holds():
+    # the longest lists of candidates there may be: the scores of 32 items at a time
+    r = _rows([2, 2, 2, 2, 2, 2], [520000, 3000, 900, 100, 3000, 400000], 8, 8, seed=50, mpp=32768)
+    prob = Z.problem(r, 8, 17, 4, 64, mode=sa.SUMMARY_MEAN)
+    assert prob.block_slots() == 65536
+    g = torch.Generator(device="cuda").manual_seed(51)
+    summ = torch.empty(prob.summary_shape(), dtype=torch.bfloat16, device="cuda")
+    for b in range(6):
+        summ[b] = torch.randn(summ[b].shape, generator=g, device="cuda").to(torch.bfloat16)
+    _check(r, prob, summ)
+
+
 def test_close_scores():
     # scores that differ in the last bits: the order of their sums decides
     r = _rows([64], [4000], 8, 2, seed=8)

@@ -107,6 +107,21 @@ def test_many_sequences():
     _check(*_case(rows, [(i * 37) % 400 for i in range(150)], 8, 2, [16, 8], 4, 4, 64, seed=10))
 
 
+def test_many_items_taken_whole():
+    # more items than eight a block: each block takes the next, and none is cut
+    r, prob, idx, cnt = _case([1 + i % 3 for i in range(180)], [(i * 53) % 700 for i in range(180)], 8, 8, [16, 64, 8, 32] * 2, 5, 4, 64, seed=21)
+    out, lse = _check(r, prob, idx, cnt)
+    ws = sa.Workspace(prob, rows=True, max_rows=r.n_rows)
+    o, x = torch.zeros_like(out), torch.zeros_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.sparse_row_attention(prob, r.q, r.k_pool, r.v_pool, r.table, r.lens, r.offsets, idx, cnt, o, ws, lse=x)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(x, lse) and ws.status() == sa.SA_OK
+
+
 def test_rows_of_nobody_and_rows_that_see_nothing():
     _check(*_case([40, 5], [100, 3], 8, 2, 16, 3, 4, 64, seed=11, extra_rows=21, lead=6))
     r, prob, idx, cnt = _case([40, 5], [0, 3], 8, 2, 16, 3, 4, 64, seed=12)

@@ -56,6 +56,8 @@ def test_selection_limits(lib):  # noqa: F811
     assert _select(lib, _prob(k_per_head=[9] + [3] * 7)) == sa.SA_ERR_CAPACITY
     assert _select(lib, _prob(selection=sa.SELECT_GROUP, k_per_head=[1, 2, 1, 1, 1, 1, 1, 1])) == BAD
     assert _select(lib, _prob(), n=0, q=None, idx=None, cnt=None) == sa.SA_OK
+    assert _select(lib, _prob(B=1, max_pages_per_seq=65536, block_sizes=[16, 64]), n=0) == sa.SA_OK
+    assert _select(lib, _prob(B=1, max_pages_per_seq=65537, block_sizes=[16, 64]), n=0) == UNSUP      # 65537 block slots
 
 
 def test_binding_refuses_host_tensors():
