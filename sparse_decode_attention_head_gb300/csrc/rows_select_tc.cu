@@ -63,7 +63,8 @@ struct Warp {
 };
 struct Ctl {
   Warp warp[kThreads / 32];
-  uint64_t q_full, s_full[4], free[4], done;
+  uint64_t q_full, s_full[4], free[4], done, drain;
+  uint32_t loaded, q_loaded;      // tiles of summaries and of q asked for so far
   float norm[kRows];
   uint32_t tmem;
   ItemPlace place;
@@ -696,6 +697,8 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
       mbar_init(&c->free[i], 1);
     }
     mbar_init(&c->done, 1);
+    mbar_init(&c->drain, 1);
+    c->loaded = c->q_loaded = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&c->tmem, kCols);
@@ -757,6 +760,7 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
         auto load = [&](int i) {     // summaries behind the item's last come along; no row looks at them
           uint64_t* bar = &c->s_full[(tile + i) % kS];
           mbar_arrive_expect_tx(bar, kStageBytes);
+          c->loaded = tile + i + 1;
           for (int y = 0; y < kPieces; ++y)
             tma_load_3d(s_k + (tile + i) % kS * kStageBytes + y * kSummHalf, &tmS, (y & 1) * 64, MINMAX ? 1 - (y >> 1) : 0,
                         slot0 + i * kTile, bar);
@@ -764,6 +768,7 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
         if (tid == 0) {
           if (!A.group && w0 == 0) {
             mbar_arrive_expect_tx(&c->q_full, T * A.G * kD * 2);
+            c->q_loaded = q_phase + 1;
             for (int half = 0; half < 2; ++half)
               tma_load_3d(s_q + half * kHalfTile, &tmQ, half * 64, h0, it.row0, &c->q_full);
           }
@@ -834,6 +839,14 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+  }
+  if (!ok && tid == 0) {      // a wait gave up: what is in flight ends before the block does
+    constexpr uint32_t kS = kStages<MINMAX>;
+    for (uint32_t x = c->loaded - min(c->loaded, kS); x < c->loaded; ++x)
+      (void)mbar_wait_bounded(&c->s_full[x % kS], (x / kS) & 1, A.status);
+    if (c->q_loaded > 0) (void)mbar_wait_bounded(&c->q_full, (c->q_loaded - 1) & 1, A.status);
+    tc_commit(&c->drain);
+    (void)mbar_wait_bounded(&c->drain, 0, A.status);
   }
   tc_fence_before();
   __syncthreads();
