@@ -66,7 +66,7 @@
 // Two more instances of the kernel (Kind below).  With shared prefixes the rows of
 // a group's sequences are one item's over the prefix, which is so read once, and
 // each sequence's own tokens are items of their own; the two parts are joined
-// as 32-bit sums.  128 single tokens behind 32K, 32 / 8 heads: 174 us for 616 MB
+// as 32-bit sums.  128 single tokens behind 32K, 32 / 8 heads: 178 us for 616 MB
 // (3.5 TB/s): prefix tiles of 256 rows are bound by the tensor core's chain, the
 // sequences' own by HBM, and an item's start and end cost 3.4 us.  With selected
 // blocks an item's tiles are the pages that some of its rows see, and each row
@@ -109,7 +109,8 @@ using Args = std::conditional_t<KIND == kPlain, RowsAttnArgs, RowsMoreArgs>;
 // loads: measured 1.45 us a tile of them) and with two (1.6 us), and an item's
 // query load, first tile and epilogue (3.4 us).
 // With shared prefixes items with one query tile run beside others with two, which leave them more of the
-// memory's rate, and most items are a sequence's few own tokens (128 sequences behind 32K: 179 us at the others' costs).
+// memory's rate, and most items are a sequence's few own tokens (128 sequences behind 32K: 179 us at the others' costs,
+// 173 at these, both with all own tokens as items).
 template <int KIND>
 constexpr int kOneCost = KIND == kShared ? 5 : 6;
 template <int KIND>
