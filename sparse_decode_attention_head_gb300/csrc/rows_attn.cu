@@ -1062,7 +1062,7 @@ rows_attention_kernel(Args<KIND> A, const __grid_constant__ CUtensorMap tmQ, con
           // halves of which a row sees some tokens, where its sinks end, its window begins and the row itself is: those
           // tokens are taken out in TMEM, and the half counts as seen.  Few columns of a tile, by a short loop.
           for (uint32_t x = bad & 255u; x != 0; x &= x - 1) mask &= ~(3u << (2 * (__ffs(x) - 1)));
-          mask &= bits16(16 * kt, ((min(lim, p.end) + 7) >> 3) - p.out, 16 * kt);      // a block reaches behind the row
+          mask &= bits16(16 * kt, ((min(lim, p.end) + 7) >> 3) - p.out, 16 * kt);      // a block reaches behind row or table
           const int s0 = (A.S >> 3) - 16 * kt, w0 = ((lim - A.W) >> 3) - p.out - 16 * kt, c0 = (lim >> 3) - p.out - 16 * kt;
           uint32_t cut = 0;
           if ((A.S & 7) != 0 && A.S < lim && (unsigned)s0 < 16u) cut |= 1u << s0;
@@ -1519,9 +1519,11 @@ rows_attention_kernel(Args<KIND> A, const __grid_constant__ CUtensorMap tmQ, con
             int* place = ring->page[(tile + t) % kPageDepth];
             page = pages.next();
             if (lane < kRows / kP) place[lane] = page;
-            // views begin or end inside 8 tokens where the sinks do, and where rows' windows and the rows themselves are
+            // views begin or end inside 8 tokens where the sinks do, and where rows' windows and the rows themselves are;
+            // on an item's last page a block may go on behind it (rows behind a table that ends inside a block)
             const int t0 = page * kP, w0 = p.a + 1 - A.W, w1 = w0 + p.tokens - 1;
-            const bool in = ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) || t0 + kP > p.a;
+            const bool in = ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) ||
+                            t0 + kP > min(p.a, p.end - 1);
             next_cut = __any_sync(0xffffffffu, page >= 0 && in) ? kCut : 0;
             next_there = page >= 0;
           } else {
