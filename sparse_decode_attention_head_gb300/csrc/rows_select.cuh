@@ -7,10 +7,13 @@
 
 namespace sa {
 
-// Candidate blocks [j0, j1) of a row at position pos.  Every row with some has the same j0.
+// Candidate blocks [j0, j1) of a row at position pos, j0 <= j1.  Every row with
+// some has the same j0.  A row ahead of the cache (pos < 0) has none: its length
+// less a window near 2^31 would be no int32.  Nor has one whose sinks reach
+// behind the table.
 __device__ __forceinline__ void row_candidates(const SelectArgs& A, int pos, int size, int& j0, int& j1) {
-  candidate_range(pos + 1, A.S, A.W, size, j0, j1);
-  j1 = min(j1, (A.mpp * kP + size - 1) / size);
+  candidate_range(max(pos + 1, 0), A.S, A.W, size, j0, j1);
+  j1 = max(j0, min(j1, (A.mpp * kP + size - 1) / size));
 }
 
 // Candidates [j0, j1) of an item's rows together, the last of them at position
