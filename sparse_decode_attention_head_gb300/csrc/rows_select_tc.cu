@@ -20,9 +20,14 @@
 // the positive and negative part, a product of twice the length, half of it zeros.
 // Heads that select together: a row is a token, and what the product takes is
 // the sum of the group's queries (of their positive and of their negative
-// parts), as two bf16 that hold 2^-17 of it, one product behind the other:
-// twice the steps, so E = 2^-14 |sum over heads of |q|| max_j |k_j|, which has
-// room for the heads' canonical sums and the rounding of the operand.
+// parts), as two bf16 that hold 2^-17 of it, one product behind the other.  In
+// units of |Q| |K|, Q the sum over heads of |q| and K the largest of max_j |k_j|:
+//   means: 256 products and 16 sums, 272 * 2^-23 < 2^-14.9;
+//   min/max: with heads of both signs a dim has two products in each of the two,
+//   512 products and 32 sums, 544 * 2^-23 < 2^-13.9;
+//   the operand 2^-17 and its sums of eight 2^-21, the heads' canonical sums
+//   (18 roundings each, 7 between them) 2^-19.
+// Together below 2^-14.5 and 2^-13.7: E = 2^-14 |Q| |K| of means and 2^-13 of min/max.
 //
 // A block (four warps, two blocks an SM) takes an item: one KV head with 128
 // rows (tokens and heads; tokens, for heads that select together) of a sequence, a thread a row.  Scores stay in
@@ -830,7 +835,7 @@ select_rows_tc_kernel(SelectArgs A, const __grid_constant__ CUtensorMap tmQ, con
     if (!ok) break;
     // squares below the smallest fp32 are lost: together less than (5e-22)^2
     const float k_norm = sqrtf(__int_as_float(__ldg(A.norms + it.b * A.Hk + it.kvh))) + 5e-22f;
-    t.E = (A.group ? 6.103515625e-5f : 3.0517578125e-5f) * (norm + 5e-22f) * k_norm * 1.001f + 1e-35f;
+    t.E = (!A.group ? 0x1p-15f : MINMAX ? 0x1p-13f : 0x1p-14f) * (norm + 5e-22f) * k_norm * 1.001f + 1e-35f;
     float2* list = reinterpret_cast<float2*>(smem) + tid;      // the operands are done with
     const int n = t.valid ? t.n : 0;
     if (memory) select_list<MINMAX, true>(A, t, Scores<true>{mine, scratch + tid, n}, keys, &c->warp[warp], list);
