@@ -532,8 +532,9 @@ int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, con
  * by sa_plan_pages: beams, samples of one prompt, conversations behind one
  * system prompt).  Groups are neighbouring sequences: group g has those from
  * group_offsets[g] to group_offsets[g + 1] - 1 (device int32 [n_groups + 1],
- * non-decreasing; offsets that decrease or pass B are cut and record
- * SA_ERR_INVALID_ARG; n_groups is at most B).
+ * non-decreasing; offsets that decrease or pass B record SA_ERR_INVALID_ARG and
+ * are cut: a group begins where those before it have ended; n_groups is at most
+ * B).
  *
  * sa_shared_prefixes finds what each group shares: the longest run of leading
  * table entries, all in the pool, that is the same for every sequence of the

@@ -28,19 +28,31 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 shared_prefixes_kernel(const int* table, const int* seq_lens, const int* row_offsets, const int* group_offsets,
                        int n_groups, int min_tokens, int* members, int* prefix_lens, int B, int mpp, int num_pages,
                        int* status) {
-  __shared__ int s_first, s_with, s_pages, s_answer;
+  __shared__ int s_first, s_with, s_pages, s_answer, s_begin, s_end;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = (int)cluster.block_rank(), g = blockIdx.x / kCluster;
   pdl_wait();
   pdl_trigger();
-  int b0 = B, b1 = B;
+  if (tid == 0) {
+    s_first = INT_MAX;
+    s_with = 0;
+    s_pages = mpp;
+    s_begin = s_end = 0;
+  }
+  __syncthreads();
+  // A group begins where those before it have ended, whatever its offset says: a
+  // sequence has one group, and one cluster that writes its answer.
+  auto offset = [&](int i) { return min(max(__ldg(group_offsets + i), 0), B); };
   if (g < n_groups) {
-    const int o0 = __ldg(group_offsets + g), o1 = __ldg(group_offsets + g + 1);
-    b0 = min(max(o0, 0), B);
-    b1 = min(max(o1, b0), B);
-    if ((b0 != o0 || b1 != o1) && rank == 0 && tid == 0) set_status(status, SA_ERR_INVALID_ARG);
-  } else {   // the cluster behind the last group: sequences of none
-    const int lo = n_groups > 0 ? __ldg(group_offsets) : B, hi = n_groups > 0 ? __ldg(group_offsets + n_groups) : B;
+    for (int i = tid; i <= g + 1; i += kThreads) {
+      const int x = offset(i);
+      if (i <= g) atomicMax(&s_begin, x);
+      else s_end = x;
+    }
+  } else {   // the cluster behind the last group: sequences of none, before and behind all groups
+    for (int i = tid; i <= n_groups; i += kThreads) atomicMax(&s_end, offset(i));
+    __syncthreads();
+    const int lo = n_groups > 0 ? offset(0) : B, hi = n_groups > 0 ? s_end : B;
     for (int b = rank * kThreads + tid; b < B; b += kCluster * kThreads) {
       if (b >= lo && b < hi) continue;
       members[b] = 0;
@@ -48,12 +60,10 @@ shared_prefixes_kernel(const int* table, const int* seq_lens, const int* row_off
     }
     return;   // all of the cluster
   }
-  if (tid == 0) {
-    s_first = INT_MAX;
-    s_with = 0;
-    s_pages = mpp;
-  }
   __syncthreads();
+  const int b0 = s_begin, b1 = max(s_end, b0);
+  if (rank == 0 && tid == 0 && (b0 != __ldg(group_offsets + g) || b1 != __ldg(group_offsets + g + 1)))
+    set_status(status, SA_ERR_INVALID_ARG);
   // the first member with rows, how many have some, and the whole pages ahead of all their rows
   for (int b = b0 + tid; b < b1; b += kThreads) {
     const RowSeq s = row_seq(row_offsets, seq_lens, b, INT_MAX, mpp, rank == 0 ? status : nullptr);
