@@ -545,7 +545,8 @@ int sa_tree_attention(const sa_problem* prob, int32_t n_rows, const void* q, con
  *   members [B]: at the group's first sequence with rows, how many sequences
  *     the group has from there on; 0 elsewhere and where nothing is shared.
  * It reads the table alone, so one answer serves every layer of a step.
- * Device errors as for other packed rows. */
+ * Device errors of offsets and lengths as for other packed rows, of sequences of
+ * no group too; a page outside the pool ends a prefix and is no error here. */
 int sa_shared_prefixes(const sa_problem* prob, const int32_t* page_table, const int32_t* seq_lens,
                        const int32_t* row_offsets, const int32_t* group_offsets, int32_t n_groups, int32_t min_tokens,
                        int32_t* members, int32_t* prefix_lens, void* ws, void* stream);

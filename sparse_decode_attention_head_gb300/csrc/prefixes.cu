@@ -55,6 +55,11 @@ shared_prefixes_kernel(const int* table, const int* seq_lens, const int* row_off
     const int lo = n_groups > 0 ? offset(0) : B, hi = n_groups > 0 ? s_end : B;
     for (int b = rank * kThreads + tid; b < B; b += kCluster * kThreads) {
       if (b >= lo && b < hi) continue;
+      // its errors are recorded too, by plain comparisons: of row_seq with a constant number of rows and no other use,
+      // nvcc 13.0 makes a test that is always true (max(y, max(x, 0)) != y alone does it)
+      const int o0 = __ldg(row_offsets + b), o1 = __ldg(row_offsets + b + 1);
+      if (o0 < 0 || o1 < o0) set_status(status, SA_ERR_INVALID_ARG);
+      if (__ldg(seq_lens + b) > mpp * kP) set_status(status, SA_ERR_CAPACITY);
       members[b] = 0;
       prefix_lens[b] = 0;
     }
