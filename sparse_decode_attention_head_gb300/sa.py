@@ -666,10 +666,12 @@ def shared_prefixes(prob: Problem, page_table, seq_lens, row_offsets, group_offs
 
 def _check_room(prob: Problem, ws: Workspace, size: str, n: int):
     """The workspace is made for n rows, and has what `size` (a size function of
-    the library) says they need for this problem; asked when their number changes."""
-    if prob._room.get(size, (-1, 0))[0] != n:
-        prob._room[size] = (n, int(getattr(lib(), size)(prob.ref, n)))
-    if n > ws.max_rows or prob._room[size][1] > ws.buf.numel():
+    the library) says they need for this problem; asked when their number changes.
+    The note is read once: another thread may write its own."""
+    note = prob._room.get(size)
+    if note is None or note[0] != n:
+        note = prob._room[size] = (n, int(getattr(lib(), size)(prob.ref, n)))
+    if n > ws.max_rows or note[1] > ws.buf.numel():
         raise ValueError("the workspace must be made with max_rows, for as many rows of this problem")
 
 
