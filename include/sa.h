@@ -581,18 +581,20 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
  * of the cache with all rows in it serve every row.
  * sel_idx: [n_rows][Hq][kcap] int32, entries behind the count are left as they
  * were; sel_cnt: [n_rows][Hq] int32.  Rows of nobody are left as they were; a
- * row without a position (more rows than tokens) has count 0.
- * max_rows rows need a workspace of
- * sa_sparse_workspace_size; more than about 2^30 / Hk rows, or more
- * than 65536 block slots, give SA_ERR_UNSUPPORTED. */
+ * row without a position (more rows than tokens) has count 0.  Of offsets that
+ * decrease the rows of later sequences may be left as they were.
+ * max_rows rows need a workspace of sa_sparse_workspace_size.  More than 2^30
+ * items (a KV head with up to 32 / G of a sequence's rows: about 2^30 (32 / G) /
+ * Hk rows), or more than 65536 block slots, give SA_ERR_UNSUPPORTED. */
 int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const void* summaries,
                    const int32_t* seq_lens, const int32_t* row_offsets, int32_t* sel_idx, int32_t* sel_cnt, void* ws,
                    void* stream);
 
 /* Workspace bytes of sa_select_rows and sa_sparse_row_attention for up to
- * max_rows rows (0 if prob is invalid, its table or max_rows too large or
- * max_rows negative); enough for every call that sa_rows_workspace_size serves
- * too. */
+ * max_rows rows; enough for every call that sa_rows_workspace_size serves too.
+ * 0 if prob is invalid, max_rows negative or over the limit of rows, or the table
+ * too wide for both calls (more than 819200 columns).  With more than 65536 block
+ * slots, which sa_select_rows refuses, it serves sa_sparse_row_attention. */
 size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows);
 
 /* sa_sparse_decode for packed rows: the row at position p attends the sinks
@@ -604,7 +606,8 @@ size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows);
  * ignored; a count outside [0, kcap] is cut to it).  out (bf16) and lse as
  * sa_prompt_attention, rounded alike; a row that sees nothing gets out = 0,
  * lse = -inf; what a row does not see cannot change it.  Pages that several
- * neighbouring rows see are read once for all of them.
+ * neighbouring rows see are read once for all of them.  Offsets that decrease, and
+ * the limit of rows, as sa_select_rows.
  * A page table with more than 819200 columns gives SA_ERR_UNSUPPORTED. */
 int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
                             const void* v_pool, const int32_t* page_table, const int32_t* seq_lens,

@@ -442,6 +442,7 @@ int sa_shared_attention(const sa_problem* prob, int32_t n_rows, const void* q, c
 size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows) {
   Params p;
   if (make_params(prob, &p) != SA_OK || max_rows < 0 || max_items(p, max_rows, 32) > kMaxItems) return 0;
+  if (p.mpp > kMaxSparsePages) return 0;      // neither call takes it: that many pages are more slots than kSelectMaxSlots
   return std::max({sa_rows_workspace_size(prob), sparse_layout(p, max_rows).total,
                    p.slots <= kSelectMaxSlots ? select_layout(p, max_rows).total : 0});
 }
