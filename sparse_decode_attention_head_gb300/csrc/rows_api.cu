@@ -159,13 +159,13 @@ PageLayout page_layout(const Params& p) {
   return l;
 }
 
-// q [n_rows][Hq][D] as boxes of 64 dims x some heads x some tokens.
-int make_q_map(CUtensorMap* m, const void* q, int n_rows, const Params& p, int tokens, int heads) {
+// q [n_rows][Hq][D] as boxes of 64 dims x G heads x some tokens.
+int make_q_map(CUtensorMap* m, const void* q, int n_rows, const Params& p, int tokens) {
   auto fn = sa_host::encode_fn();
   if (fn == nullptr) return SA_ERR_CUDA;
   cuuint64_t dims[3] = {SA_HEAD_DIM, (cuuint64_t)p.Hq, (cuuint64_t)n_rows};
   cuuint64_t strides[2] = {SA_HEAD_DIM * 2, (cuuint64_t)p.Hq * SA_HEAD_DIM * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tokens};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -235,7 +235,7 @@ int attention_args(const sa_problem* prob, int32_t n_rows, const void* q, const 
   sa::RowsMoreArgs& A = c->A;
   A = sa::RowsMoreArgs{};
   A.tpt = 128 / p.G;
-  if ((rc = make_q_map(&c->tmQ, q, n_rows, p, A.tpt, p.G)) != SA_OK) return rc;
+  if ((rc = make_q_map(&c->tmQ, q, n_rows, p, A.tpt)) != SA_OK) return rc;
   if ((rc = make_tile_map(&c->tmK, k_pool, p)) != SA_OK) return rc;
   if ((rc = make_tile_map(&c->tmV, v_pool, p)) != SA_OK) return rc;
   const AttnLayout l = attn_layout();
@@ -491,8 +491,8 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   }
   const int T = A.group ? 128 : 128 / p.G;
   A.n_items = (int)(((long long)n_rows / T + std::min(p.B, n_rows)) * p.Hk);
-  CUtensorMap tmQ, tmS;
-  int e = make_q_map(&tmQ, q, n_rows, p, T, A.group ? 1 : p.G);
+  CUtensorMap tmQ{}, tmS;
+  int e = A.group ? SA_OK : make_q_map(&tmQ, q, n_rows, p, T);      // the sum of a group's queries is no copy of them
   if (e == SA_OK) e = make_summary_map(&tmS, summaries, p);
   return e == SA_OK ? sa::launch_select_tc(A, tmQ, tmS, std::min(nsm, sa::kRowsMaxCtas), as_stream(stream)) : e;
 }
