@@ -666,10 +666,12 @@ struct Walk<kSparse> {
   }
 };
 
-// One warp: the item and tile at weight w of all items (w = total: behind the last).
+// One warp: the item and tile at weight w of all items (w = total: behind the
+// last that there is; there is room for one more a sequence and KV head, and the
+// last block would walk over those).
 __device__ __forceinline__ int4 locate_item(const RowsMoreArgs& A, long long w) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = A.n_items;      // before[lo] <= w < before[hi]
+  int lo = 0, hi = __ldg(A.ticket + 1);      // before[lo] <= w < before[hi]
   if (w >= __ldg(A.before + hi)) return make_int4(hi, 0, 0, 0);
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + step * (lane + 1);
