@@ -525,7 +525,7 @@ int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* 
   A.rank_stride = l.rank_stride;
   A.kcap = p.kcap;
   A.S = std::min(p.S, 1 << 30);
-  A.W = std::min(p.W, 1 << 30);
+  A.W = p.W;      // of a row behind the table the window may begin in it however far that is
   for (int h = 0; h < p.Hk; ++h) A.bs_shift[h] = (unsigned char)(p.bs[h] == 8 ? 3 : p.bs[h] == 16 ? 4 : p.bs[h] == 32 ? 5 : 6);
   return sa::launch_sparse_attention(A, c.tmQ, c.tmK, c.tmV, c.nsm, as_stream(stream));
 }

@@ -1026,7 +1026,7 @@ rows_attention_kernel(Args<KIND> A, const __grid_constant__ CUtensorMap tmQ, con
       int lim = 0;
       unsigned long long word = 0;
       if (KIND == kSparse) {
-        lim = valid ? p.a + tok + 1 : 0;      // and of those what its mask has
+        lim = valid ? max(p.a + tok + 1, 0) : 0;      // and of those what its mask has
       } else if (valid) {
         if (A.tree != nullptr) {
           lim = p.a;
@@ -1077,7 +1077,7 @@ rows_attention_kernel(Args<KIND> A, const __grid_constant__ CUtensorMap tmQ, con
           for (uint32_t x = __reduce_or_sync(0xffffffffu, cut); x != 0; x &= x - 1) {
             const int e = __ffs(x) - 1, t0 = page[e >> 1] * kP + 8 * (e & 1);
             auto below = [t0](int y) { return (1u << min(max(y - t0, 0), 8)) - 1u; };   // of 8 tokens, those before y
-            uint32_t see = (mask >> e) & 1u ? 0xffu : below(A.S) | (~below(lim - A.W) & 0xffu);
+            uint32_t see = (mask >> e) & 1u ? 0xffu : below(A.S) | (~below(max(lim - A.W, 0)) & 0xffu);
             see &= below(lim);
             if (!((cut >> e) & 1u)) see = 0xffu;     // this row's half is whole, or not seen at all
             uint32_t y[8];
@@ -1523,7 +1523,7 @@ rows_attention_kernel(Args<KIND> A, const __grid_constant__ CUtensorMap tmQ, con
             if (lane < kRows / kP) place[lane] = page;
             // views begin or end inside 8 tokens where the sinks do, and where rows' windows and the rows themselves are;
             // on an item's last page a block may go on behind it (rows behind a table that ends inside a block)
-            const int t0 = page * kP, w0 = p.a + 1 - A.W, w1 = w0 + p.tokens - 1;
+            const int t0 = page * kP, w0 = max(p.a + 1, 0) - A.W, w1 = w0 + p.tokens - 1;
             const bool in = ((A.S & 7) != 0 && t0 == (A.S & ~(kP - 1))) || (t0 + kP > w0 && t0 <= w1) ||
                             t0 + kP > min(p.a, p.end - 1);
             next_cut = __any_sync(0xffffffffu, page >= 0 && in) ? kCut : 0;
