@@ -108,17 +108,23 @@ SparseLayout sparse_layout(const Params& p, int n_rows) {
 // The selection's scratch behind the norms.
 constexpr int kSelectMaxSlots = 1024 * 64;      // candidates that a block's top-k holds
 // Which form takes less, from what each measured (32 heads over 8): the tensor
-// cores' one a round of two items an SM, 15 us and 0.16 us a candidate block
-// (seven times that where lists are long: their k-th is looked for among all);
-// the canonical one 15 us and 1 us for 60000 scores.  8 x 64 rows of 8K, blocks
-// of 64: 29 us against 85; 8 x 8 rows of 32K, blocks of 16: 330 against 80.
+// cores' one a round of two items an SM, 15 us and 0.16 us a candidate block;
+// the canonical one 15 us and 1 us for 60000 scores.  At most 40 blocks kept:
+// 8 x 64 rows of 8K, blocks of 64: 32 us against 100; 8 x 8 rows of 32K, blocks
+// of 16: 330 us against 81.  Longer lists, whose k-th is looked for among all
+// candidates, took the tensor form 2.6 to 4.5 times what lists of 40 did; they
+// count seven times here, which leaves them to it in groups alone.  Per head: 41
+// of 256 blocks for 16384 rows 1384 us against 2755 here, 41 of 512 for 32768
+// 7865 against 7403, 100 of 2048 for 32768 26.1 ms against 20.9.
 // Both are bounded by the table's width, not by lengths, which the host does not see.
-bool select_by_tensor(const Params& p, int n_rows, bool at_most) {
+// ctas: blocks that run at a time; 0: for a workspace, whether any number of rows
+// up to n_rows takes the tensor form (a round is the least it needs).
+bool select_by_tensor(const Params& p, int n_rows, int ctas) {
   if (p.slots > sa::kTcMaxSlots || (long long)p.B * p.Hk * p.slots >= (1ll << 31)) return false;
   const int T = p.sel_mode == SA_SELECT_GROUP ? 128 : 128 / p.G;
   const int k = *std::max_element(p.k, p.k + p.Hq);
   const long long items = ((long long)n_rows / T + std::min(p.B, n_rows)) * p.Hk;
-  const long long rounds = at_most ? 1 : (items + 303) / 304;    // at_most: for any number of rows up to these
+  const long long rounds = ctas == 0 ? 1 : (items + ctas - 1) / ctas;
   const double tensor = rounds * (15.0 + 0.16 * p.slots) * (k > 40 ? 7.0 : 1.0);
   return tensor < 15.0 + (double)n_rows * p.Hq * p.slots / 60e3;
 }
@@ -133,7 +139,7 @@ SelectLayout select_layout(const Params& p, int n_rows) {
   l.scores = off;
   // a workspace for n_rows serves fewer too, in either form
   size_t scores = sa::score_rows_scratch(p.slots, max_items(p, n_rows, 32));
-  if (select_by_tensor(p, n_rows, true))
+  if (select_by_tensor(p, n_rows, 0))
     scores = std::max(scores, sa::select_tc_scratch(p.slots, max_items(p, n_rows, 128)));
   off = up(off + scores);
   l.total = off;
@@ -458,8 +464,9 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   if (n_rows == 0) return SA_OK;
   if (!q || !sel_idx || !sel_cnt) return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(summaries) || !aligned16(ws)) return SA_ERR_INVALID_ARG;
-  const int nsm = sa_host::num_sms_current();
+  int nsm = sa_host::num_sms_current();
   if (nsm <= 0) return SA_ERR_CUDA;
+  nsm = std::min(nsm, sa::kRowsMaxCtas);
   sa::SelectArgs A{};
   A.q = static_cast<const __nv_bfloat16*>(q);
   A.summaries = static_cast<const __nv_bfloat16*>(summaries);
@@ -485,7 +492,7 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   A.group = p.sel_mode == SA_SELECT_GROUP;
   std::copy(p.bs, p.bs + p.Hk, A.bs);
   std::copy(p.k, p.k + p.Hq, A.k);
-  if (!select_by_tensor(p, n_rows, false)) {
+  if (!select_by_tensor(p, n_rows, 2 * nsm)) {
     A.n_items = (int)max_items(p, n_rows, 32);
     return sa::launch_score_rows(A, p.slots, as_stream(stream));
   }
@@ -494,7 +501,7 @@ int sa_select_rows(const sa_problem* prob, int32_t n_rows, const void* q, const 
   CUtensorMap tmQ{}, tmS;
   int e = A.group ? SA_OK : make_q_map(&tmQ, q, n_rows, p, T);      // the sum of a group's queries is no copy of them
   if (e == SA_OK) e = make_summary_map(&tmS, summaries, p);
-  return e == SA_OK ? sa::launch_select_tc(A, tmQ, tmS, std::min(nsm, sa::kRowsMaxCtas), as_stream(stream)) : e;
+  return e == SA_OK ? sa::launch_select_tc(A, tmQ, tmS, nsm, as_stream(stream)) : e;
 }
 
 int sa_sparse_row_attention(const sa_problem* prob, int32_t n_rows, const void* q, const void* k_pool,
