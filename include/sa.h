@@ -604,7 +604,8 @@ size_t sa_sparse_workspace_size(const sa_problem* prob, int32_t max_rows);
  * them: blocks of the KV head's size, ascending (with entries out of order the
  * row's result is undefined; equal, negative and later ones than p's are
  * ignored; a count outside [0, kcap] is cut to it).  out (bf16) and lse as
- * sa_prompt_attention, rounded alike; a row that sees nothing gets out = 0,
+ * sa_prompt_attention, rounded alike (softmax weights to bf16, of which
+ * sa_sparse_decode keeps about 16 bits); a row that sees nothing gets out = 0,
  * lse = -inf; what a row does not see cannot change it.  Pages that several
  * neighbouring rows see are read once for all of them.  Offsets that decrease, and
  * the limit of rows, as sa_select_rows.

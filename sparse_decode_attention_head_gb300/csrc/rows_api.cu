@@ -112,7 +112,7 @@ constexpr int kSelectMaxSlots = 1024 * 64;      // candidates that a block's top
 // the canonical one 15 us and 1 us for 60000 scores.  At most 40 blocks kept:
 // 8 x 64 rows of 8K, blocks of 64: 32 us against 100; 8 x 8 rows of 32K, blocks
 // of 16: 330 us against 81.  Longer lists, whose k-th is looked for among all
-// candidates, took the tensor form 2.6 to 4.5 times what lists of 40 did; they
+// candidates, took the tensor form 1.4 to 4.6 times what lists of 40 did; they
 // count seven times here, which leaves them to it in groups alone.  Per head: 41
 // of 256 blocks for 16384 rows 1384 us against 2755 here, 41 of 512 for 32768
 // 7865 against 7403, 100 of 2048 for 32768 26.1 ms against 20.9.

@@ -62,6 +62,10 @@
 // behind 30K others: 0.68 ms, 1.56 PFLOP/s, and 0.72 ms, 1.48 PFLOP/s.  With one
 // query tile the cache's bytes bound it: 32 drafted tokens for each of 8
 // sequences of 32K: 177 us, 6.1 TB/s.
+// Slower for the 16384 rows: two issuing warps, one a group (1.94 ms: the groups'
+// instructions interleave and both finish late); one barrier for all of a tile's
+// weights in place of one for each half (2 %); two threads a row (1.90 ms: 104
+// registers do not hold what they need, and they meet once a tile).
 //
 // Two more instances of the kernel (Kind below).  With shared prefixes the rows of
 // a group's sequences are one item's over the prefix, which is so read once, and
@@ -73,10 +77,6 @@
 // finds its own in them: 32768 rows, 16 blocks of 64 each and a window of 512,
 // 3.1 ms; a tile of 256 rows takes 1.9 us, of which the tensor core's chain alone
 // is 1.54, and the items see five times what a row does.
-// Slower: two issuing warps, one a group (1.94 ms: the groups' instructions
-// interleave and both finish late); one barrier for all of a tile's weights
-// in place of one for each half (2 %); two threads a row (1.90 ms: 104
-// registers do not hold what they need, and they meet once a tile).
 #include <algorithm>
 #include <type_traits>
 
